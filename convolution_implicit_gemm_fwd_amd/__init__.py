@@ -7,7 +7,11 @@ include/convimg.h.  ``abi`` is the ctypes binding of that ABI (same names);
 memory and the current stream; ``conv2d_bwd_data_nhwc`` and
 ``conv2d_bwd_weight_nhwc`` do the same for the gradients with respect to the
 input (stride 1) and to the weights, and ``conv2d_nchw`` for NCHW / OIHW
-tensors with an fp32 or bf16 output.
+tensors with an fp32 or bf16 output.  The row operators (``rows``): layer
+norm over the channels and its gradient (``layer_norm_nhwc``,
+``layer_norm_bwd_nhwc``), MXFP4 rows (``mxfp4_quantize_nhwc``) and the 1x1
+convolution on them with its gradient (``mxfp4_linear_nhwc``,
+``mxfp4_linear_bwd_nhwc``).
 
 Importing the package loads nothing; the HIP library is loaded on first use
 and its absence is an error (there is no fallback path).
@@ -21,8 +25,11 @@ from .abi import (CONVIMG_BF16, CONVIMG_FP32, LibraryMissing, conv2d_bwd_data,
                   conv2d_fwd_nchw, conv2d_fwd_nchw_workspace, conv2d_fwd_num_tiles, conv2d_fwd_out_dim,
                   conv2d_fwd_plan, conv2d_fwd_status, conv2d_fwd_test_spin_limit, conv2d_release,
                   conv2d_strerror)
+from .rows import (Mxfp4Tensor, layer_norm_bwd_nhwc, layer_norm_mxfp4_nhwc, layer_norm_nhwc,
+                   mxfp4_dequantize_nhwc, mxfp4_linear_bwd_nhwc, mxfp4_linear_nhwc, mxfp4_quantize_nhwc)
 
-__all__ = ["abi", "conv2d_nhwc", "conv2d_bwd_data_nhwc", "conv2d_bwd_weight_nhwc",
+__all__ = ["abi", "layer_norm_nhwc", "layer_norm_bwd_nhwc", "layer_norm_mxfp4_nhwc", "Mxfp4Tensor",
+           "mxfp4_quantize_nhwc", "mxfp4_dequantize_nhwc", "mxfp4_linear_nhwc", "mxfp4_linear_bwd_nhwc", "conv2d_nhwc", "conv2d_bwd_data_nhwc", "conv2d_bwd_weight_nhwc",
            "conv2d_bwd_data", "conv2d_bwd_data_weights", "conv2d_bwd_weight",
            "conv2d_bwd_weight_workspace", "conv2d_fwd", "conv2d_fwd_autotune",
            "conv2d_fwd_autotune_clear", "conv2d_fwd_nchw", "conv2d_fwd_nchw_workspace", "conv2d_nchw",

@@ -13,6 +13,8 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libconvimg.
 
 CONVIMG_BF16 = 0
 CONVIMG_FP32 = 1
+CONVIMG_FP16 = 2       # row operators only
+CONVIMG_MXFP4 = 3      # row operators only
 
 CONVIMG_OK = 0
 CONVIMG_ERR_NULL = 1
@@ -27,6 +29,7 @@ CONVIMG_ERR_TIMEOUT = 9
 CONVIMG_ERR_UNSUPPORTED = 10
 CONVIMG_ERR_WORKSPACE = 11
 CONVIMG_ERR_SCRATCH = 12
+CONVIMG_ERR_ALIGN = 13
 
 CONVIMG_LOADER_TAP = 0
 CONVIMG_LOADER_VEC8 = 1
@@ -47,7 +50,9 @@ EXPORTS = ("conv2d_fwd", "conv2d_fwd_out_dim", "conv2d_fwd_plan", "conv2d_strerr
            "conv2d_release", "conv2d_bwd_data", "conv2d_bwd_data_weights", "conv2d_bwd_weight",
            "conv2d_bwd_weight_workspace", "conv2d_fwd_autotune", "conv2d_fwd_autotune_clear",
            "conv2d_fwd_nchw", "conv2d_fwd_nchw_workspace", "conv2d_fwd_test_spin_limit",
-           "conv2d_fwd_noalloc")
+           "conv2d_fwd_noalloc", "layer_norm_fwd", "layer_norm_fwd_mxfp4", "layer_norm_bwd",
+           "layer_norm_bwd_workspace", "mxfp4_bytes", "mxfp4_quantize", "mxfp4_dequantize",
+           "mxfp4_linear_fwd", "mxfp4_linear_workspace", "mxfp4_linear_bwd", "mxfp4_linear_bwd_workspace")
 
 
 class convimg_plan(ctypes.Structure):
@@ -119,6 +124,22 @@ def load(path: str = LIB_PATH):
     lib.conv2d_fwd_nchw.restype = i
     lib.conv2d_fwd_nchw_workspace.argtypes = [i] * 11 + [ctypes.POINTER(ctypes.c_size_t)]
     lib.conv2d_fwd_nchw_workspace.restype = i
+    ll, f, sz = ctypes.c_longlong, ctypes.c_float, ctypes.c_size_t
+    szp = ctypes.POINTER(sz)
+    for name, args in (
+            ("layer_norm_fwd", [vp, ll, vp, vp, ll, i, f, i, i, vp, vp, vp, vp]),
+            ("layer_norm_fwd_mxfp4", [vp, ll, vp, vp, ll, i, f, i, vp, vp, vp, vp, vp]),
+            ("layer_norm_bwd", [vp, ll, vp, ll, vp, vp, vp, ll, i, i, i, i, vp, vp, vp, vp, sz, vp]),
+            ("layer_norm_bwd_workspace", [ll, i, szp]),
+            ("mxfp4_bytes", [ll, i, szp, szp]),
+            ("mxfp4_quantize", [vp, ll, i, i, i, i, vp, vp, vp]),
+            ("mxfp4_dequantize", [vp, vp, i, i, i, vp, vp]),
+            ("mxfp4_linear_fwd", [vp, ll, vp, i, vp, vp, vp, i, i, i, i, vp, vp, sz, vp]),
+            ("mxfp4_linear_workspace", [i, i, i, i, szp]),
+            ("mxfp4_linear_bwd", [vp, ll, i, vp, ll, vp, ll, i, i, i, i, i, vp, vp, vp, vp, sz, vp]),
+            ("mxfp4_linear_bwd_workspace", [i, i, i, szp])):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = i
     _lib = lib
     return lib
 
@@ -232,3 +253,74 @@ def conv2d_fwd_test_spin_limit(iterations):
 
 def conv2d_release():
     load().conv2d_release()
+
+
+def layer_norm_fwd(x, ldx, gamma, beta, rows, cols, eps, x_dtype, y_dtype, y, mean, rstd, stream):
+    """Raw C call (device addresses as integers or None), returns a status."""
+    return load().layer_norm_fwd(x, ldx, gamma, beta, rows, cols, eps, x_dtype, y_dtype, y, mean, rstd,
+                                 stream)
+
+
+def layer_norm_fwd_mxfp4(x, ldx, gamma, beta, rows, cols, eps, x_dtype, codes, scales, mean, rstd, stream):
+    """Raw C call, returns a status."""
+    return load().layer_norm_fwd_mxfp4(x, ldx, gamma, beta, rows, cols, eps, x_dtype, codes, scales, mean,
+                                       rstd, stream)
+
+
+def layer_norm_bwd(dy, lddy, x, ldx, gamma, mean, rstd, rows, cols, dy_dtype, x_dtype, dx_dtype, dx, dgamma,
+                   dbeta, ws, ws_bytes, stream):
+    """Raw C call, returns a status."""
+    return load().layer_norm_bwd(dy, lddy, x, ldx, gamma, mean, rstd, rows, cols, dy_dtype, x_dtype,
+                                 dx_dtype, dx, dgamma, dbeta, ws, ws_bytes, stream)
+
+
+def layer_norm_bwd_workspace(rows, cols):
+    """Returns (status, workspace bytes of layer_norm_bwd)."""
+    b = ctypes.c_size_t(0)
+    rc = load().layer_norm_bwd_workspace(rows, cols, ctypes.byref(b))
+    return rc, b.value
+
+
+def mxfp4_bytes(rows, cols):
+    """Returns (status, bytes of the codes, bytes of the scales) of packed rows."""
+    c, s = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    rc = load().mxfp4_bytes(rows, cols, ctypes.byref(c), ctypes.byref(s))
+    return rc, c.value, s.value
+
+
+def mxfp4_quantize(x, ldx, rows, cols, dtype, transpose, codes, scales, stream):
+    """Raw C call, returns a status."""
+    return load().mxfp4_quantize(x, ldx, rows, cols, dtype, transpose, codes, scales, stream)
+
+
+def mxfp4_dequantize(codes, scales, rows, cols, dtype, out, stream):
+    """Raw C call, returns a status."""
+    return load().mxfp4_dequantize(codes, scales, rows, cols, dtype, out, stream)
+
+
+def mxfp4_linear_fwd(x, ldx, x_scales, x_dtype, w_codes, w_scales, bias, M, N, K, out_dtype, out, ws,
+                     ws_bytes, stream):
+    """Raw C call, returns a status."""
+    return load().mxfp4_linear_fwd(x, ldx, x_scales, x_dtype, w_codes, w_scales, bias, M, N, K, out_dtype,
+                                   out, ws, ws_bytes, stream)
+
+
+def mxfp4_linear_workspace(M, N, K, x_dtype):
+    """Returns (status, workspace bytes of mxfp4_linear_fwd)."""
+    b = ctypes.c_size_t(0)
+    rc = load().mxfp4_linear_workspace(M, N, K, x_dtype, ctypes.byref(b))
+    return rc, b.value
+
+
+def mxfp4_linear_bwd(dy, lddy, dy_dtype, x, ldx, w, ldw, dtype, M, N, K, dx_dtype, dx, dw, db, ws, ws_bytes,
+                     stream):
+    """Raw C call, returns a status."""
+    return load().mxfp4_linear_bwd(dy, lddy, dy_dtype, x, ldx, w, ldw, dtype, M, N, K, dx_dtype, dx, dw, db,
+                                   ws, ws_bytes, stream)
+
+
+def mxfp4_linear_bwd_workspace(M, N, K):
+    """Returns (status, workspace bytes of mxfp4_linear_bwd)."""
+    b = ctypes.c_size_t(0)
+    rc = load().mxfp4_linear_bwd_workspace(M, N, K, ctypes.byref(b))
+    return rc, b.value

@@ -2081,9 +2081,10 @@ const char *conv2d_strerror(int status)
     case CONVIMG_ERR_UNSUPPORTED:
         return "unsupported by the backward passes (data: stride 1, KH == KW, pad <= dilation*(KH-1); "
                "weights: bf16 storage)";
-    case CONVIMG_ERR_WORKSPACE: return "workspace smaller than conv2d_bwd_weight_workspace reports";
+    case CONVIMG_ERR_WORKSPACE: return "workspace smaller than its size query reports";
     case CONVIMG_ERR_SCRATCH:
         return "conv2d_fwd_noalloc: the plan needs more split-K semaphores than its fixed scratch holds";
+    case CONVIMG_ERR_ALIGN: return "a packed operand or workspace is below its alignment";
     default: return "unknown status";
     }
 }

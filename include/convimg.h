@@ -34,6 +34,9 @@ extern "C" {
 /* Storage type of x and w.  The output and the bias are always fp32. */
 #define CONVIMG_BF16 0   /* bf16 inputs, bf16 MFMA products, fp32 accumulation */
 #define CONVIMG_FP32 1   /* fp32 inputs, fp32 MFMA products, fp32 accumulation */
+/* Further types, taken by the row operators (layer norm, MXFP4) only. */
+#define CONVIMG_FP16 2   /* IEEE half */
+#define CONVIMG_MXFP4 3  /* packed 4-bit rows with a scale per 32 values (see mxfp4_quantize) */
 
 /* Status codes.  0 is success; every error is returned before any work is
  * queued, and then `out` is untouched, except CONVIMG_ERR_LAUNCH. */
@@ -51,6 +54,7 @@ extern "C" {
                                       stride, window and padding, conv2d_bwd_weight fp32 storage */
 #define CONVIMG_ERR_WORKSPACE 11   /* conv2d_bwd_weight: ws_bytes below what it needs */
 #define CONVIMG_ERR_SCRATCH 12     /* conv2d_fwd_noalloc: the plan needs more semaphores than its scratch holds */
+#define CONVIMG_ERR_ALIGN 13       /* row operators: a packed operand or workspace below its alignment */
 
 /* Loader variants used by the plan. */
 #define CONVIMG_LOADER_TAP    0  /* IC % 64 == 0: one 64-channel slice of one tap per K tile, 16-byte loads */
@@ -392,6 +396,124 @@ int conv2d_bwd_weight(const void *x, const void *dy, int N, int H, int W, int IC
  * the argument errors of conv2d_bwd_weight, CONVIMG_ERR_DEVICE. */
 int conv2d_bwd_weight_workspace(int N, int H, int W, int IC, int OC, int KH, int KW, int stride, int pad,
                                 int dilation, int dtype, size_t *bytes);
+
+/* ---- Row operators ------------------------------------------------------
+ *
+ * Layer normalisation over channels and a linear layer on 4-bit rows, for
+ * channels-last data: a row is one pixel of an NHWC map or one token, its
+ * `cols` columns are the channels.  A dense operand is `rows` rows whose
+ * first elements are ld >= cols elements apart (a view into a wider buffer
+ * is fine, at any element alignment); outputs are contiguous.  dtype
+ * arguments take CONVIMG_BF16, _FP32 and _FP16; gamma, beta, bias, the
+ * statistics and the parameters' gradients are fp32.  rows (M) may be 0.
+ *
+ * Everything is asynchronous on `stream`; nothing is allocated, so the calls
+ * can be captured in a graph; workspaces are caller-owned, 16-byte aligned and in
+ * use until the stream has run the call.  Results do not depend on timing: every
+ * sum is taken in a fixed order.
+ *
+ * Errors, all before any work is queued: CONVIMG_ERR_SHAPE (rows < 0,
+ * cols <= 0, ld < cols), _DTYPE, _RANGE (rows or columns of 2^31 or more,
+ * packed codes of 2 GiB or more), _NULL, _ALIGN, _WORKSPACE, _ALIAS (an
+ * output or the workspace overlaps any other buffer of the call).
+ * CONVIMG_ERR_LAUNCH if a launch fails. */
+
+/* Layer normalisation: y = (x - mean) * rstd * gamma + beta with mean and
+ * rstd = 1 / sqrt(var + eps) over each row's columns (var without
+ * correction).
+ *
+ *   gamma, beta  device, fp32 [cols], or NULL for ones / zeros
+ *   y            device, [rows][cols] in y_dtype (rounded once from fp32)
+ *   mean, rstd   device, fp32 [rows], kept for layer_norm_bwd; either may be
+ *                NULL */
+int layer_norm_fwd(const void *x, long long ldx, const float *gamma, const float *beta, long long rows, int cols,
+                   float eps, int x_dtype, int y_dtype, void *y, float *mean, float *rstd, hipStream_t stream);
+
+/* layer_norm_fwd whose result is written as MXFP4 rows (the layout of
+ * mxfp4_quantize, quantised from the fp32 result), the input form of
+ * mxfp4_linear_fwd. */
+int layer_norm_fwd_mxfp4(const void *x, long long ldx, const float *gamma, const float *beta, long long rows,
+                         int cols, float eps, int x_dtype, void *codes, void *scales, float *mean, float *rstd,
+                         hipStream_t stream);
+
+/* Gradient of layer_norm_fwd: with n = (x - mean) * rstd and h = dy * gamma,
+ *
+ *   dx     = rstd * (h - mean(h) - n * mean(h * n))    (means over a row)
+ *   dgamma = sum over rows of dy * n,   dbeta = sum over rows of dy
+ *
+ *   dy           device, dy_dtype, rows lddy apart
+ *   x, gamma     as in the forward call; mean, rstd: what it wrote
+ *   dx           device, [rows][cols] in dx_dtype
+ *   dgamma, dbeta  device, fp32 [cols], overwritten; NULL together to skip
+ *   ws           at least layer_norm_bwd_workspace bytes (none if skipped) */
+int layer_norm_bwd(const void *dy, long long lddy, const void *x, long long ldx, const float *gamma,
+                   const float *mean, const float *rstd, long long rows, int cols, int dy_dtype, int x_dtype,
+                   int dx_dtype, void *dx, float *dgamma, float *dbeta, void *ws, size_t ws_bytes,
+                   hipStream_t stream);
+int layer_norm_bwd_workspace(long long rows, int cols, size_t *bytes);
+
+/* MXFP4 rows.  A block is 32 consecutive values of a row (the last one
+ * filled with zeros).  With t its largest magnitude its scale byte is
+ * s = clamp(floor(log2 t) - 2 + 127, 0, 254) and its scale 2^(s - 127); a
+ * value is stored as the nearest of 0, .5, 1, 1.5, 2, 3, 4, 6 (codes 0 .. 7,
+ * plus 8 for the sign) to value / scale, ties to the even code, larger ones
+ * as 6.  A block that holds an infinity or a NaN gets the byte 255 and
+ * stands for NaN throughout.  Layout, with kp = cols rounded up to 32:
+ *
+ *   codes   [rows][kp / 2] bytes, the even column in the low four bits;
+ *           16-byte aligned
+ *   scales  [ceil(kp / 128)][rows][4] bytes: the bytes of four neighbouring
+ *           blocks of a row together, so that a tile of rows reads them as
+ *           one contiguous run; 0 for blocks past the last; 4-byte aligned
+ *
+ * mxfp4_bytes reports the two sizes. */
+int mxfp4_bytes(long long rows, int cols, size_t *codes, size_t *scales);
+
+/* Quantises x [rows][cols].  transpose != 0: quantises x's transpose, so that
+ * blocks run down the columns of x and the packed operand has cols rows of
+ * rows columns (then rows must not be 0). */
+int mxfp4_quantize(const void *x, long long ldx, int rows, int cols, int dtype, int transpose, void *codes,
+                   void *scales, hipStream_t stream);
+
+/* out [rows][cols] = the values that packed rows stand for. */
+int mxfp4_dequantize(const void *codes, const void *scales, int rows, int cols, int dtype, void *out,
+                     hipStream_t stream);
+
+/* Linear layer (a 1x1 convolution) on 4-bit rows:
+ *
+ *   out[m][n] = sum_k Q(x)[m][k] * w[n][k] + bias[n],   m < M, n < N, k < K
+ *
+ *   x         x_dtype CONVIMG_MXFP4: packed codes of M rows of K columns,
+ *             with x_scales (ldx is not read); else dense rows ldx apart, which the
+ *             call quantises (x_scales is not read)
+ *   w_codes, w_scales   packed weights, N rows of K columns
+ *   bias      device, fp32 [N], or NULL
+ *   out       device, [M][N] in out_dtype, rounded once from the fp32 sum
+ *   ws        at least mxfp4_linear_workspace bytes (0 for packed x)
+ */
+int mxfp4_linear_fwd(const void *x, long long ldx, const void *x_scales, int x_dtype, const void *w_codes,
+                     const void *w_scales, const float *bias, int M, int N, int K, int out_dtype, void *out, void *ws,
+                     size_t ws_bytes, hipStream_t stream);
+int mxfp4_linear_workspace(int M, int N, int K, int x_dtype, size_t *bytes);
+
+/* Gradient of the linear layer with both products on 4-bit operands, each
+ * quantised in blocks along the axis it is contracted over (the rounding
+ * itself is passed through unchanged, the straight-through estimate):
+ *
+ *   dx[m][k] = sum_n Q(dy)[m][n] * Q(w)[n][k]     blocks along n
+ *   dw[n][k] = sum_m Q(dy)[m][n] * Q(x)[m][k]     blocks along m
+ *   db[n]    = sum_m dy[m][n]                     from dy itself
+ *
+ *   dy   device, [M][N] in dy_dtype, rows lddy apart
+ *   x, w device, dense, in `dtype`: the forward input [M][K] and the weights
+ *        [N][K] before quantisation, rows ldx and ldw apart
+ *   dx   device, [M][K] in dx_dtype; dw: device, fp32 [N][K]; db: device,
+ *        fp32 [N], or NULL
+ *   ws   at least mxfp4_linear_bwd_workspace bytes */
+int mxfp4_linear_bwd(const void *dy, long long lddy, int dy_dtype, const void *x, long long ldx, const void *w,
+                     long long ldw, int dtype, int M, int N, int K, int dx_dtype, void *dx, float *dw, float *db,
+                     void *ws, size_t ws_bytes, hipStream_t stream);
+int mxfp4_linear_bwd_workspace(int M, int N, int K, size_t *bytes);
 
 /* Free every library-owned buffer (synchronising each device that has
  * one).  Later calls allocate again as needed.  Library plumbing with no
