@@ -15,14 +15,9 @@
 // scale byte per lane and operand: a lane of the 32x32x64 form holds 32
 // consecutive k of one row, which is one block, so blocks need no regrouping.
 // Sums are fp32.
-#include "row_common.hpp"
+#include "mxfp4_gemm.hpp"
 
 namespace convimg {
-
-typedef int i32x8_t __attribute__((ext_vector_type(8)));
-typedef float f32x16_t __attribute__((ext_vector_type(16)));
-
-constexpr int kMxThreads = 256;
 
 struct MxQuantArgs {
     const void *x;
@@ -118,65 +113,6 @@ __global__ __launch_bounds__(kMxThreads) void mx_dequantize_rows(const unsigned 
     }
 }
 
-struct MxGemmArgs {
-    const unsigned char *a, *b;     // codes: a [M][kb * 16], b [N][kb * 16]
-    const unsigned char *sa, *sb;   // scales: [quads][M or N][4]
-    const float *bias;              // [N] or NULL
-    void *out;                      // [M][N]
-    int M, N, kb;                   // kb: blocks of 32 along the contracted axis
-};
-
-// One 16-byte block of codes and its scale, zeros past the operand.
-__device__ __forceinline__ void mx_block(const unsigned char *codes, const unsigned char *scales, int rows, int row,
-                                         int kb, int blk, i32x8_t &v, int &s)
-{
-    v = i32x8_t{};
-    s = 0;
-    if (row < rows && blk < kb) {
-        const u32v4_t q = *(const u32v4_t *)(codes + ((long long)row * kb + blk) * 16);
-        v[0] = (int)q[0];
-        v[1] = (int)q[1];
-        v[2] = (int)q[2];
-        v[3] = (int)q[3];
-        s = scales[((long long)(blk >> 2) * rows + row) * 4 + (blk & 3)];
-    }
-}
-
-template <typename O>
-__device__ __forceinline__ void mx_store4(const MxGemmArgs &g, int m, int n, const float (&v)[4])
-{
-    if (m >= g.M)
-        return;
-    typename O::raw *o = (typename O::raw *)g.out + (long long)m * g.N + n;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (n + e < g.N)
-            store1<O>(o + e, v[e] + (g.bias ? g.bias[n + e] : 0.f));
-}
-
-// out = a b^T + bias, 64x64 a workgroup, a 32x32 block a wave, operands read
-// straight from memory.  b's rows are the matrix instruction's rows, so that
-// a lane holds four neighbouring columns of one output row.
-template <typename O>
-__global__ __launch_bounds__(kMxThreads) void mx_gemm_plain(MxGemmArgs g)
-{
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int m0 = blockIdx.x * 64 + (wave & 1) * 32, n0 = blockIdx.y * 64 + (wave >> 1) * 32;
-    f32x16_t acc = {};
-    for (int blk = lane >> 5; blk < ((g.kb + 1) & ~1); blk += 2) {
-        i32x8_t a, b;
-        int sa, sb;
-        mx_block(g.a, g.sa, g.M, m0 + (lane & 31), g.kb, blk, a, sa);
-        mx_block(g.b, g.sb, g.N, n0 + (lane & 31), g.kb, blk, b, sb);
-        acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, acc, 4, 4, 0, sb, 0, sa);
-    }
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const float v[4] = {acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
-        mx_store4<O>(g, m0 + (lane & 31), n0 + 8 * q + 4 * (lane >> 5), v);
-    }
-}
-
 // Column sums of x in two steps: every parts-th row into part[p][cols], then
 // the partial sums in a fixed order.
 template <typename T>
@@ -245,13 +181,28 @@ void quantize(const void *x, long long ldx, int rows, int cols, int dtype, bool 
     });
 }
 
+template <int BM, int BN, typename O>
+void gemm_tiles(MxGemmArgs g, hipStream_t stream)
+{
+    g.tm = (g.M + BM - 1) / BM;
+    g.tn = (g.N + BN - 1) / BN;
+    const unsigned grid = (unsigned)(((long long)g.tm * g.tn + 7) / 8 * 8);
+    hipLaunchKernelGGL((mx_gemm_tile<BM, BN, 4, O>), dim3(grid), dim3(kMxThreads), 0, stream, g);
+}
+
 void gemm(MxOperand a, MxOperand b, const float *bias, int M, int N, int K, int out_dtype, void *out,
           hipStream_t stream)
 {
-    const MxGemmArgs g = {a.codes, b.codes, a.scales, b.scales, bias, out, M, N, mx_blocks(K)};
+    const MxGemmArgs g = {a.codes, b.codes, a.scales, b.scales, bias, out, M, N, mx_blocks(K), 0, 0};
+    auto tiles = [&](long long t) { return ((M + t - 1) / t) * ((N + t - 1) / t); };
     with_dtype(out_dtype, [&](auto o) {
-        hipLaunchKernelGGL(mx_gemm_plain<decltype(o)>, dim3((M + 63) / 64, (N + 63) / 64), dim3(kMxThreads), 0,
-                           stream, g);
+        typedef decltype(o) O;
+        if (tiles(256) >= 192)
+            gemm_tiles<256, 256, O>(g, stream);
+        else if (tiles(128) >= 192)
+            gemm_tiles<128, 128, O>(g, stream);
+        else
+            gemm_tiles<64, 64, O>(g, stream);
     });
 }
 

@@ -1,0 +1,305 @@
+// mxfp4_gemm.hpp -- products of MXFP4 rows: out = a b^T + bias for a [M][K],
+// b [N][K] in 32-value blocks along K (the layout of mxfp4_quantize).
+//
+// v_mfma_scale_f32_32x32x64_f8f6f4 takes from each lane 32 consecutive k of
+// one row, which is one block, with its scale byte picked out of a dword; so
+// a dword of four scale bytes serves 128 k, and the lanes of the upper half
+// shift theirs down by one byte once.  b's rows are the instruction's rows,
+// so that a lane ends with four neighbouring columns of one output row.
+#pragma once
+
+#include "row_common.hpp"
+
+namespace convimg {
+
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
+constexpr int kMxThreads = 256;
+constexpr unsigned kMxOutOfRange = 0x80000000u;   // buffer offset past every packed operand
+constexpr int kMxRsrcWord3 = 0x00020000;          // raw buffer, 32-bit data format
+
+struct MxGemmArgs {
+    const unsigned char *a, *b;     // codes: a [M][kb * 16], b [N][kb * 16]
+    const unsigned char *sa, *sb;   // scales: [quads][M or N][4]
+    const float *bias;              // [N] or NULL
+    void *out;                      // [M][N]
+    int M, N, kb;                   // kb: blocks of 32 along the contracted axis
+    int tm, tn;                     // tiles along M and N
+};
+
+// s_waitcnt vmcnt(N) alone (gfx9 encoding; 7 and 15 leave the other counters
+// unconstrained).
+template <int N>
+__device__ __forceinline__ void mx_wait_vm()
+{
+    static_assert(N >= 0 && N < 64, "vmcnt is 6 bits");
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+
+__device__ __forceinline__ void mx_wait_lds() { __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4)); }
+
+__device__ __forceinline__ void mx_barrier()
+{
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);   // no compiler motion of LDS accesses across
+    __builtin_amdgcn_s_barrier();
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+
+__device__ __forceinline__ void mx_dma16(__amdgpu_buffer_rsrc_t r, unsigned char *lds, unsigned off)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)lds, 16, off, 0, 0, 0);
+}
+
+__device__ __forceinline__ void mx_dma4(__amdgpu_buffer_rsrc_t r, unsigned char *lds, unsigned off)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)lds, 4, off, 0, 0, 0);
+}
+
+template <int SEL>
+__device__ __forceinline__ f32x16_t mx_mfma32(i32x4_t b, i32x4_t a, f32x16_t c, int sb, int sa)
+{
+    const i32x8_t b8 = {b[0], b[1], b[2], b[3], 0, 0, 0, 0}, a8 = {a[0], a[1], a[2], a[3], 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b8, a8, c, 4, 4, SEL, sb, SEL, sa);
+}
+
+// Tile of workgroup `bid`.  Workgroups go to the 8 XCDs in turn; each XCD
+// takes one run of tiles (so that its L2 serves neighbours), ordered in
+// groups of 8 tile rows so that the tiles in flight are near square.
+__device__ __forceinline__ bool mx_tile(const MxGemmArgs &g, int &m, int &n)
+{
+    const int per = gridDim.x / 8;
+    const int id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if (id >= g.tm * g.tn)
+        return false;
+    const int span = 8 * g.tn, group = id / span, in = id - group * span;
+    const int rows = min(g.tm - group * 8, 8);
+    n = in / rows;
+    m = group * 8 + in - n * rows;
+    return true;
+}
+
+// BM x BN tiles, four waves 2 x 2, K tiles of 128 (four blocks a row).
+template <int BM, int BN, int STAGES, typename O>
+__global__ __launch_bounds__(kMxThreads) void mx_gemm_tile(MxGemmArgs g)
+{
+    constexpr int FM = BM / 64, FN = BN / 64;               // 32 x 32 blocks of a wave
+    constexpr int ROWS = BM + BN;
+    constexpr int CODES = ROWS * 64, STAGE = CODES + ROWS * 4;
+    constexpr int CP = ROWS / 64;                           // code copies a wave and stage: 64 rows a pass
+    constexpr int SP = ROWS >= 256 ? ROWS / 256 : 1;        // scale copies: 64 rows a wave
+    constexpr int PER = CP + SP;
+    constexpr int OS = sizeof(typename O::raw);
+    constexpr int PITCH = FN * 32 * OS + 16;                // epilogue: 32 rows a wave
+    constexpr int SMEM = STAGES * STAGE > 4 * 32 * PITCH ? STAGES * STAGE : 4 * 32 * PITCH;
+    static_assert((STAGES & (STAGES - 1)) == 0 && (STAGES - 2) * PER < 64, "ring of stages");
+    __shared__ __attribute__((aligned(16))) unsigned char smem[SMEM];
+
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave & 1, wn = wave >> 1;
+    const int half = lane >> 5, l32 = lane & 31;
+    int tm, tn;
+    if (!mx_tile(g, tm, tn))
+        return;
+    const int m0 = tm * BM, n0 = tn * BN;
+    const int quads = (g.kb + 3) / 4;
+
+    const unsigned ca = (unsigned)g.M * g.kb * 16u, cb = (unsigned)g.N * g.kb * 16u;
+    const unsigned na = (unsigned)g.M * quads * 4u, nb = (unsigned)g.N * quads * 4u;
+    const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void *)g.a, 0, ca, kMxRsrcWord3);
+    const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc((void *)g.b, 0, cb, kMxRsrcWord3);
+
+    // Copies of codes: pass p, this lane: tile row p * 64 + wave * 16 +
+    // lane / 4, physical 16-byte chunk lane % 4 of its 64 bytes.  Chunk c of
+    // row r lies at c ^ (r / 4 % 4): 16 rows' equal chunks then cover all
+    // banks.
+    const int chunk = (lane & 3) ^ ((lane >> 4) & 3);
+    unsigned coff[CP];
+#pragma unroll
+    for (int p = 0; p < CP; ++p) {
+        const int r = p * 64 + wave * 16 + (lane >> 2);
+        const bool isa = p * 64 < BM;
+        const int row = isa ? m0 + r : n0 + r - BM;
+        coff[p] = row < (isa ? g.M : g.N) ? (unsigned)row * (unsigned)g.kb * 16u + chunk * 16 : kMxOutOfRange;
+    }
+    // Copies of scales: 64 rows a wave instruction.
+    __amdgpu_buffer_rsrc_t rs[SP];
+    unsigned soff[SP], sstep[SP];
+    int sgroup[SP];
+#pragma unroll
+    for (int p = 0; p < SP; ++p) {
+        sgroup[p] = (p * 4 + wave) % (ROWS / 64);
+        const bool isa = sgroup[p] * 64 < BM;
+        const int row = isa ? m0 + sgroup[p] * 64 + lane : n0 + sgroup[p] * 64 - BM + lane;
+        const int rows = isa ? g.M : g.N;
+        rs[p] = __builtin_amdgcn_make_buffer_rsrc((void *)(isa ? g.sa : g.sb), 0, isa ? na : nb, kMxRsrcWord3);
+        soff[p] = row < rows ? (unsigned)row * 4u : kMxOutOfRange;
+        sstep[p] = (unsigned)rows * 4u;
+    }
+    // Copy c of K tile t into its stage.  Past the last block everything
+    // reads as zeros, tiles past the last one included, so every stage counts
+    // PER copies.
+    auto issue1 = [&](int t, int c) {
+        unsigned char *s = smem + (t & (STAGES - 1)) * STAGE;
+        if (c < CP)
+            mx_dma16(c * 64 < BM ? ra : rb, s + c * 4096 + wave * 1024,
+                     t * 4 + chunk < g.kb ? coff[c] + t * 64u : kMxOutOfRange);
+        else
+            mx_dma4(rs[c - CP], s + CODES + sgroup[c - CP] * 256, soff[c - CP] + t * sstep[c - CP]);
+    };
+
+    // The sums start from the bias.
+    f32x16_t acc[FM][FN];
+    {
+        const __amdgpu_buffer_rsrc_t rbias =
+            __builtin_amdgcn_make_buffer_rsrc((void *)g.bias, 0, g.bias ? (unsigned)g.N * 4u : 0u, kMxRsrcWord3);
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int n = n0 + wn * (BN / 2) + j * 32 + (e >> 2) * 8 + half * 4 + (e & 3);
+                acc[0][j][e] = __uint_as_float(
+                    __builtin_amdgcn_raw_buffer_load_b32(rbias, n < g.N ? n * 4u : kMxOutOfRange, 0, 0));
+            }
+#pragma unroll
+        for (int i = 1; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                acc[i][j] = acc[0][j];
+    }
+
+#pragma unroll
+    for (int t = 0; t < STAGES - 1; ++t)
+#pragma unroll
+        for (int c = 0; c < PER; ++c)
+            issue1(t, c);
+
+    // Half j of a K tile: blocks 2 j (lanes 0 .. 31) and 2 j + 1 of each row.
+    const int key = (l32 >> 2) & 3;
+    const int arow = wm * (BM / 2) + l32, brow = BM + wn * (BN / 2) + l32;
+    auto frag1 = [&](int t, int j, int k, i32x4_t (&a)[FM], i32x4_t (&b)[FN]) {
+        const unsigned char *s = smem + (t & (STAGES - 1)) * STAGE + (((2 * j + half) ^ key) * 16);
+        if (k < FN)
+            b[k] = *(const i32x4_t *)(s + (brow + k * 32) * 64);
+        else
+            a[k - FN] = *(const i32x4_t *)(s + (arow + (k - FN) * 32) * 64);
+    };
+    auto scale1 = [&](int t, int k, unsigned (&a)[FM], unsigned (&b)[FN]) {
+        const unsigned char *s = smem + (t & (STAGES - 1)) * STAGE + CODES;
+        if (k < FN)
+            b[k] = *(const unsigned *)(s + (brow + k * 32) * 4);
+        else
+            a[k - FN] = *(const unsigned *)(s + (arow + (k - FN) * 32) * 4);
+    };
+
+    // While the products of one half run, the other half's operands are read
+    // and the copies of the tile STAGES - 1 ahead are issued, a few
+    // instructions in the shadow of each product (32 cycles); the order is
+    // fixed here, as a run of reads or copies without products between them
+    // leaves the matrix unit idle.
+    constexpr int NM = FM * FN, FR = FM + FN;
+    i32x4_t a0[FM], b0[FN], a1[FM], b1[FN];
+    unsigned ra0[FM], rb0[FN];
+    int sa[FM], sb[FN];
+    mx_wait_vm<(STAGES - 2) * PER>();
+    mx_barrier();
+#pragma unroll
+    for (int k = 0; k < FR; ++k) {
+        frag1(0, 0, k, a0, b0);
+        scale1(0, k, ra0, rb0);
+    }
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    int t = 0;
+    do {      // quads > 0
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+            sa[i] = (int)(ra0[i] >> (8 * half));
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+            sb[j] = (int)(rb0[j] >> (8 * half));
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+            acc[m / FN][m % FN] = mx_mfma32<0>(b0[m % FN], a0[m / FN], acc[m / FN][m % FN], sb[m % FN], sa[m / FN]);
+            // copies: into the stage of tile t - 1, which every wave has read
+#pragma unroll
+            for (int k = m * (FR + PER) / NM; k < (m + 1) * (FR + PER) / NM; ++k)
+                if (k < FR)
+                    frag1(t, 1, k, a1, b1);
+                else
+                    issue1(t + STAGES - 1, k - FR);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+            acc[m / FN][m % FN] = mx_mfma32<2>(b1[m % FN], a1[m / FN], acc[m / FN][m % FN], sb[m % FN], sa[m / FN]);
+            if (m == 0) {
+                mx_wait_vm<(STAGES - 2) * PER>();      // tile t + 1 has landed
+                mx_wait_lds();                         // tile t has been read
+                mx_barrier();
+            }
+            constexpr int SPAN = NM >= 16 ? NM - 4 : NM;      // the last reads return before they are needed
+#pragma unroll
+            for (int k = m * 2 * FR / SPAN; k < (m + 1) * 2 * FR / SPAN && k < 2 * FR; ++k)
+                if (k < FR)
+                    frag1(t + 1, 0, k, a0, b0);
+                else
+                    scale1(t + 1, k - FR, ra0, rb0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        // (a fence: the compiler would sink the reads to the next iteration)
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    } while (++t < quads);
+
+    // Rows of the output through LDS, 32 at a time and wave, so that stores
+    // are 16 bytes a lane along the row.
+    mx_wait_vm<0>();
+    mx_wait_lds();
+    mx_barrier();
+    unsigned char *mine = smem + wave * 32 * PITCH;
+    constexpr int CHUNKS = FN * 32 * OS / 16, EPC = 16 / OS;      // 16-byte chunks a row, elements a chunk
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                unsigned char *p = mine + l32 * PITCH + (j * 32 + q * 8 + half * 4) * OS;
+                const float *v = (const float *)&acc[i][j] + q * 4;
+                if constexpr (OS == 4)
+                    *(f32x4_t *)p = f32x4_t{v[0], v[1], v[2], v[3]};
+                else if constexpr (O::code == CONVIMG_BF16)
+                    *(uint2 *)p = uint2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+                else
+                    *(uint2 *)p = uint2{pack_fp16(v[0], v[1]), pack_fp16(v[2], v[3])};
+            }
+        mx_wait_lds();
+        __builtin_amdgcn_wave_barrier();
+        constexpr int RP = 64 / CHUNKS;      // rows a wave instruction
+        const int k = lane % CHUNKS, n = n0 + wn * (BN / 2) + k * EPC;
+        const int rows = min(g.M - m0 - wm * (BM / 2) - i * 32, 32);
+        typename O::raw *o = (typename O::raw *)g.out + (long long)(m0 + wm * (BM / 2) + i * 32) * g.N + n;
+        if (n + EPC <= g.N) {
+#pragma unroll
+            for (int p = 0; p < 32 / RP; ++p) {
+                const int r = p * RP + lane / CHUNKS;
+                const u32v4_t v = *(const u32v4_t *)(mine + r * PITCH + k * 16);
+                if (r < rows) {
+                    if constexpr (OS == 4)
+                        *(u32v4_a4_t *)(o + (long long)r * g.N) = v;
+                    else
+                        *(u32v4_a2_t *)(o + (long long)r * g.N) = v;
+                }
+            }
+        } else if (n < g.N) {
+            for (int r = lane / CHUNKS; r < rows; r += RP)
+                for (int e = 0; n + e < g.N; ++e)
+                    o[(long long)r * g.N + e] = ((const typename O::raw *)(mine + r * PITCH + k * 16))[e];
+        }
+        mx_wait_lds();
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+}  // namespace convimg
