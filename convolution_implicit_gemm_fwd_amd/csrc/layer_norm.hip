@@ -12,6 +12,8 @@
 // All statistics and sums are fp32.  The variance is taken from the
 // differences to the mean, a second pass over the row, so that rows whose
 // mean is large against their spread keep their precision.
+#include <type_traits>
+
 #include "row_common.hpp"
 
 namespace convimg {
@@ -47,25 +49,25 @@ struct Mx4 {};
 template <typename Y>
 __device__ __forceinline__ void ln_emit(const LnFwdArgs &a, long long row, int col, const float (&v)[8])
 {
+    // (past the row there is nothing; the lanes of a block agree on this)
+    if (col >= ((a.cols + 31) & ~31))
+        return;
     if constexpr (__is_same(Y, Mx4)) {
         unsigned top = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             top = mx_top(top, v[e]);
-        top = max(top, (unsigned)__shfl_xor((int)top, 1, 64));
-        top = max(top, (unsigned)__shfl_xor((int)top, 2, 64));
+        top = quad_max(top);
         const unsigned byte = mx_scale_byte(top);
         const int kp = (a.cols + 31) & ~31;
-        if (col < kp) {
-            ((unsigned *)a.y)[row * (kp / 8) + col / 8] = mx_encode8(v, mx_scale_value(byte));
-            unsigned char *s = (unsigned char *)(a.scales + (long long)(col >> 7) * a.rows + row);
-            if ((col & 31) == 0) {
-                s[(col >> 5) & 3] = (unsigned char)byte;
-                // bytes of blocks past the row's last one are 0
-                if (col + 32 == kp)
-                    for (int b = ((col >> 5) & 3) + 1; b < 4; ++b)
-                        s[b] = 0;
-            }
+        ((unsigned *)a.y)[row * (kp / 8) + col / 8] = mx_encode8(v, mx_scale_value(byte));
+        unsigned char *s = (unsigned char *)(a.scales + (long long)(col >> 7) * a.rows + row);
+        if ((col & 31) == 0) {
+            s[(col >> 5) & 3] = (unsigned char)byte;
+            // bytes of blocks past the row's last one are 0
+            if (col + 32 == kp)
+                for (int b = ((col >> 5) & 3) + 1; b < 4; ++b)
+                    s[b] = 0;
         }
     } else {
         store8<Y>((typename Y::raw *)a.y + row * a.cols, col, a.cols, v);
@@ -87,6 +89,68 @@ __device__ __forceinline__ void ln_affine(const LnFwdArgs &a, int col, float mea
         if (a.beta)
             t += b[e];
         v[e] = col + e < a.cols ? t : 0.f;
+    }
+}
+
+// Sum of v over the TPR threads of a row, the same in each: part of a wave,
+// or the whole workgroup (`lds` then 4 floats, of alternate buffers in
+// consecutive calls, so that one barrier a sum is enough).
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float *lds)
+{
+    if constexpr (TPR <= 64) {
+        return group_sum<TPR>(v);
+    } else {
+        v = group_sum<64>(v);
+        if ((threadIdx.x & 63) == 0)
+            lds[threadIdx.x >> 6] = v;
+        __syncthreads();
+        return (lds[0] + lds[1]) + (lds[2] + lds[3]);
+    }
+}
+
+// Rows that fit the registers of TPR threads, 8 V columns each; a workgroup
+// takes kLnThreads / TPR rows at once and reads each once.
+template <typename X, typename Y, int TPR, int V>
+__global__ __launch_bounds__(kLnThreads) void ln_fwd_rows(LnFwdArgs a)
+{
+    __shared__ float lds[2][4];
+    constexpr int RPB = kLnThreads / TPR;
+    const int l = threadIdx.x % TPR;
+    const float inv = 1.f / (float)a.cols;
+    for (long long row = (long long)blockIdx.x * RPB + threadIdx.x / TPR; row < a.rows;
+         row += (long long)gridDim.x * RPB) {
+        const typename X::raw *x = (const typename X::raw *)a.x + row * a.ldx;
+        float v[V][8], s = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            load8<X>(x, (i * TPR + l) * 8, a.cols, v[i]);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                s += v[i][e];
+        const float mean = row_sum<TPR>(s, lds[0]) * inv;
+        s = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float d = (i * TPR + l) * 8 + e < a.cols ? v[i][e] - mean : 0.f;
+                s += d * d;
+            }
+        const float rstd = 1.f / sqrtf(row_sum<TPR>(s, lds[1]) * inv + a.eps);
+        if (l == 0) {
+            if (a.mean)
+                a.mean[row] = mean;
+            if (a.rstd)
+                a.rstd[row] = rstd;
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            ln_affine(a, (i * TPR + l) * 8, mean, rstd, v[i]);
+            ln_emit<Y>(a, row, (i * TPR + l) * 8, v[i]);
+        }
     }
 }
 
@@ -136,8 +200,7 @@ struct LnBwdArgs {
     const void *dy, *x;
     const float *gamma, *mean, *rstd;
     void *dx;
-    float *part;           // [parts][2][cols]: sums of dy n and of dy
-    float *dgamma, *dbeta;
+    float *part;           // [parts][2][cols]: sums of dy n and of dy; NULL to skip them
     long long rows, lddy, ldx;
     int cols, dx_dtype, parts;
 };
@@ -219,27 +282,163 @@ __global__ __launch_bounds__(kLnThreads) void ln_bwd_cols_wide(LnBwdArgs a)
     store8<Fp32>(p + a.cols, c, a.cols, db);
 }
 
-// dgamma and dbeta: the partial sums in a fixed order.
-__global__ __launch_bounds__(kLnThreads) void ln_bwd_reduce(const float *part, float *dgamma, float *dbeta, int cols,
-                                                            int parts)
+// Two sums over the TPR threads of a row at once.
+template <int TPR>
+__device__ __forceinline__ void row_sum2(float &s1, float &s2, float (*lds)[2])
 {
-    const int c = blockIdx.x * kLnThreads + threadIdx.x;
-    if (c >= cols)
-        return;
-    float g = 0.f, b = 0.f;
-    for (int p = 0; p < parts; ++p) {
-        g += part[(long long)p * 2 * cols + c];
-        b += part[(long long)p * 2 * cols + cols + c];
+    if constexpr (TPR <= 64) {
+        s1 = group_sum<TPR>(s1);
+        s2 = group_sum<TPR>(s2);
+    } else {
+        s1 = group_sum<64>(s1);
+        s2 = group_sum<64>(s2);
+        if ((threadIdx.x & 63) == 0) {
+            lds[threadIdx.x >> 6][0] = s1;
+            lds[threadIdx.x >> 6][1] = s2;
+        }
+        __syncthreads();
+        s1 = (lds[0][0] + lds[1][0]) + (lds[2][0] + lds[3][0]);
+        s2 = (lds[0][1] + lds[1][1]) + (lds[2][1] + lds[3][1]);
     }
-    dgamma[c] = g;
-    dbeta[c] = b;
+}
+
+// The whole gradient in one pass over dy and x, for rows that fit the
+// registers of TPR threads (8 V columns each).  A workgroup walks every
+// parts-th group of kLnThreads / TPR rows, reads the next group's values
+// before it sums the present one's, and keeps its columns' sums of dy n and
+// dy in registers; at the end it adds those of its row groups in a fixed
+// order and writes one partial sum.
+template <typename DY, typename X, int TPR, int V>
+__global__ __launch_bounds__(kLnThreads) void ln_bwd_rows(LnBwdArgs a)
+{
+    constexpr int RPB = kLnThreads / TPR;
+    __shared__ float lds[2][4][2];
+    __shared__ float sums[TPR > 64 ? 1 : 4][2][TPR > 64 ? 1 : TPR * 8 * V];
+    const int l = threadIdx.x % TPR;
+    const float inv = 1.f / (float)a.cols;
+    float gm[V][8], dg[V][8] = {}, db[V][8] = {};
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        if (a.gamma)
+            load8<Fp32>(a.gamma, (i * TPR + l) * 8, a.cols, gm[i]);
+        else
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                gm[i][e] = 1.f;
+    }
+    Raw8<X> rx[V];
+    Raw8<DY> rd[V];
+    float mean = 0.f, rstd = 0.f;
+    const long long step = (long long)a.parts * RPB;
+    long long row = (long long)blockIdx.x * RPB + threadIdx.x / TPR;
+    auto fetch = [&](long long r) {
+        if (r >= a.rows)
+            return;
+        mean = a.mean[r];
+        rstd = a.rstd[r];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            rx[i] = load_raw8<X>((const typename X::raw *)a.x + r * a.ldx, (i * TPR + l) * 8, a.cols);
+            rd[i] = load_raw8<DY>((const typename DY::raw *)a.dy + r * a.lddy, (i * TPR + l) * 8, a.cols);
+        }
+    };
+    fetch(row);
+    for (int k = 0; row < a.rows; row += step, k ^= 1) {
+        float n[V][8], h[V][8], s1 = 0.f, s2 = 0.f;
+        const float m = mean, r = rstd;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            unpack8<X>(rx[i], n[i]);
+            unpack8<DY>(rd[i], h[i]);
+        }
+        fetch(row + step);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                // (past the row h is 0 and n finite, unless the statistics are not)
+                n[i][e] = (i * TPR + l) * 8 + e < a.cols ? (n[i][e] - m) * r : 0.f;
+                dg[i][e] += h[i][e] * n[i][e];
+                db[i][e] += h[i][e];
+                h[i][e] *= gm[i][e];
+                s1 += h[i][e];
+                s2 += h[i][e] * n[i][e];
+            }
+        row_sum2<TPR>(s1, s2, lds[k]);
+        s1 *= inv;
+        s2 *= inv;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                h[i][e] = r * (h[i][e] - s1 - n[i][e] * s2);
+            if ((i * TPR + l) * 8 < a.cols)
+                store8_as(a.dx_dtype, a.dx, row, (i * TPR + l) * 8, a.cols, h[i]);
+        }
+    }
+    if (!a.part)
+        return;
+    float *p = a.part + (long long)blockIdx.x * 2 * a.cols;
+    if constexpr (TPR > 64) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if ((i * TPR + l) * 8 < a.cols) {
+                store8<Fp32>(p, (i * TPR + l) * 8, a.cols, dg[i]);
+                store8<Fp32>(p + a.cols, (i * TPR + l) * 8, a.cols, db[i]);
+            }
+    } else {
+        // the wave's row groups, then the four waves
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float g = stride_sum<TPR>(dg[i][e]), b = stride_sum<TPR>(db[i][e]);
+                if ((threadIdx.x & 63) < TPR) {
+                    sums[threadIdx.x >> 6][0][(i * TPR + l) * 8 + e] = g;
+                    sums[threadIdx.x >> 6][1][(i * TPR + l) * 8 + e] = b;
+                }
+            }
+        __syncthreads();
+        for (int c = threadIdx.x; c < 2 * a.cols; c += kLnThreads) {
+            const int w = c < a.cols ? 0 : 1, k = c - w * a.cols;
+            p[c] = (sums[0][w][k] + sums[1][w][k]) + (sums[2][w][k] + sums[3][w][k]);
+        }
+    }
+}
+
+// dgamma and dbeta: the partial sums in a fixed order, 16 columns a workgroup
+// and 64 threads a column.
+constexpr int kLnRedCols = 16, kLnRedThreads = 1024;
+
+__global__ __launch_bounds__(kLnRedThreads) void ln_bwd_reduce(const float *part, float *dgamma, float *dbeta,
+                                                               int cols, int parts)
+{
+    constexpr int LANES = kLnRedThreads / kLnRedCols;
+    __shared__ float lds[LANES][kLnRedCols + 1];
+    const int k = threadIdx.x % kLnRedCols, p0 = threadIdx.x / kLnRedCols;
+    const long long c = (long long)blockIdx.x * kLnRedCols + k;
+    float s = 0.f;
+    if (c < 2LL * cols)
+#pragma unroll 4
+        for (int p = p0; p < parts; p += LANES)
+            s += part[(long long)p * 2 * cols + c];
+    lds[p0][k] = s;
+    __syncthreads();
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) {
+        if (p0 < o)
+            lds[p0][k] += lds[p0 + o][k];
+        __syncthreads();
+    }
+    if (p0 == 0 && c < 2LL * cols) {
+        if (c < cols)
+            dgamma[c] = lds[0][k];
+        else
+            dbeta[c - cols] = lds[0][k];
+    }
 }
 
 constexpr long long kMaxRows = 0x7fffffffLL;
-
-// Workgroups for one a row: a launch holds fewer than 2^32 threads, so many
-// rows are walked in strides of the grid.
-unsigned ln_grid(long long rows) { return (unsigned)(rows < (1 << 22) ? rows : (1 << 22)); }
 
 // Rows and columns each fit an int; all element offsets are 64-bit.
 int ln_check(const void *x, long long ldx, long long rows, int cols, int dtype)
@@ -255,16 +454,58 @@ int ln_check(const void *x, long long ldx, long long rows, int cols, int dtype)
     return CONVIMG_OK;
 }
 
-template <typename X>
-void ln_fwd_launch(const LnFwdArgs &a, int y_dtype, hipStream_t stream)
+// Calls f<TPR, V>() for the threads a row that hold `cols` columns at 8 V
+// each: as few threads as one eighth of the columns needs (a power of two;
+// all of a wave's rows then move together), two and then four groups of eight
+// a thread for longer rows; f<0, 0>() past 8192 columns.
+template <typename F>
+void with_row_shape(int cols, F &&f)
 {
-    const dim3 grid(ln_grid(a.rows));
-    if (a.scales)
-        hipLaunchKernelGGL((ln_fwd_wide<X, Mx4>), grid, dim3(kLnThreads), 0, stream, a);
+    using std::integral_constant;
+    auto call = [&](auto t, auto v) { f(t, v); };
+#define CONVIMG_ROWS(T, V) call(integral_constant<int, T>{}, integral_constant<int, V>{})
+    if (cols <= 32)
+        CONVIMG_ROWS(4, 1);
+    else if (cols <= 64)
+        CONVIMG_ROWS(8, 1);
+    else if (cols <= 128)
+        CONVIMG_ROWS(16, 1);
+    else if (cols <= 256)
+        CONVIMG_ROWS(32, 1);
+    else if (cols <= 512)
+        CONVIMG_ROWS(64, 1);
+    else if (cols <= 1024)
+        CONVIMG_ROWS(64, 2);
+    else if (cols <= 2048)
+        CONVIMG_ROWS(256, 1);
+    else if (cols <= 4096)
+        CONVIMG_ROWS(256, 2);
+    else if (cols <= 8192)
+        CONVIMG_ROWS(256, 4);
     else
-        with_dtype(y_dtype, [&](auto y) {
-            hipLaunchKernelGGL((ln_fwd_wide<X, decltype(y)>), grid, dim3(kLnThreads), 0, stream, a);
-        });
+        CONVIMG_ROWS(0, 0);
+#undef CONVIMG_ROWS
+}
+
+// Workgroups for `rows` rows, `per` at once: a launch holds fewer than 2^32
+// threads, so very many rows are walked in strides of the grid.
+unsigned ln_grid(long long rows, int per = 1)
+{
+    const long long n = (rows + per - 1) / per;
+    return (unsigned)(n < (1 << 22) ? n : (1 << 22));
+}
+
+template <typename X, typename Y>
+void ln_fwd_launch(const LnFwdArgs &a, hipStream_t stream)
+{
+    with_row_shape(a.cols, [&](auto t, auto v) {
+        constexpr int TPR = decltype(t)::value, V = decltype(v)::value;
+        if constexpr (TPR == 0)
+            hipLaunchKernelGGL((ln_fwd_wide<X, Y>), dim3(ln_grid(a.rows)), dim3(kLnThreads), 0, stream, a);
+        else
+            hipLaunchKernelGGL((ln_fwd_rows<X, Y, TPR, V>), dim3(ln_grid(a.rows, kLnThreads / TPR)),
+                               dim3(kLnThreads), 0, stream, a);
+    });
 }
 
 int ln_fwd_call(const LnFwdArgs &a, int x_dtype, int y_dtype, hipStream_t stream)
@@ -285,13 +526,49 @@ int ln_fwd_call(const LnFwdArgs &a, int x_dtype, int y_dtype, hipStream_t stream
     }
     if (a.rows == 0)
         return CONVIMG_OK;
-    with_dtype(x_dtype, [&](auto x) { ln_fwd_launch<decltype(x)>(a, y_dtype, stream); });
+    with_dtype(x_dtype, [&](auto x) {
+        if (a.scales)
+            ln_fwd_launch<decltype(x), Mx4>(a, stream);
+        else
+            with_dtype(y_dtype, [&](auto y) { ln_fwd_launch<decltype(x), decltype(y)>(a, stream); });
+    });
     return hipGetLastError() == hipSuccess ? CONVIMG_OK : CONVIMG_ERR_LAUNCH;
 }
 
-constexpr int kLnMaxParts = 256;
+// Partial sums of the parameters' gradients, one a workgroup of the
+// backward pass: enough workgroups to keep the memory busy, few enough that
+// the partial sums (2 cols fp32 each, written and read) stay small beside
+// dy, x and dx.
+int ln_parts(long long rows, int cols)
+{
+    int per = 1;
+    with_row_shape(cols, [&](auto t, auto) {
+        if constexpr (decltype(t)::value > 0)
+            per = kLnThreads / decltype(t)::value;
+    });
+    const long long groups = (rows + per - 1) / per;
+    const int most = cols <= 512 ? 1024 : cols <= 8192 ? 512 : 256;
+    return (int)(groups < 1 ? 1 : groups < most ? groups : most);
+}
 
-int ln_parts(long long rows) { return (int)(rows < kLnMaxParts ? (rows > 0 ? rows : 1) : kLnMaxParts); }
+template <typename DY, typename X>
+void ln_bwd_launch(const LnBwdArgs &a, hipStream_t stream)
+{
+    with_row_shape(a.cols, [&](auto t, auto v) {
+        constexpr int TPR = decltype(t)::value, V = decltype(v)::value;
+        if constexpr (TPR == 0) {
+            if (a.rows > 0)
+                hipLaunchKernelGGL((ln_bwd_dx_wide<DY, X>), dim3(ln_grid(a.rows)), dim3(kLnThreads),
+                                   0, stream, a);
+            if (a.part)
+                hipLaunchKernelGGL((ln_bwd_cols_wide<DY, X>),
+                                   dim3((a.cols + 8 * kLnThreads - 1) / (8 * kLnThreads), a.parts), dim3(kLnThreads),
+                                   0, stream, a);
+        } else {
+            hipLaunchKernelGGL((ln_bwd_rows<DY, X, TPR, V>), dim3(a.parts), dim3(kLnThreads), 0, stream, a);
+        }
+    });
+}
 
 }  // namespace convimg
 
@@ -336,7 +613,7 @@ int layer_norm_bwd_workspace(long long rows, int cols, size_t *bytes)
         return CONVIMG_ERR_NULL;
     if (rows < 0 || cols <= 0)
         return CONVIMG_ERR_SHAPE;
-    *bytes = (size_t)ln_parts(rows) * 2 * (size_t)cols * 4;
+    *bytes = (size_t)ln_parts(rows, cols) * 2 * (size_t)cols * 4;
     return CONVIMG_OK;
 }
 
@@ -377,22 +654,17 @@ int layer_norm_bwd(const void *dy, long long lddy, const void *x, long long ldx,
             if (row_overlaps(out[i], nout[i], out[j], nout[j]))
                 return CONVIMG_ERR_ALIAS;
     }
-    const LnBwdArgs a = {dy,     x,     gamma, mean, rstd, dx,   (float *)ws, dgamma,
-                         dbeta,  rows,  lddy,  ldx,  cols, dx_dtype, ln_parts(rows)};
-    const int cgrid = (cols + 8 * kLnThreads - 1) / (8 * kLnThreads);
+    const LnBwdArgs a = {dy,   x,    gamma, mean, rstd,     dx,   dgamma ? (float *)ws : nullptr,
+                         rows, lddy, ldx,   cols, dx_dtype, ln_parts(rows, cols)};
+    if (rows == 0 && !dgamma)
+        return CONVIMG_OK;
+    // (with no rows the one partial sum is 0)
     with_dtype(dy_dtype, [&](auto d) {
-        with_dtype(x_dtype, [&](auto t) {
-            if (rows > 0)
-                hipLaunchKernelGGL((ln_bwd_dx_wide<decltype(d), decltype(t)>), dim3(ln_grid(rows)),
-                                   dim3(kLnThreads), 0, stream, a);
-            if (dgamma)
-                hipLaunchKernelGGL((ln_bwd_cols_wide<decltype(d), decltype(t)>), dim3(cgrid, a.parts),
-                                   dim3(kLnThreads), 0, stream, a);
-        });
+        with_dtype(x_dtype, [&](auto t) { ln_bwd_launch<decltype(d), decltype(t)>(a, stream); });
     });
     if (dgamma)
-        hipLaunchKernelGGL(ln_bwd_reduce, dim3((cols + kLnThreads - 1) / kLnThreads), dim3(kLnThreads), 0, stream,
-                           a.part, dgamma, dbeta, cols, a.parts);
+        hipLaunchKernelGGL(ln_bwd_reduce, dim3((unsigned)((2LL * cols + kLnRedCols - 1) / kLnRedCols)),
+                           dim3(kLnRedThreads), 0, stream, a.part, dgamma, dbeta, cols, a.parts);
     return hipGetLastError() == hipSuccess ? CONVIMG_OK : CONVIMG_ERR_LAUNCH;
 }
 

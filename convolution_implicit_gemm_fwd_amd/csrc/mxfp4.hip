@@ -44,8 +44,7 @@ __global__ __launch_bounds__(kMxThreads) void mx_quantize_rows(MxQuantArgs a)
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             top = mx_top(top, v[e]);
-        top = max(top, (unsigned)__shfl_xor((int)top, 1, 64));
-        top = max(top, (unsigned)__shfl_xor((int)top, 2, 64));
+        top = quad_max(top);
         const unsigned byte = mx_scale_byte(top);
         ((unsigned *)a.codes)[row * (kp / 8) + c / 8] = mx_encode8(v, mx_scale_value(byte));
         if ((c & 31) == 0) {

@@ -74,40 +74,66 @@ __device__ __forceinline__ void store1(typename T::raw *p, float v)
         *p = __builtin_bit_cast(unsigned short, (_Float16)v);
 }
 
-// Eight consecutive elements of a row whose first is element `col`, of which
-// those below `cols` exist; the others read as 0.
+// Eight consecutive elements of a row as they lie in memory.
 template <typename T>
-__device__ __forceinline__ void load8(const typename T::raw *row, int col, int cols, float (&v)[8])
+struct Raw8 {
+    u32v4_t w[T::code == CONVIMG_FP32 ? 2 : 1];
+};
+
+// The first is element `col`; of the eight those below `cols` exist, the
+// others read as 0.
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_raw8(const typename T::raw *row, int col, int cols)
 {
+    Raw8<T> r;
     if (col + 8 <= cols) {
         if constexpr (T::code == CONVIMG_FP32) {
             const u32v4_a4_t *p = (const u32v4_a4_t *)(row + col);
-            const u32v4_t a = p[0], b = p[1];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[e] = __uint_as_float(a[e]);
-                v[4 + e] = __uint_as_float(b[e]);
-            }
+            r.w[0] = p[0];
+            r.w[1] = p[1];
         } else {
-            const u32v4_t a = *(const u32v4_a2_t *)(row + col);
+            r.w[0] = *(const u32v4_a2_t *)(row + col);
+        }
+        return r;
+    }
+    typename T::raw e[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const unsigned w = a[e];
-                if constexpr (T::code == CONVIMG_BF16) {
-                    v[2 * e] = __uint_as_float(w << 16);
-                    v[2 * e + 1] = __uint_as_float(w & 0xffff0000u);
-                } else {
-                    const f16x2_t h = __builtin_bit_cast(f16x2_t, w);
-                    v[2 * e] = (float)h[0];
-                    v[2 * e + 1] = (float)h[1];
-                }
+    for (int k = 0; k < 8; ++k) {
+        e[k] = 0;
+        if (col + k < cols)
+            e[k] = row[col + k];
+    }
+    __builtin_memcpy(&r, e, sizeof(r));
+    return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack8(const Raw8<T> &r, float (&v)[8])
+{
+    if constexpr (T::code == CONVIMG_FP32) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = __uint_as_float(r.w[e / 4][e % 4]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const unsigned w = r.w[0][e];
+            if constexpr (T::code == CONVIMG_BF16) {
+                v[2 * e] = __uint_as_float(w << 16);
+                v[2 * e + 1] = __uint_as_float(w & 0xffff0000u);
+            } else {
+                const f16x2_t h = __builtin_bit_cast(f16x2_t, w);
+                v[2 * e] = (float)h[0];
+                v[2 * e + 1] = (float)h[1];
             }
         }
-        return;
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        v[e] = col + e < cols ? load1<T>(row + col + e) : 0.f;
+}
+
+template <typename T>
+__device__ __forceinline__ void load8(const typename T::raw *row, int col, int cols, float (&v)[8])
+{
+    unpack8<T>(load_raw8<T>(row, col, cols), v);
 }
 
 template <typename T>
@@ -140,15 +166,90 @@ __device__ __forceinline__ void store8(typename T::raw *row, int col, int cols, 
             store1<T>(row + col + e, v[e]);
 }
 
+// gfx950's swap of v's upper with its lower group of O lanes (O 16 or 32), in
+// every pair of groups: element 0 holds the lower group's values in both
+// groups of a pair, element 1 the upper group's.
+template <int O>
+__device__ __forceinline__ void lane_pair(float v, float (&r)[2])
+{
+    typedef unsigned u32v2 __attribute__((ext_vector_type(2)));
+    const unsigned i = __float_as_uint(v);
+    u32v2 s;
+    if constexpr (O == 16)
+        s = __builtin_amdgcn_permlane16_swap(i, i, false, false);
+    else
+        s = __builtin_amdgcn_permlane32_swap(i, i, false, false);
+    r[0] = __uint_as_float(s[0]);
+    r[1] = __uint_as_float(s[1]);
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v)
+{
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+
+// v plus the value O lanes away (in the lane number's bit O), for powers of
+// two.  MIRROR: groups of O lanes hold one value each, so that a mirrored
+// lane will do for O = 4 and 8.
+template <int O, bool MIRROR>
+__device__ __forceinline__ float pair_sum(float v)
+{
+    if constexpr (O == 1)
+        return v + dpp<0xB1>(v);       // quad [1, 0, 3, 2]
+    else if constexpr (O == 2)
+        return v + dpp<0x4E>(v);       // quad [2, 3, 0, 1]
+    else if constexpr (O == 4 && MIRROR)
+        return v + dpp<0x141>(v);      // half row mirrored
+    else if constexpr (O == 8)
+        return v + dpp<MIRROR ? 0x140 : 0x128>(v);      // row mirrored, row rotated by 8
+    else if constexpr (O == 4)
+        return v + __shfl_xor(v, 4, 64);
+    float r[2];
+    lane_pair<O>(v, r);
+    return r[0] + r[1];
+}
+
 // Sum over groups of W neighbouring lanes (W a power of two up to 64), the
 // same in every lane of a group.
 template <int W>
 __device__ __forceinline__ float group_sum(float v)
 {
-#pragma unroll
-    for (int o = W / 2; o > 0; o >>= 1)
-        v += __shfl_xor(v, o, 64);
+    if constexpr (W >= 2)
+        v = pair_sum<1, true>(v);
+    if constexpr (W >= 4)
+        v = pair_sum<2, true>(v);
+    if constexpr (W >= 8)
+        v = pair_sum<4, true>(v);
+    if constexpr (W >= 16)
+        v = pair_sum<8, true>(v);
+    if constexpr (W >= 32)
+        v = pair_sum<16, true>(v);
+    if constexpr (W >= 64)
+        v = pair_sum<32, true>(v);
     return v;
+}
+
+// Sum over the lanes of a wave that are equal modulo W.
+template <int W>
+__device__ __forceinline__ float stride_sum(float v)
+{
+    if constexpr (W <= 4)
+        v = pair_sum<4, false>(v);
+    if constexpr (W <= 8)
+        v = pair_sum<8, false>(v);
+    if constexpr (W <= 16)
+        v = pair_sum<16, false>(v);
+    if constexpr (W <= 32)
+        v = pair_sum<32, false>(v);
+    return v;
+}
+
+// Largest of the four lanes of a quad.
+__device__ __forceinline__ unsigned quad_max(unsigned v)
+{
+    v = max(v, (unsigned)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xf, 0xf, true));
+    return max(v, (unsigned)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xf, 0xf, true));
 }
 
 // The MXFP4 scale byte of a block from the bits of its largest magnitude:
