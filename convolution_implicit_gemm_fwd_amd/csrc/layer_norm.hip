@@ -92,8 +92,11 @@ __device__ __forceinline__ void ln_affine(const LnFwdArgs &a, int col, float mea
     }
 }
 
+// Threads of a workgroup whose rows take TPR threads each.
+constexpr int row_threads(int tpr) { return tpr > kLnThreads ? tpr : kLnThreads; }
+
 // Sum of v over the TPR threads of a row, the same in each: part of a wave,
-// or the whole workgroup (`lds` then 4 floats, of alternate buffers in
+// or the whole workgroup (`lds` then TPR / 64 floats, of alternate buffers in
 // consecutive calls, so that one barrier a sum is enough).
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float *lds)
@@ -105,26 +108,53 @@ __device__ __forceinline__ float row_sum(float v, float *lds)
         if ((threadIdx.x & 63) == 0)
             lds[threadIdx.x >> 6] = v;
         __syncthreads();
-        return (lds[0] + lds[1]) + (lds[2] + lds[3]);
+        v = 0.f;
+#pragma unroll
+        for (int w = 0; w < TPR / 64; w += 2)
+            v += lds[w] + lds[w + 1];
+        return v;
     }
 }
 
 // Rows that fit the registers of TPR threads, 8 V columns each; a workgroup
-// takes kLnThreads / TPR rows at once and reads each once.
+// takes row_threads(TPR) / TPR rows at once, reads each once, and the next
+// ones before it sums the present ones.
 template <typename X, typename Y, int TPR, int V>
-__global__ __launch_bounds__(kLnThreads) void ln_fwd_rows(LnFwdArgs a)
+__global__ __launch_bounds__(row_threads(TPR)) void ln_fwd_rows(LnFwdArgs a)
 {
-    __shared__ float lds[2][4];
-    constexpr int RPB = kLnThreads / TPR;
+    __shared__ float lds[2][16];
+    constexpr int RPB = row_threads(TPR) / TPR;
     const int l = threadIdx.x % TPR;
     const float inv = 1.f / (float)a.cols;
-    for (long long row = (long long)blockIdx.x * RPB + threadIdx.x / TPR; row < a.rows;
-         row += (long long)gridDim.x * RPB) {
-        const typename X::raw *x = (const typename X::raw *)a.x + row * a.ldx;
+    float gm[V][8], bt[V][8];
+    Raw8<X> raw[V];
+    const long long step = (long long)gridDim.x * RPB;
+    long long row = (long long)blockIdx.x * RPB + threadIdx.x / TPR;
+    auto fetch = [&](long long r) {
+        if (r < a.rows)
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                raw[i] = load_raw8<X>((const typename X::raw *)a.x + r * a.ldx, (i * TPR + l) * 8, a.cols);
+    };
+    fetch(row);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            gm[i][e] = 1.f;
+            bt[i][e] = 0.f;
+        }
+        if (a.gamma)
+            load8<Fp32>(a.gamma, (i * TPR + l) * 8, a.cols, gm[i]);
+        if (a.beta)
+            load8<Fp32>(a.beta, (i * TPR + l) * 8, a.cols, bt[i]);
+    }
+    for (; row < a.rows; row += step) {
         float v[V][8], s = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            load8<X>(x, (i * TPR + l) * 8, a.cols, v[i]);
+            unpack8<X>(raw[i], v[i]);
+        fetch(row + step);
 #pragma unroll
         for (int i = 0; i < V; ++i)
 #pragma unroll
@@ -136,8 +166,8 @@ __global__ __launch_bounds__(kLnThreads) void ln_fwd_rows(LnFwdArgs a)
         for (int i = 0; i < V; ++i)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float d = (i * TPR + l) * 8 + e < a.cols ? v[i][e] - mean : 0.f;
-                s += d * d;
+                v[i][e] = (i * TPR + l) * 8 + e < a.cols ? v[i][e] - mean : 0.f;
+                s += v[i][e] * v[i][e];
             }
         const float rstd = 1.f / sqrtf(row_sum<TPR>(s, lds[1]) * inv + a.eps);
         if (l == 0) {
@@ -148,7 +178,10 @@ __global__ __launch_bounds__(kLnThreads) void ln_fwd_rows(LnFwdArgs a)
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            ln_affine(a, (i * TPR + l) * 8, mean, rstd, v[i]);
+            // (past the row v, beta and so the result are 0)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[i][e] = v[i][e] * rstd * gm[i][e] + bt[i][e];
             ln_emit<Y>(a, row, (i * TPR + l) * 8, v[i]);
         }
     }
@@ -297,8 +330,12 @@ __device__ __forceinline__ void row_sum2(float &s1, float &s2, float (*lds)[2])
             lds[threadIdx.x >> 6][1] = s2;
         }
         __syncthreads();
-        s1 = (lds[0][0] + lds[1][0]) + (lds[2][0] + lds[3][0]);
-        s2 = (lds[0][1] + lds[1][1]) + (lds[2][1] + lds[3][1]);
+        s1 = s2 = 0.f;
+#pragma unroll
+        for (int w = 0; w < TPR / 64; w += 2) {
+            s1 += lds[w][0] + lds[w + 1][0];
+            s2 += lds[w][1] + lds[w + 1][1];
+        }
     }
 }
 
@@ -309,10 +346,10 @@ __device__ __forceinline__ void row_sum2(float &s1, float &s2, float (*lds)[2])
 // dy in registers; at the end it adds those of its row groups in a fixed
 // order and writes one partial sum.
 template <typename DY, typename X, int TPR, int V>
-__global__ __launch_bounds__(kLnThreads) void ln_bwd_rows(LnBwdArgs a)
+__global__ __launch_bounds__(row_threads(TPR)) void ln_bwd_rows(LnBwdArgs a)
 {
-    constexpr int RPB = kLnThreads / TPR;
-    __shared__ float lds[2][4][2];
+    constexpr int RPB = row_threads(TPR) / TPR;
+    __shared__ float lds[2][16][2];
     __shared__ float sums[TPR > 64 ? 1 : 4][2][TPR > 64 ? 1 : TPR * 8 * V];
     const int l = threadIdx.x % TPR;
     const float inv = 1.f / (float)a.cols;
@@ -479,20 +516,25 @@ void with_row_shape(int cols, F &&f)
     else if (cols <= 2048)
         CONVIMG_ROWS(256, 1);
     else if (cols <= 4096)
-        CONVIMG_ROWS(256, 2);
+        CONVIMG_ROWS(512, 1);
     else if (cols <= 8192)
-        CONVIMG_ROWS(256, 4);
+        CONVIMG_ROWS(1024, 1);
     else
         CONVIMG_ROWS(0, 0);
 #undef CONVIMG_ROWS
 }
 
-// Workgroups for `rows` rows, `per` at once: a launch holds fewer than 2^32
-// threads, so very many rows are walked in strides of the grid.
-unsigned ln_grid(long long rows, int per = 1)
+// Workgroups for one a row: a launch holds fewer than 2^32 threads, so very
+// many rows are walked in strides of the grid.
+unsigned ln_grid(long long rows) { return (unsigned)(rows < (1 << 22) ? rows : (1 << 22)); }
+
+// Workgroups of the forward pass: at most what 256 CUs hold of 2048 threads,
+// which walk the rows.
+unsigned ln_fwd_grid(long long rows, int tpr)
 {
-    const long long n = (rows + per - 1) / per;
-    return (unsigned)(n < (1 << 22) ? n : (1 << 22));
+    const long long per = row_threads(tpr) / tpr, n = (rows + per - 1) / per;
+    const long long most = 256 * 2048 / row_threads(tpr);
+    return (unsigned)(n < most ? n : most);
 }
 
 template <typename X, typename Y>
@@ -503,8 +545,8 @@ void ln_fwd_launch(const LnFwdArgs &a, hipStream_t stream)
         if constexpr (TPR == 0)
             hipLaunchKernelGGL((ln_fwd_wide<X, Y>), dim3(ln_grid(a.rows)), dim3(kLnThreads), 0, stream, a);
         else
-            hipLaunchKernelGGL((ln_fwd_rows<X, Y, TPR, V>), dim3(ln_grid(a.rows, kLnThreads / TPR)),
-                               dim3(kLnThreads), 0, stream, a);
+            hipLaunchKernelGGL((ln_fwd_rows<X, Y, TPR, V>), dim3(ln_fwd_grid(a.rows, TPR)),
+                               dim3(row_threads(TPR)), 0, stream, a);
     });
 }
 
@@ -544,7 +586,7 @@ int ln_parts(long long rows, int cols)
     int per = 1;
     with_row_shape(cols, [&](auto t, auto) {
         if constexpr (decltype(t)::value > 0)
-            per = kLnThreads / decltype(t)::value;
+            per = row_threads(decltype(t)::value) / decltype(t)::value;
     });
     const long long groups = (rows + per - 1) / per;
     const int most = cols <= 512 ? 1024 : cols <= 8192 ? 512 : 256;
@@ -565,7 +607,7 @@ void ln_bwd_launch(const LnBwdArgs &a, hipStream_t stream)
                                    dim3((a.cols + 8 * kLnThreads - 1) / (8 * kLnThreads), a.parts), dim3(kLnThreads),
                                    0, stream, a);
         } else {
-            hipLaunchKernelGGL((ln_bwd_rows<DY, X, TPR, V>), dim3(a.parts), dim3(kLnThreads), 0, stream, a);
+            hipLaunchKernelGGL((ln_bwd_rows<DY, X, TPR, V>), dim3(a.parts), dim3(row_threads(TPR)), 0, stream, a);
         }
     });
 }
