@@ -15,128 +15,11 @@
 // scale byte per lane and operand: a lane of the 32x32x64 form holds 32
 // consecutive k of one row, which is one block, so blocks need no regrouping.
 // Sums are fp32.
+#include <type_traits>
+
 #include "mxfp4_gemm.hpp"
 
 namespace convimg {
-
-struct MxQuantArgs {
-    const void *x;
-    unsigned char *codes, *scales;
-    long long ldx;
-    int rows, cols;        // of x
-    int lg;                // log2 of the threads a row
-};
-
-// Rows to MXFP4: a thread takes 8 columns, 4 neighbouring lanes a block.
-template <typename T>
-__global__ __launch_bounds__(kMxThreads) void mx_quantize_rows(MxQuantArgs a)
-{
-    const int tpr = 1 << a.lg;
-    const long long row = (long long)blockIdx.x * (kMxThreads >> a.lg) + (threadIdx.x >> a.lg);
-    if (row >= a.rows)
-        return;
-    const typename T::raw *x = (const typename T::raw *)a.x + row * a.ldx;
-    const int kp = (a.cols + 31) & ~31;
-    for (int c = (threadIdx.x & (tpr - 1)) * 8; c < kp; c += tpr * 8) {
-        float v[8];
-        load8<T>(x, c, a.cols, v);
-        unsigned top = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            top = mx_top(top, v[e]);
-        top = quad_max(top);
-        const unsigned byte = mx_scale_byte(top);
-        ((unsigned *)a.codes)[row * (kp / 8) + c / 8] = mx_encode8(v, mx_scale_value(byte));
-        if ((c & 31) == 0) {
-            unsigned char *s = a.scales + ((long long)(c >> 7) * a.rows + row) * 4;
-            s[(c >> 5) & 3] = (unsigned char)byte;
-            if (c + 32 == kp)      // bytes of blocks past the row's last one are 0
-                for (int b = ((c >> 5) & 3) + 1; b < 4; ++b)
-                    s[b] = 0;
-        }
-    }
-}
-
-// Columns to MXFP4 rows (blocks run down the columns of x): a thread takes
-// 32 rows of one column.
-template <typename T>
-__global__ __launch_bounds__(kMxThreads) void mx_quantize_cols(MxQuantArgs a)
-{
-    const int col = blockIdx.x * kMxThreads + threadIdx.x;
-    if (col >= a.cols)
-        return;
-    const int nb = mx_blocks(a.rows);
-    for (int blk = blockIdx.y; blk < nb; blk += gridDim.y) {
-        float v[32];
-        unsigned top = 0;
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-            const int r = blk * 32 + e;
-            v[e] = r < a.rows ? load1<T>((const typename T::raw *)a.x + r * a.ldx + col) : 0.f;
-            top = mx_top(top, v[e]);
-        }
-        const unsigned byte = mx_scale_byte(top);
-        const float scale = mx_scale_value(byte);
-        u32v4_t q;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float w[8] = {v[8 * i], v[8 * i + 1], v[8 * i + 2], v[8 * i + 3],
-                                v[8 * i + 4], v[8 * i + 5], v[8 * i + 6], v[8 * i + 7]};
-            q[i] = mx_encode8(w, scale);
-        }
-        *(u32v4_t *)(a.codes + ((long long)col * nb + blk) * 16) = q;
-        unsigned char *s = a.scales + ((long long)(blk >> 2) * a.cols + col) * 4;
-        s[blk & 3] = (unsigned char)byte;
-        if (blk + 1 == nb)
-            for (int b = (blk & 3) + 1; b < 4; ++b)
-                s[b] = 0;
-    }
-}
-
-// MXFP4 rows to values: a thread takes 8 columns.
-template <typename T>
-__global__ __launch_bounds__(kMxThreads) void mx_dequantize_rows(const unsigned char *codes,
-                                                                 const unsigned char *scales, void *out, int rows,
-                                                                 int cols, int lg)
-{
-    const int tpr = 1 << lg;
-    const long long row = (long long)blockIdx.x * (kMxThreads >> lg) + (threadIdx.x >> lg);
-    if (row >= rows)
-        return;
-    const int kp = (cols + 31) & ~31;
-    for (int c = (threadIdx.x & (tpr - 1)) * 8; c < cols; c += tpr * 8) {
-        const unsigned byte = scales[((long long)(c >> 7) * rows + row) * 4 + ((c >> 5) & 3)];
-        float v[8];
-        mx_decode8(((const unsigned *)codes)[row * (kp / 8) + c / 8], mx_scale_value(byte), v);
-        store8<T>((typename T::raw *)out + row * cols, c, cols, v);
-    }
-}
-
-// Column sums of x in two steps: every parts-th row into part[p][cols], then
-// the partial sums in a fixed order.
-template <typename T>
-__global__ __launch_bounds__(kMxThreads) void mx_colsum_part(const void *x, long long ldx, int rows, int cols,
-                                                             float *part)
-{
-    const int c = blockIdx.x * kMxThreads + threadIdx.x;
-    if (c >= cols)
-        return;
-    float s = 0.f;
-    for (int r = blockIdx.y; r < rows; r += gridDim.y)
-        s += load1<T>((const typename T::raw *)x + r * ldx + c);
-    part[(long long)blockIdx.y * cols + c] = s;
-}
-
-__global__ __launch_bounds__(kMxThreads) void mx_colsum_reduce(const float *part, int parts, int cols, float *out)
-{
-    const int c = blockIdx.x * kMxThreads + threadIdx.x;
-    if (c >= cols)
-        return;
-    float s = 0.f;
-    for (int p = 0; p < parts; ++p)
-        s += part[(long long)p * cols + c];
-    out[c] = s;
-}
 
 // ---- host side -------------------------------------------------------------
 
@@ -164,44 +47,63 @@ int row_lg(int cols)
 
 unsigned row_grid(int rows, int lg) { return (unsigned)(((long long)rows + (kMxThreads >> lg) - 1) / (kMxThreads >> lg)); }
 
-void quantize(const void *x, long long ldx, int rows, int cols, int dtype, bool transpose, unsigned char *codes,
+void quantize(const void *x, long long ldx, int rows, int cols, int dtype, unsigned char *codes,
               unsigned char *scales, hipStream_t stream)
 {
-    MxQuantArgs a = {x, codes, scales, ldx, rows, cols, row_lg(cols)};
+    const MxQuantArgs a = {x, codes, scales, ldx, rows, cols, row_lg(cols)};
     with_dtype(dtype, [&](auto t) {
-        typedef decltype(t) T;
-        if (!transpose) {
-            hipLaunchKernelGGL(mx_quantize_rows<T>, dim3(row_grid(rows, a.lg)), dim3(kMxThreads), 0, stream, a);
-        } else {
-            const int nb = mx_blocks(rows);
-            hipLaunchKernelGGL(mx_quantize_cols<T>, dim3((cols + kMxThreads - 1) / kMxThreads, nb < 65535 ? nb : 65535),
-                               dim3(kMxThreads), 0, stream, a);
-        }
+        hipLaunchKernelGGL(mx_quantize_rows<decltype(t)>, dim3(row_grid(rows, a.lg)), dim3(kMxThreads), 0, stream, a);
     });
 }
 
-template <int BM, int BN, typename O>
-void gemm_tiles(MxGemmArgs g, hipStream_t stream)
+unsigned eights(long long n) { return (unsigned)((n + 7) / 8 * 8); }
+
+void quantize_cols(const void *x, long long ldx, int rows, int cols, int dtype, unsigned char *codes,
+                   unsigned char *scales, hipStream_t stream)
 {
-    g.tm = (g.M + BM - 1) / BM;
-    g.tn = (g.N + BN - 1) / BN;
-    const unsigned grid = (unsigned)(((long long)g.tm * g.tn + 7) / 8 * 8);
-    hipLaunchKernelGGL((mx_gemm_tile<BM, BN, 4, O>), dim3(grid), dim3(kMxThreads), 0, stream, g);
+    const MxTileArgs a = {x, ldx, rows, cols, codes, scales, nullptr, nullptr, nullptr};
+    const long long tiles = mx_tiles(rows, cols);
+    with_dtype(dtype, [&](auto t) {
+        hipLaunchKernelGGL(mx_quantize_cols<decltype(t)>, dim3(eights(tiles)), dim3(kMxThreads), 0, stream, a,
+                           (unsigned)tiles);
+    });
 }
 
-void gemm(MxOperand a, MxOperand b, const float *bias, int M, int N, int K, int out_dtype, void *out,
-          hipStream_t stream)
+long long tile_count(int M, int N, int t) { return (long long)((M + t - 1) / t) * ((N + t - 1) / t); }
+
+// Calls f with the tile edge for a launch whose tiles of an edge number
+// count(edge): the largest that still gives most CUs one.
+template <typename C, typename F>
+void with_tile(C &&count, F &&f)
 {
-    const MxGemmArgs g = {a.codes, b.codes, a.scales, b.scales, bias, out, M, N, mx_blocks(K), 0, 0};
-    auto tiles = [&](long long t) { return ((M + t - 1) / t) * ((N + t - 1) / t); };
+    if (count(256) >= 192)
+        f(std::integral_constant<int, 256>{});
+    else if (count(128) >= 192)
+        f(std::integral_constant<int, 128>{});
+    else
+        f(std::integral_constant<int, 64>{});
+}
+
+MxGemmArgs gemm_args(MxOperand a, MxOperand b, const float *bias, int M, int N, int K, void *out)
+{
+    return {a.codes, b.codes, a.scales, b.scales, bias, out, M, N, mx_blocks(K), 0, 0};
+}
+
+unsigned gemm_grid(MxGemmArgs &g, int tile)
+{
+    g.tm = (g.M + tile - 1) / tile;
+    g.tn = (g.N + tile - 1) / tile;
+    return eights((long long)g.tm * g.tn);
+}
+
+void gemm(MxGemmArgs g, int out_dtype, hipStream_t stream)
+{
     with_dtype(out_dtype, [&](auto o) {
-        typedef decltype(o) O;
-        if (tiles(256) >= 192)
-            gemm_tiles<256, 256, O>(g, stream);
-        else if (tiles(128) >= 192)
-            gemm_tiles<128, 128, O>(g, stream);
-        else
-            gemm_tiles<64, 64, O>(g, stream);
+        with_tile([&](int t) { return tile_count(g.M, g.N, t); }, [&](auto tile) {
+            constexpr int T = decltype(tile)::value;
+            const unsigned grid = gemm_grid(g, T);
+            hipLaunchKernelGGL((mx_gemm_tile<T, T, 4, decltype(o)>), dim3(grid), dim3(kMxThreads), 0, stream, g);
+        });
     });
 }
 
@@ -216,9 +118,6 @@ int mx_shape(long long rows, long long cols)
 }
 
 int launched() { return hipGetLastError() == hipSuccess ? CONVIMG_OK : CONVIMG_ERR_LAUNCH; }
-
-constexpr int kMxSumParts = 128;
-int sum_parts(int rows) { return rows < kMxSumParts ? (rows > 0 ? rows : 1) : kMxSumParts; }
 
 bool misaligned(const void *p, unsigned n) { return ((uintptr_t)p & (n - 1)) != 0; }
 
@@ -240,7 +139,7 @@ BwdLayout bwd_layout(int M, int N, int K)
     l.wt = take(packed_bytes(K, N));
     l.dyt = take(M > 0 ? packed_bytes(N, M) : 0);
     l.xt = take(M > 0 ? packed_bytes(K, M) : 0);
-    l.part = take(align256((size_t)sum_parts(M) * N * 4));
+    l.part = take(align256((size_t)((M + kMxTile - 1) / kMxTile) * N * 4));
     l.total = at;
     return l;
 }
@@ -311,7 +210,10 @@ int mxfp4_quantize(const void *x, long long ldx, int rows, int cols, int dtype, 
     const size_t nx = span_bytes(rows, ldx, cols, dtype), nc = mx_code_bytes(qr, qc), ns = mx_scale_bytes(qr, qc);
     if (row_overlaps(codes, nc, x, nx) || row_overlaps(scales, ns, x, nx) || row_overlaps(codes, nc, scales, ns))
         return CONVIMG_ERR_ALIAS;
-    quantize(x, ldx, rows, cols, dtype, transpose != 0, (unsigned char *)codes, (unsigned char *)scales, stream);
+    if (transpose)
+        quantize_cols(x, ldx, rows, cols, dtype, (unsigned char *)codes, (unsigned char *)scales, stream);
+    else
+        quantize(x, ldx, rows, cols, dtype, (unsigned char *)codes, (unsigned char *)scales, stream);
     return launched();
 }
 
@@ -391,10 +293,10 @@ int mxfp4_linear_fwd(const void *x, long long ldx, const void *x_scales, int x_d
     const MxOperand b = {(const unsigned char *)w_codes, (const unsigned char *)w_scales};
     if (dense) {
         unsigned char *c = (unsigned char *)ws, *s = c + align256(mx_code_bytes(M, K));
-        quantize(x, ldx, M, K, x_dtype, false, c, s, stream);
+        quantize(x, ldx, M, K, x_dtype, c, s, stream);
         a = {c, s};
     }
-    gemm(a, b, bias, M, N, K, out_dtype, out, stream);
+    gemm(gemm_args(a, b, bias, M, N, K, out), out_dtype, stream);
     return launched();
 }
 
@@ -449,25 +351,39 @@ int mxfp4_linear_bwd(const void *dy, long long lddy, int dy_dtype, const void *x
     auto operand = [&](size_t at, int rows, int cols) {
         return MxOperand{base + at, base + at + align256(mx_code_bytes(rows, cols))};
     };
-    auto pack = [&](const void *p, long long ld, int rows, int cols, int t, bool tr, MxOperand o) {
-        quantize(p, ld, rows, cols, t, tr, (unsigned char *)o.codes, (unsigned char *)o.scales, stream);
-    };
     const MxOperand qdy = operand(l.dy, M, N), qwt = operand(l.wt, K, N), qdyt = operand(l.dyt, N, M),
                     qxt = operand(l.xt, K, M);
-    pack(dy, lddy, M, N, dy_dtype, false, qdy);
-    pack(w, ldw, N, K, dtype, true, qwt);
-    pack(dy, lddy, M, N, dy_dtype, true, qdyt);
-    pack(x, ldx, M, K, dtype, true, qxt);
-    gemm(qdy, qwt, nullptr, M, K, N, dx_dtype, dx, stream);
-    gemm(qdyt, qxt, nullptr, N, K, M, CONVIMG_FP32, dw, stream);
-    if (db) {
-        float *part = (float *)(base + l.part);
-        const dim3 grid((N + kMxThreads - 1) / kMxThreads, sum_parts(M));
-        with_dtype(dy_dtype, [&](auto t) {
-            hipLaunchKernelGGL(mx_colsum_part<decltype(t)>, grid, dim3(kMxThreads), 0, stream, dy, lddy, M, N, part);
+    float *part = (float *)(base + l.part);
+    auto tiles = [](const void *p, long long ld, int rows, int cols, MxOperand down, MxOperand along, float *sums) {
+        return MxTileArgs{p,
+                          ld,
+                          rows,
+                          cols,
+                          (unsigned char *)down.codes,
+                          (unsigned char *)down.scales,
+                          (unsigned char *)along.codes,
+                          (unsigned char *)along.scales,
+                          sums};
+    };
+    const long long t_dy = mx_tiles(M, N), t_w = mx_tiles(N, K), t_all = t_dy + t_w + mx_tiles(M, K);
+    const MxTileArgs a_dy = tiles(dy, lddy, M, N, qdyt, qdy, part), a_w = tiles(w, ldw, N, K, qwt, {}, nullptr),
+                     a_x = tiles(x, ldx, M, K, qxt, {}, nullptr);
+    with_dtype(dy_dtype, [&](auto d) {
+        with_dtype(dtype, [&](auto t) {
+            hipLaunchKernelGGL((mx_quantize_bwd<decltype(d), decltype(t)>), dim3(eights(t_all)), dim3(kMxThreads), 0,
+                               stream, a_dy, a_w, a_x, (unsigned)t_dy, (unsigned)t_w, (unsigned)t_all);
         });
-        hipLaunchKernelGGL(mx_colsum_reduce, dim3(grid.x), dim3(kMxThreads), 0, stream, part, sum_parts(M), N, db);
-    }
+    });
+    MxGemmArgs g_dx = gemm_args(qdy, qwt, nullptr, M, K, N, dx), g_dw = gemm_args(qdyt, qxt, nullptr, N, K, M, dw);
+    const MxSumArgs sum = {part, db, (M + kMxTile - 1) / kMxTile, N};
+    with_dtype(dx_dtype, [&](auto o) {
+        with_tile([&](int t) { return tile_count(M, K, t) + tile_count(N, K, t); }, [&](auto tile) {
+            constexpr int T = decltype(tile)::value;
+            const unsigned n_dx = gemm_grid(g_dx, T), n_dw = gemm_grid(g_dw, T), n_db = db ? (N + 63) / 64 : 0;
+            hipLaunchKernelGGL((mx_gemm_bwd<T, T, 4, decltype(o)>), dim3(n_dw + n_dx + n_db), dim3(kMxThreads), 0,
+                               stream, g_dw, g_dx, sum, n_dw, n_dx);
+        });
+    });
     return launched();
 }
 

@@ -8,7 +8,7 @@
 // so that a lane ends with four neighbouring columns of one output row.
 #pragma once
 
-#include "row_common.hpp"
+#include "mxfp4_quant.hpp"
 
 namespace convimg {
 
@@ -16,7 +16,6 @@ typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
-constexpr int kMxThreads = 256;
 constexpr unsigned kMxOutOfRange = 0x80000000u;   // buffer offset past every packed operand
 constexpr int kMxRsrcWord3 = 0x00020000;          // raw buffer, 32-bit data format
 
@@ -64,25 +63,27 @@ __device__ __forceinline__ f32x16_t mx_mfma32(i32x4_t b, i32x4_t a, f32x16_t c, 
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b8, a8, c, 4, 4, SEL, sb, SEL, sa);
 }
 
-// Tile of workgroup `bid`.  Workgroups go to the 8 XCDs in turn; each XCD
-// takes one run of tiles (so that its L2 serves neighbours), ordered in
-// groups of 8 tile rows so that the tiles in flight are near square.
-__device__ __forceinline__ bool mx_tile(const MxGemmArgs &g, int &m, int &n)
+// Tile number `id` (mx_xcd_tile: each XCD takes one run of them, so that its
+// L2 serves neighbours), in groups of 8 tile rows so that the tiles in flight
+// are near square.
+__device__ __forceinline__ void mx_tile(const MxGemmArgs &g, int id, int &m, int &n)
 {
-    const int per = gridDim.x / 8;
-    const int id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if (id >= g.tm * g.tn)
-        return false;
     const int span = 8 * g.tn, group = id / span, in = id - group * span;
     const int rows = min(g.tm - group * 8, 8);
     n = in / rows;
     m = group * 8 + in - n * rows;
-    return true;
+}
+
+template <int BM, int BN, int STAGES, int OS>
+constexpr int mx_gemm_lds()
+{
+    constexpr int ring = STAGES * (BM + BN) * 68, rows = 4 * 32 * (BN / 2 * OS + 16);
+    return ring > rows ? ring : rows;
 }
 
 // BM x BN tiles, four waves 2 x 2, K tiles of 128 (four blocks a row).
 template <int BM, int BN, int STAGES, typename O>
-__global__ __launch_bounds__(kMxThreads) void mx_gemm_tile(MxGemmArgs g)
+__device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsigned char *smem)
 {
     constexpr int FM = BM / 64, FN = BN / 64;               // 32 x 32 blocks of a wave
     constexpr int ROWS = BM + BN;
@@ -92,17 +93,14 @@ __global__ __launch_bounds__(kMxThreads) void mx_gemm_tile(MxGemmArgs g)
     constexpr int PER = CP + SP;
     constexpr int OS = sizeof(typename O::raw);
     constexpr int PITCH = FN * 32 * OS + 16;                // epilogue: 32 rows a wave
-    constexpr int SMEM = STAGES * STAGE > 4 * 32 * PITCH ? STAGES * STAGE : 4 * 32 * PITCH;
     static_assert((STAGES & (STAGES - 1)) == 0 && (STAGES - 2) * PER < 64, "ring of stages");
-    __shared__ __attribute__((aligned(16))) unsigned char smem[SMEM];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave & 1, wn = wave >> 1;
     const int half = lane >> 5, l32 = lane & 31;
     int tm, tn;
-    if (!mx_tile(g, tm, tn))
-        return;
+    mx_tile(g, id, tm, tn);
     const int m0 = tm * BM, n0 = tn * BN;
     const int quads = (g.kb + 3) / 4;
 
@@ -299,6 +297,57 @@ __global__ __launch_bounds__(kMxThreads) void mx_gemm_tile(MxGemmArgs g)
         }
         mx_wait_lds();
         __builtin_amdgcn_wave_barrier();
+    }
+}
+
+template <int BM, int BN, int STAGES, typename O>
+__global__ __launch_bounds__(kMxThreads) void mx_gemm_tile(MxGemmArgs g)
+{
+    __shared__ __attribute__((aligned(16))) unsigned char smem[mx_gemm_lds<BM, BN, STAGES, sizeof(typename O::raw)>()];
+    const unsigned id = mx_xcd_tile(blockIdx.x, gridDim.x);
+    if (id < (unsigned)g.tm * g.tn)
+        mx_gemm_body<BM, BN, STAGES, O>(g, id, smem);
+}
+
+// Column sums from partial sums [parts][cols], 64 columns a workgroup.
+struct MxSumArgs {
+    const float *part;
+    float *out;            // NULL: none
+    int parts, cols;
+};
+
+__device__ __forceinline__ void mx_sum_parts(const MxSumArgs &a, unsigned block, float *lds)
+{
+    const int c = (int)block * 64 + (threadIdx.x & 63), w = threadIdx.x >> 6;
+    float s = 0.f;
+    if (c < a.cols)
+#pragma unroll 4
+        for (int p = w; p < a.parts; p += 4)
+            s += a.part[(long long)p * a.cols + c];
+    lds[threadIdx.x] = s;
+    __syncthreads();
+    if (w == 0 && c < a.cols)
+        a.out[c] = (lds[threadIdx.x] + lds[threadIdx.x + 64]) + (lds[threadIdx.x + 128] + lds[threadIdx.x + 192]);
+}
+
+// Both products of the backward pass and the sums of db in one launch; the
+// first `dw_blocks` workgroups take dw's tiles (fp32), the next `dx_blocks`
+// those of dx, the others 64 columns of db each.
+template <int BM, int BN, int STAGES, typename O>
+__global__ __launch_bounds__(kMxThreads) void mx_gemm_bwd(MxGemmArgs dw, MxGemmArgs dx, MxSumArgs db,
+                                                          unsigned dw_blocks, unsigned dx_blocks)
+{
+    __shared__ __attribute__((aligned(16))) unsigned char smem[mx_gemm_lds<BM, BN, STAGES, 4>()];
+    if (blockIdx.x < dw_blocks) {
+        const unsigned id = mx_xcd_tile(blockIdx.x, dw_blocks);
+        if (id < (unsigned)dw.tm * dw.tn)
+            mx_gemm_body<BM, BN, STAGES, Fp32>(dw, id, smem);
+    } else if (blockIdx.x < dw_blocks + dx_blocks) {
+        const unsigned id = mx_xcd_tile(blockIdx.x - dw_blocks, dx_blocks);
+        if (id < (unsigned)dx.tm * dx.tn)
+            mx_gemm_body<BM, BN, STAGES, O>(dx, id, smem);
+    } else {
+        mx_sum_parts(db, blockIdx.x - dw_blocks - dx_blocks, (float *)smem);
     }
 }
 

@@ -1,0 +1,242 @@
+// mxfp4_quant.hpp -- dense rows to MXFP4 and back.
+//
+// Blocks along a row are quantised straight from memory (four neighbouring
+// lanes hold one).  Blocks down the columns go through LDS in tiles of 128 x
+// 128 (four blocks either way, so that a tile owns whole scale dwords); a
+// tile can also be quantised along its rows and summed down its columns, so
+// that an operand that is contracted over either axis is read once.
+#pragma once
+
+#include "row_common.hpp"
+
+namespace convimg {
+
+constexpr int kMxThreads = 256;
+
+struct MxQuantArgs {
+    const void *x;
+    unsigned char *codes, *scales;
+    long long ldx;
+    int rows, cols;        // of x
+    int lg;                // log2 of the threads a row
+};
+
+// Rows to MXFP4: a thread takes 8 columns.
+template <typename T>
+__global__ __launch_bounds__(kMxThreads) void mx_quantize_rows(MxQuantArgs a)
+{
+    const int tpr = 1 << a.lg;
+    const long long row = (long long)blockIdx.x * (kMxThreads >> a.lg) + (threadIdx.x >> a.lg);
+    if (row >= a.rows)
+        return;
+    const typename T::raw *x = (const typename T::raw *)a.x + row * a.ldx;
+    const int kp = (a.cols + 31) & ~31;
+    for (int c = (threadIdx.x & (tpr - 1)) * 8; c < kp; c += tpr * 8) {
+        float v[8];
+        load8<T>(x, c, a.cols, v);
+        unsigned top = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            top = mx_top(top, v[e]);
+        top = quad_max(top);
+        const unsigned byte = mx_scale_byte(top);
+        ((unsigned *)a.codes)[row * (kp / 8) + c / 8] = mx_encode8(v, mx_scale_value(byte));
+        if ((c & 31) == 0) {
+            unsigned char *s = a.scales + ((long long)(c >> 7) * a.rows + row) * 4;
+            s[(c >> 5) & 3] = (unsigned char)byte;
+            if (c + 32 == kp)      // bytes of blocks past the row's last one are 0
+                for (int b = ((c >> 5) & 3) + 1; b < 4; ++b)
+                    s[b] = 0;
+        }
+    }
+}
+
+// A matrix that is quantised in tiles: down its columns into ccodes
+// [cols][rows / 32 blocks], along its rows into rcodes, and summed down its
+// columns, one partial sum a row of tiles.
+struct MxTileArgs {
+    const void *x;
+    long long ldx;
+    int rows, cols;
+    unsigned char *ccodes, *cscales, *rcodes, *rscales;
+    float *part;           // [tiles down][cols]
+};
+
+constexpr int kMxTile = 128;
+constexpr int kMxOutPitch = 64 + 16;      // LDS bytes of a column's result: four blocks of codes, their scales
+
+template <typename T>
+constexpr int mx_tile_pitch() { return kMxTile * (int)sizeof(typename T::raw) + 16; }
+
+template <typename T>
+constexpr int mx_tile_lds() { return kMxTile * (mx_tile_pitch<T>() + kMxOutPitch + 16); }
+
+inline long long mx_tiles(int rows, int cols)
+{
+    return (long long)((rows + kMxTile - 1) / kMxTile) * ((cols + kMxTile - 1) / kMxTile);
+}
+
+// 32 values to four code dwords and a scale byte.
+__device__ __forceinline__ unsigned mx_encode32(const float (&v)[32], u32v4_t &q)
+{
+    unsigned top = 0;
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+        top = mx_top(top, v[e]);
+    const unsigned byte = mx_scale_byte(top);
+    const float scale = mx_scale_value(byte);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float w[8] = {v[8 * i],     v[8 * i + 1], v[8 * i + 2], v[8 * i + 3],
+                            v[8 * i + 4], v[8 * i + 5], v[8 * i + 6], v[8 * i + 7]};
+        q[i] = mx_encode8(w, scale);
+    }
+    return byte;
+}
+
+// One tile, by the whole workgroup; lds: mx_tile_lds<T>() bytes, 16-byte
+// aligned.  ROWS: along the rows and the column sums too.
+template <typename T, bool ROWS>
+__device__ __forceinline__ void mx_quantize_tile(const MxTileArgs &a, unsigned tile, unsigned char *lds)
+{
+    constexpr int PITCH = mx_tile_pitch<T>(), ES = sizeof(typename T::raw);
+    unsigned char *out = lds + kMxTile * PITCH;
+    float *sums = (float *)(out + kMxTile * kMxOutPitch);      // [4 waves][128]
+    const int across = (a.cols + kMxTile - 1) / kMxTile;
+    const int tr = (int)(tile / across), tc = (int)(tile - (unsigned)tr * across);
+    const int r0 = tr * kMxTile, c0 = tc * kMxTile;
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+
+    // 16 threads a row of the tile, zeros past the matrix
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+        const int r = p * 16 + (t >> 4), c = (t & 15) * 8;
+        Raw8<T> v = {};
+        if (r0 + r < a.rows)
+            v = load_raw8<T>((const typename T::raw *)a.x + (long long)(r0 + r) * a.ldx, c0 + c, a.cols);
+        *(Raw8<T> *)(lds + r * PITCH + c * ES) = v;
+    }
+    __syncthreads();
+
+    // down: a wave takes 32 rows, a lane two columns of them
+    {
+        float v[2][32], s[2] = {0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+            typename T::raw w[2];
+            __builtin_memcpy(w, __builtin_assume_aligned(lds + (wave * 32 + e) * PITCH + lane * 2 * ES, 2 * ES), 2 * ES);
+            v[0][e] = load1<T>(&w[0]);
+            v[1][e] = load1<T>(&w[1]);
+            s[0] += v[0][e];
+            s[1] += v[1][e];
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            u32v4_t q;
+            const unsigned byte = mx_encode32(v[k], q);
+            *(u32v4_t *)(out + (lane * 2 + k) * kMxOutPitch + wave * 16) = q;
+            out[(lane * 2 + k) * kMxOutPitch + 64 + wave] = (unsigned char)byte;
+            if constexpr (ROWS)
+                sums[wave * kMxTile + lane * 2 + k] = s[k];
+        }
+    }
+    // along: a thread takes two blocks of a row
+    if constexpr (ROWS) {
+        const int row = r0 + (t >> 1), nb = mx_blocks(a.cols), b0 = tc * 4 + (t & 1) * 2;
+        unsigned bytes = 0;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float v[32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const Raw8<T> w = *(const Raw8<T> *)(lds + (t >> 1) * PITCH + ((t & 1) * 64 + k * 32 + i * 8) * ES);
+                float u[8];
+                unpack8<T>(w, u);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[i * 8 + e] = u[e];
+            }
+            u32v4_t q;
+            bytes |= mx_encode32(v, q) << (8 * k);
+            if (row < a.rows && b0 + k < nb)
+                *(u32v4_t *)(a.rcodes + ((long long)row * nb + b0 + k) * 16) = q;
+        }
+        bytes |= (unsigned)__builtin_amdgcn_mov_dpp((int)bytes, 0xB1, 0xf, 0xf, true) << 16;
+        if (row < a.rows && (t & 1) == 0)
+            *(unsigned *)(a.rscales + ((long long)tc * a.rows + row) * 4) = bytes;
+    }
+    __syncthreads();
+
+    // the columns' results, two lanes a column
+    {
+        const int col = c0 + (t >> 1), nb = mx_blocks(a.rows), b0 = tr * 4 + (t & 1) * 2;
+        const unsigned char *o = out + (t >> 1) * kMxOutPitch;
+        if (col < a.cols) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                if (b0 + k < nb)
+                    *(u32v4_t *)(a.ccodes + ((long long)col * nb + b0 + k) * 16) =
+                        *(const u32v4_t *)(o + ((t & 1) * 2 + k) * 16);
+            if ((t & 1) == 0)
+                *(unsigned *)(a.cscales + ((long long)tr * a.cols + col) * 4) = *(const unsigned *)(o + 64);
+        }
+        if constexpr (ROWS)
+            if (t < kMxTile && c0 + t < a.cols)
+                a.part[(long long)tr * a.cols + c0 + t] =
+                    (sums[t] + sums[kMxTile + t]) + (sums[2 * kMxTile + t] + sums[3 * kMxTile + t]);
+    }
+}
+
+// Tile of a workgroup among `tiles`: each of the 8 XCDs, which take
+// workgroups in turn, gets one run, so that the halves of a cache line that
+// neighbouring tiles write meet in one L2.
+__device__ __forceinline__ unsigned mx_xcd_tile(unsigned block, unsigned blocks)
+{
+    return (block & 7) * (blocks >> 3) + (block >> 3);
+}
+
+template <typename T>
+__global__ __launch_bounds__(kMxThreads) void mx_quantize_cols(MxTileArgs a, unsigned tiles)
+{
+    __shared__ __attribute__((aligned(16))) unsigned char lds[mx_tile_lds<T>()];
+    const unsigned tile = mx_xcd_tile(blockIdx.x, gridDim.x);
+    if (tile < tiles)
+        mx_quantize_tile<T, false>(a, tile, lds);
+}
+
+// The operands of the backward pass in one launch: dy both ways with its
+// column sums, w and x down their columns.
+template <typename DY, typename X>
+__global__ __launch_bounds__(kMxThreads) void mx_quantize_bwd(MxTileArgs dy, MxTileArgs w, MxTileArgs x,
+                                                              unsigned dy_tiles, unsigned w_tiles, unsigned tiles)
+{
+    constexpr int LDS = mx_tile_lds<DY>() > mx_tile_lds<X>() ? mx_tile_lds<DY>() : mx_tile_lds<X>();
+    __shared__ __attribute__((aligned(16))) unsigned char lds[LDS];
+    const unsigned tile = mx_xcd_tile(blockIdx.x, gridDim.x);
+    if (tile < dy_tiles)
+        mx_quantize_tile<DY, true>(dy, tile, lds);
+    else if (tile < tiles)
+        mx_quantize_tile<X, false>(tile < dy_tiles + w_tiles ? w : x,
+                                   tile - (tile < dy_tiles + w_tiles ? dy_tiles : dy_tiles + w_tiles), lds);
+}
+
+// MXFP4 rows to values: a thread takes 8 columns.
+template <typename T>
+__global__ __launch_bounds__(kMxThreads) void mx_dequantize_rows(const unsigned char *codes,
+                                                                 const unsigned char *scales, void *out, int rows,
+                                                                 int cols, int lg)
+{
+    const int tpr = 1 << lg;
+    const long long row = (long long)blockIdx.x * (kMxThreads >> lg) + (threadIdx.x >> lg);
+    if (row >= rows)
+        return;
+    const int kp = (cols + 31) & ~31;
+    for (int c = (threadIdx.x & (tpr - 1)) * 8; c < cols; c += tpr * 8) {
+        const unsigned byte = scales[((long long)(c >> 7) * rows + row) * 4 + ((c >> 5) & 3)];
+        float v[8];
+        mx_decode8(((const unsigned *)codes)[row * (kp / 8) + c / 8], mx_scale_value(byte), v);
+        store8<T>((typename T::raw *)out + row * cols, c, cols, v);
+    }
+}
+
+}  // namespace convimg
