@@ -102,7 +102,7 @@ void gemm(MxGemmArgs g, int out_dtype, hipStream_t stream)
         with_tile([&](int t) { return tile_count(g.M, g.N, t); }, [&](auto tile) {
             constexpr int T = decltype(tile)::value;
             const unsigned grid = gemm_grid(g, T);
-            hipLaunchKernelGGL((mx_gemm_tile<T, T, 4, decltype(o)>), dim3(grid), dim3(kMxThreads), 0, stream, g);
+            hipLaunchKernelGGL((mx_gemm_tile<T, T, 256, 2, decltype(o)>), dim3(grid), dim3(kMxThreads), 0, stream, g);
         });
     });
 }
@@ -380,7 +380,7 @@ int mxfp4_linear_bwd(const void *dy, long long lddy, int dy_dtype, const void *x
         with_tile([&](int t) { return tile_count(M, K, t) + tile_count(N, K, t); }, [&](auto tile) {
             constexpr int T = decltype(tile)::value;
             const unsigned n_dx = gemm_grid(g_dx, T), n_dw = gemm_grid(g_dw, T), n_db = db ? (N + 63) / 64 : 0;
-            hipLaunchKernelGGL((mx_gemm_bwd<T, T, 4, decltype(o)>), dim3(n_dw + n_dx + n_db), dim3(kMxThreads), 0,
+            hipLaunchKernelGGL((mx_gemm_bwd<T, T, 256, 2, decltype(o)>), dim3(n_dw + n_dx + n_db), dim3(kMxThreads), 0,
                                stream, g_dw, g_dx, sum, n_dw, n_dx);
         });
     });

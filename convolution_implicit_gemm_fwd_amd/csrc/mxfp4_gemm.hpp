@@ -74,26 +74,29 @@ __device__ __forceinline__ void mx_tile(const MxGemmArgs &g, int id, int &m, int
     m = group * 8 + in - n * rows;
 }
 
-template <int BM, int BN, int STAGES, int OS>
+template <int BM, int BN, int BK, int STAGES, int OS>
 constexpr int mx_gemm_lds()
 {
-    constexpr int ring = STAGES * (BM + BN) * 68, rows = 4 * 32 * (BN / 2 * OS + 16);
+    constexpr int ring = STAGES * (BM + BN) * (BK / 2 + BK / 32), rows = 4 * 32 * (BN / 2 * OS + 16);
     return ring > rows ? ring : rows;
 }
 
-// BM x BN tiles, four waves 2 x 2, K tiles of 128 (four blocks a row).
-template <int BM, int BN, int STAGES, typename O>
+// BM x BN tiles, four waves 2 x 2, K tiles of BK in a ring of STAGES.
+template <int BM, int BN, int BK, int STAGES, typename O>
 __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsigned char *smem)
 {
     constexpr int FM = BM / 64, FN = BN / 64;               // 32 x 32 blocks of a wave
     constexpr int ROWS = BM + BN;
-    constexpr int CODES = ROWS * 64, STAGE = CODES + ROWS * 4;
-    constexpr int CP = ROWS / 64;                           // code copies a wave and stage: 64 rows a pass
-    constexpr int SP = ROWS >= 256 ? ROWS / 256 : 1;        // scale copies: 64 rows a wave
-    constexpr int PER = CP + SP;
+    constexpr int C = BK / 32, Q = BK / 128, H = BK / 64;   // blocks, scale dwords and product steps of a K tile
+    constexpr int CODES = ROWS * C * 16, STAGE = CODES + ROWS * Q * 4;
+    constexpr int RPC = 64 / C;                             // rows a wave's copy
+    constexpr int CP = ROWS / (4 * RPC);                    // code copies a wave and stage
+    constexpr int SP = ROWS >= 256 ? ROWS / 256 : 1;        // scale copies (64 rows) a wave and dword
+    constexpr int PER = CP + SP * Q, EARLY = PER / 2;
     constexpr int OS = sizeof(typename O::raw);
     constexpr int PITCH = FN * 32 * OS + 16;                // epilogue: 32 rows a wave
-    static_assert((STAGES & (STAGES - 1)) == 0 && (STAGES - 2) * PER < 64, "ring of stages");
+    static_assert((STAGES & (STAGES - 1)) == 0 && (STAGES - 2) * PER + EARLY < 64, "ring of stages");
+    static_assert(C == 4 || C == 8, "64 or 128 bytes a row");
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -102,23 +105,24 @@ __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsign
     int tm, tn;
     mx_tile(g, id, tm, tn);
     const int m0 = tm * BM, n0 = tn * BN;
-    const int quads = (g.kb + 3) / 4;
+    const int quads = (g.kb + 3) / 4, nk = (g.kb + C - 1) / C;
 
     const unsigned ca = (unsigned)g.M * g.kb * 16u, cb = (unsigned)g.N * g.kb * 16u;
     const unsigned na = (unsigned)g.M * quads * 4u, nb = (unsigned)g.N * quads * 4u;
     const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void *)g.a, 0, ca, kMxRsrcWord3);
     const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc((void *)g.b, 0, cb, kMxRsrcWord3);
 
-    // Copies of codes: pass p, this lane: tile row p * 64 + wave * 16 +
-    // lane / 4, physical 16-byte chunk lane % 4 of its 64 bytes.  Chunk c of
-    // row r lies at c ^ (r / 4 % 4): 16 rows' equal chunks then cover all
-    // banks.
-    const int chunk = (lane & 3) ^ ((lane >> 4) & 3);
+    // Copies of codes: this lane's row of the wave's RPC, and the physical
+    // 16-byte chunk lane % C of that row.  Chunk c of row r lies at
+    // c ^ key(r): 16 rows' equal chunks then cover all banks.
+    auto key = [](int r) { return C == 4 ? (r >> 2) & 3 : (r >> 1) & 7; };
+    const int crow = wave * RPC + lane / C;
+    const int chunk = (lane & (C - 1)) ^ key(crow);
     unsigned coff[CP];
 #pragma unroll
     for (int p = 0; p < CP; ++p) {
-        const int r = p * 64 + wave * 16 + (lane >> 2);
-        const bool isa = p * 64 < BM;
+        const int r = p * 4 * RPC + crow;      // (4 RPC rows a pass keep the key)
+        const bool isa = p * 4 * RPC < BM;
         const int row = isa ? m0 + r : n0 + r - BM;
         coff[p] = row < (isa ? g.M : g.N) ? (unsigned)row * (unsigned)g.kb * 16u + chunk * 16 : kMxOutOfRange;
     }
@@ -141,11 +145,13 @@ __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsign
     // PER copies.
     auto issue1 = [&](int t, int c) {
         unsigned char *s = smem + (t & (STAGES - 1)) * STAGE;
-        if (c < CP)
-            mx_dma16(c * 64 < BM ? ra : rb, s + c * 4096 + wave * 1024,
-                     t * 4 + chunk < g.kb ? coff[c] + t * 64u : kMxOutOfRange);
-        else
-            mx_dma4(rs[c - CP], s + CODES + sgroup[c - CP] * 256, soff[c - CP] + t * sstep[c - CP]);
+        if (c < CP) {
+            mx_dma16(c * 4 * RPC < BM ? ra : rb, s + c * 4096 + wave * 1024,
+                     t * C + chunk < g.kb ? coff[c] + t * (C * 16u) : kMxOutOfRange);
+        } else {
+            const int p = (c - CP) / Q, q = (c - CP) % Q;
+            mx_dma4(rs[p], s + CODES + q * ROWS * 4 + sgroup[p] * 256, soff[p] + (t * Q + q) * sstep[p]);
+        }
     };
 
     // The sums start from the bias.
@@ -169,86 +175,91 @@ __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsign
     }
 
 #pragma unroll
-    for (int t = 0; t < STAGES - 1; ++t)
+    for (int t = 0; t < STAGES; ++t)
 #pragma unroll
-        for (int c = 0; c < PER; ++c)
+        for (int c = 0; c < (t < STAGES - 1 ? PER : EARLY); ++c)
             issue1(t, c);
 
-    // Half j of a K tile: blocks 2 j (lanes 0 .. 31) and 2 j + 1 of each row.
-    const int key = (l32 >> 2) & 3;
-    const int arow = wm * (BM / 2) + l32, brow = BM + wn * (BN / 2) + l32;
-    auto frag1 = [&](int t, int j, int k, i32x4_t (&a)[FM], i32x4_t (&b)[FN]) {
-        const unsigned char *s = smem + (t & (STAGES - 1)) * STAGE + (((2 * j + half) ^ key) * 16);
+    // Step h of a K tile takes blocks 2 h (lanes 0 .. 31) and 2 h + 1 of each row.
+    const int arow = wm * (BM / 2) + l32, brow = BM + wn * (BN / 2) + l32, k32 = key(l32);
+    i32x4_t a[2][FM], b[2][FN];
+    auto frag1 = [&](int t, int h, int k) {
+        const unsigned char *s = smem + (t & (STAGES - 1)) * STAGE + (((2 * h + half) ^ k32) * 16);
         if (k < FN)
-            b[k] = *(const i32x4_t *)(s + (brow + k * 32) * 64);
+            b[h & 1][k] = *(const i32x4_t *)(s + (brow + k * 32) * (C * 16));
         else
-            a[k - FN] = *(const i32x4_t *)(s + (arow + (k - FN) * 32) * 64);
+            a[h & 1][k - FN] = *(const i32x4_t *)(s + (arow + (k - FN) * 32) * (C * 16));
     };
-    auto scale1 = [&](int t, int k, unsigned (&a)[FM], unsigned (&b)[FN]) {
-        const unsigned char *s = smem + (t & (STAGES - 1)) * STAGE + CODES;
+    unsigned wa[Q][FM], wb[Q][FN];
+    auto scale1 = [&](int t, int q, int k) {
+        const unsigned char *s = smem + (t & (STAGES - 1)) * STAGE + CODES + q * ROWS * 4;
         if (k < FN)
-            b[k] = *(const unsigned *)(s + (brow + k * 32) * 4);
+            wb[q][k] = *(const unsigned *)(s + (brow + k * 32) * 4);
         else
-            a[k - FN] = *(const unsigned *)(s + (arow + (k - FN) * 32) * 4);
+            wa[q][k - FN] = *(const unsigned *)(s + (arow + (k - FN) * 32) * 4);
     };
 
-    // While the products of one half run, the other half's operands are read
-    // and the copies of the tile STAGES - 1 ahead are issued, a few
-    // instructions in the shadow of each product (32 cycles); the order is
-    // fixed here, as a run of reads or copies without products between them
-    // leaves the matrix unit idle.
+    // While the products of one step run, the next step's operands are read
+    // and copies are issued, a few instructions in the shadow of each product
+    // (32 cycles); the order is fixed here, as a run of reads or copies
+    // without products between them leaves the matrix unit idle.  One barrier
+    // a K tile, after the first product of its last step: tile t has been
+    // read by then and tile t + 1 has landed; the copies of tile t + STAGES
+    // follow it, the second half of them in the next step.
     constexpr int NM = FM * FN, FR = FM + FN;
-    i32x4_t a0[FM], b0[FN], a1[FM], b1[FN];
-    unsigned ra0[FM], rb0[FN];
-    int sa[FM], sb[FN];
-    mx_wait_vm<(STAGES - 2) * PER>();
+    mx_wait_vm<(STAGES - 2) * PER + EARLY>();
     mx_barrier();
 #pragma unroll
     for (int k = 0; k < FR; ++k) {
-        frag1(0, 0, k, a0, b0);
-        scale1(0, k, ra0, rb0);
+        frag1(0, 0, k);
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+            scale1(0, q, k);
     }
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
     int t = 0;
-    do {      // quads > 0
+    do {      // nk > 0
+        int sa[Q][FM], sb[Q][FN];
 #pragma unroll
-        for (int i = 0; i < FM; ++i)
-            sa[i] = (int)(ra0[i] >> (8 * half));
+        for (int q = 0; q < Q; ++q) {
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
-            sb[j] = (int)(rb0[j] >> (8 * half));
+            for (int i = 0; i < FM; ++i)
+                sa[q][i] = (int)(wa[q][i] >> (8 * half));
 #pragma unroll
-        for (int m = 0; m < NM; ++m) {
-            acc[m / FN][m % FN] = mx_mfma32<0>(b0[m % FN], a0[m / FN], acc[m / FN][m % FN], sb[m % FN], sa[m / FN]);
-            // copies: into the stage of tile t - 1, which every wave has read
-#pragma unroll
-            for (int k = m * (FR + PER) / NM; k < (m + 1) * (FR + PER) / NM; ++k)
-                if (k < FR)
-                    frag1(t, 1, k, a1, b1);
-                else
-                    issue1(t + STAGES - 1, k - FR);
-            __builtin_amdgcn_sched_barrier(0);
+            for (int j = 0; j < FN; ++j)
+                sb[q][j] = (int)(wb[q][j] >> (8 * half));
         }
 #pragma unroll
-        for (int m = 0; m < NM; ++m) {
-            acc[m / FN][m % FN] = mx_mfma32<2>(b1[m % FN], a1[m / FN], acc[m / FN][m % FN], sb[m % FN], sa[m / FN]);
-            if (m == 0) {
-                mx_wait_vm<(STAGES - 2) * PER>();      // tile t + 1 has landed
-                mx_wait_lds();                         // tile t has been read
-                mx_barrier();
-            }
-            constexpr int SPAN = NM >= 16 ? NM - 4 : NM;      // the last reads return before they are needed
+        for (int h = 0; h < H; ++h) {
+            const bool last = h == H - 1;
+            const int reads = last ? FR * (1 + Q) : FR;
+            const int copies = h == 0 ? PER - EARLY : last ? EARLY : 0;
+            const int pieces = reads + copies;
 #pragma unroll
-            for (int k = m * 2 * FR / SPAN; k < (m + 1) * 2 * FR / SPAN && k < 2 * FR; ++k)
-                if (k < FR)
-                    frag1(t + 1, 0, k, a0, b0);
-                else
-                    scale1(t + 1, k - FR, ra0, rb0);
-            __builtin_amdgcn_sched_barrier(0);
+            for (int m = 0; m < NM; ++m) {
+                const int i = m / FN, j = m % FN;
+                acc[i][j] = h & 1 ? mx_mfma32<2>(b[1][j], a[1][i], acc[i][j], sb[h / 2][j], sa[h / 2][i])
+                                  : mx_mfma32<0>(b[0][j], a[0][i], acc[i][j], sb[h / 2][j], sa[h / 2][i]);
+                if (last && m == 0) {
+                    mx_wait_vm<(STAGES - 2) * PER>();
+                    mx_wait_lds();
+                    mx_barrier();
+                }
+#pragma unroll
+                for (int k = m * pieces / NM; k < (m + 1) * pieces / NM; ++k) {
+                    if (k < FR)
+                        frag1(last ? t + 1 : t, last ? 0 : h + 1, k);
+                    else if (k < reads)
+                        scale1(t + 1, (k - FR) / FR, (k - FR) % FR);
+                    else
+                        issue1(h == 0 ? t + STAGES - 1 : t + STAGES, k - reads + (h == 0 ? EARLY : 0));
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
         // (a fence: the compiler would sink the reads to the next iteration)
         __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    } while (++t < quads);
+    } while (++t < nk);
 
     // Rows of the output through LDS, 32 at a time and wave, so that stores
     // are 16 bytes a lane along the row.
@@ -300,13 +311,13 @@ __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsign
     }
 }
 
-template <int BM, int BN, int STAGES, typename O>
+template <int BM, int BN, int BK, int STAGES, typename O>
 __global__ __launch_bounds__(kMxThreads) void mx_gemm_tile(MxGemmArgs g)
 {
-    __shared__ __attribute__((aligned(16))) unsigned char smem[mx_gemm_lds<BM, BN, STAGES, sizeof(typename O::raw)>()];
+    __shared__ __attribute__((aligned(16))) unsigned char smem[mx_gemm_lds<BM, BN, BK, STAGES, sizeof(typename O::raw)>()];
     const unsigned id = mx_xcd_tile(blockIdx.x, gridDim.x);
     if (id < (unsigned)g.tm * g.tn)
-        mx_gemm_body<BM, BN, STAGES, O>(g, id, smem);
+        mx_gemm_body<BM, BN, BK, STAGES, O>(g, id, smem);
 }
 
 // Column sums from partial sums [parts][cols], 64 columns a workgroup.
@@ -333,19 +344,19 @@ __device__ __forceinline__ void mx_sum_parts(const MxSumArgs &a, unsigned block,
 // Both products of the backward pass and the sums of db in one launch; the
 // first `dw_blocks` workgroups take dw's tiles (fp32), the next `dx_blocks`
 // those of dx, the others 64 columns of db each.
-template <int BM, int BN, int STAGES, typename O>
+template <int BM, int BN, int BK, int STAGES, typename O>
 __global__ __launch_bounds__(kMxThreads) void mx_gemm_bwd(MxGemmArgs dw, MxGemmArgs dx, MxSumArgs db,
                                                           unsigned dw_blocks, unsigned dx_blocks)
 {
-    __shared__ __attribute__((aligned(16))) unsigned char smem[mx_gemm_lds<BM, BN, STAGES, 4>()];
+    __shared__ __attribute__((aligned(16))) unsigned char smem[mx_gemm_lds<BM, BN, BK, STAGES, 4>()];
     if (blockIdx.x < dw_blocks) {
         const unsigned id = mx_xcd_tile(blockIdx.x, dw_blocks);
         if (id < (unsigned)dw.tm * dw.tn)
-            mx_gemm_body<BM, BN, STAGES, Fp32>(dw, id, smem);
+            mx_gemm_body<BM, BN, BK, STAGES, Fp32>(dw, id, smem);
     } else if (blockIdx.x < dw_blocks + dx_blocks) {
         const unsigned id = mx_xcd_tile(blockIdx.x - dw_blocks, dx_blocks);
         if (id < (unsigned)dx.tm * dx.tn)
-            mx_gemm_body<BM, BN, STAGES, O>(dx, id, smem);
+            mx_gemm_body<BM, BN, BK, STAGES, O>(dx, id, smem);
     } else {
         mx_sum_parts(db, blockIdx.x - dw_blocks - dx_blocks, (float *)smem);
     }
