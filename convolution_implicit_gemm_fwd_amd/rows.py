@@ -6,6 +6,10 @@ contiguous and the rows evenly spaced (any NHWC tensor, or a column slice of
 a matrix).  Calls run on ``stream`` (default: torch's current stream of the
 first tensor's device) without waiting; torch supplies device memory and the
 stream only.
+
+A small call costs the host more than the GPU (a launch is about 4 us, the
+kernel of one 4096-wide token 2 us), so the functions here look each thing up
+once and call the C entry points directly.
 """
 from __future__ import annotations
 
@@ -24,13 +28,25 @@ class Mxfp4Tensor(NamedTuple):
     cols: int
 
 
-_codes = {}
+_torch = None
+
+
+def _setup():
+    """torch, the loaded library and what every call takes from them."""
+    global _torch, _lib, _codes, _f32, _u8, _device, _stream
+    import torch
+
+    _lib = abi.load()
+    _codes = {torch.bfloat16: CONVIMG_BF16, torch.float32: CONVIMG_FP32, torch.float16: CONVIMG_FP16}
+    _f32, _u8 = torch.float32, torch.uint8
+    _device = torch.cuda.current_device
+    # the current stream's handle: the raw getter, where torch has it, makes no Stream object (0.1 us, not 1.9)
+    _stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) \
+        or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _torch = torch
 
 
 def _dtype(t, what):
-    if not _codes:
-        import torch
-        _codes.update({torch.bfloat16: CONVIMG_BF16, torch.float32: CONVIMG_FP32, torch.float16: CONVIMG_FP16})
     c = _codes.get(t)
     if c is None:
         raise TypeError("%s must be bfloat16, float16 or float32" % what)
@@ -67,60 +83,45 @@ def _rows_of(t, what):
     return rows, cols, ld
 
 
-def _param(t, cols, like, what):
-    import torch
-
+def _param(t, n, device, what):
+    """The address of a float32 vector of n values, None for None."""
     if t is None:
         return None
-    if t.dtype != torch.float32 or t.device != like.device or t.dim() != 1 or t.shape[0] != cols \
-            or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous float32 tensor of %d values on the input's device" % (what, cols))
+    if t.dtype is not _f32 or t.device != device or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous float32 tensor of %d values on the input's device" % (what, n))
     return t.data_ptr()
 
 
-class _Call:
-    """The device and stream of one call, and the buffers it allocates."""
+def _like(t, dtype):
+    """An uninitialised contiguous tensor of t's shape."""
+    if t.is_contiguous():
+        return _torch.empty_like(t, dtype=dtype)
+    return t.new_empty(t.shape, dtype=dtype)
 
-    def __init__(self, t, stream):
-        import torch
 
-        self.torch, self.device = torch, t.device
-        self.current = torch.cuda.current_stream(t.device).cuda_stream
-        self.stream = self.current if stream is None else stream
-        self.fresh = []
+def _elsewhere(device, f, *args):
+    """The call with the tensors' device made the current one."""
+    with _torch.cuda.device(device):
+        return f(*args)
 
-    def empty(self, shape, dtype):
-        t = self.torch.empty(shape, dtype=dtype, device=self.device)
-        if self.stream != self.current:
-            self.fresh.append(t)
-        return t
 
-    def run(self, fn, *args):
-        torch = self.torch
-        if torch.cuda.current_device() == self.device.index:
-            rc = fn(*args, self.stream)
-        else:
-            with torch.cuda.device(self.device):
-                rc = fn(*args, self.stream)
-        if rc != 0:
-            raise RuntimeError("%s failed: %s (status %d)" % (fn.__name__, abi.conv2d_strerror(rc), rc))
-        if self.fresh:
-            # allocated on torch's current stream, used on another: the
-            # allocator must not hand the memory out before that stream is done
-            ext = torch.cuda.ExternalStream(self.stream, device=self.device)
-            for t in self.fresh:
+def _fail(name, rc):
+    raise RuntimeError("%s failed: %s (status %d)" % (name, abi.conv2d_strerror(rc), rc))
+
+
+def _hold(device, stream, *tensors):
+    """Tensors allocated on torch's current stream and used on another: the
+    allocator must not hand the memory out before that stream is done."""
+    if stream != _stream(device.index):
+        ext = _torch.cuda.ExternalStream(stream, device=device)
+        for t in tensors:
+            if t is not None:
                 t.record_stream(ext)
 
 
-def _check(rc, what):
-    if rc != 0:
-        raise RuntimeError("%s failed: %s (status %d)" % (what, abi.conv2d_strerror(rc), rc))
-
-
-def _same_device(like, **tensors):
-    for name, t in tensors.items():
-        if t.device != like.device:
-            raise ValueError("%s must be on the device of the other tensors" % name)
+def _same_device(device, t, what):
+    if t.device != device:
+        raise ValueError("%s must be on the device of the other tensors" % what)
 
 
 def layer_norm_nhwc(x, gamma=None, beta=None, eps=1e-5, out_dtype=None, stats=False, stream=None):
@@ -131,36 +132,54 @@ def layer_norm_nhwc(x, gamma=None, beta=None, eps=1e-5, out_dtype=None, stats=Fa
     with ``stats`` (y, mean, rstd), the float32 row statistics that
     ``layer_norm_bwd_nhwc`` takes, of x's shape without the last dimension.
     """
+    if _torch is None:
+        _setup()
     rows, cols, ld = _rows_of(x, "x")
-    out_dtype = x.dtype if out_dtype is None else out_dtype
+    dev = x.device
+    if _device() != dev.index:
+        return _elsewhere(dev, layer_norm_nhwc, x, gamma, beta, eps, out_dtype, stats, stream)
+    if out_dtype is None:
+        out_dtype = x.dtype
     xd, yd = _dtype(x.dtype, "x"), _dtype(out_dtype, "out_dtype")
-    g, b = _param(gamma, cols, x, "gamma"), _param(beta, cols, x, "beta")
-    c = _Call(x, stream)
-    y = c.empty(x.shape, out_dtype)
-    mean = rstd = None
+    g, b = _param(gamma, cols, dev, "gamma"), _param(beta, cols, dev, "beta")
+    y = _like(x, out_dtype)
+    mean = rstd = mp = rp = None
     if stats:
-        mean, rstd = c.empty(x.shape[:-1], c.torch.float32), c.empty(x.shape[:-1], c.torch.float32)
-    c.run(abi.layer_norm_fwd, x.data_ptr(), ld, g, b, rows, cols, eps, xd, yd, y.data_ptr(),
-          mean.data_ptr() if stats else None, rstd.data_ptr() if stats else None)
+        mean, rstd = x.new_empty(x.shape[:-1], dtype=_f32), x.new_empty(x.shape[:-1], dtype=_f32)
+        mp, rp = mean.data_ptr(), rstd.data_ptr()
+    rc = _lib.layer_norm_fwd(x.data_ptr(), ld, g, b, rows, cols, eps, xd, yd, y.data_ptr(), mp, rp,
+                             _stream(dev.index) if stream is None else stream)
+    if rc:
+        _fail("layer_norm_fwd", rc)
+    if stream is not None:
+        _hold(dev, stream, y, mean, rstd)
     return (y, mean, rstd) if stats else y
 
 
-def _packed(c, rows, cols):
+def _packed(like, rows, cols):
     nb = -(-cols // 32)
-    return Mxfp4Tensor(c.empty((rows, nb * 16), c.torch.uint8), c.empty((-(-nb // 4), rows, 4), c.torch.uint8),
+    return Mxfp4Tensor(like.new_empty((rows, nb * 16), dtype=_u8), like.new_empty((-(-nb // 4), rows, 4), dtype=_u8),
                        rows, cols)
 
 
 def layer_norm_mxfp4_nhwc(x, gamma=None, beta=None, eps=1e-5, stream=None):
     """layer_norm_nhwc with its result quantised to MXFP4 rows: an
     ``Mxfp4Tensor``, the input of ``mxfp4_linear_nhwc``."""
+    if _torch is None:
+        _setup()
     rows, cols, ld = _rows_of(x, "x")
+    dev = x.device
+    if _device() != dev.index:
+        return _elsewhere(dev, layer_norm_mxfp4_nhwc, x, gamma, beta, eps, stream)
     xd = _dtype(x.dtype, "x")
-    g, b = _param(gamma, cols, x, "gamma"), _param(beta, cols, x, "beta")
-    c = _Call(x, stream)
-    q = _packed(c, rows, cols)
-    c.run(abi.layer_norm_fwd_mxfp4, x.data_ptr(), ld, g, b, rows, cols, eps, xd, q.codes.data_ptr(),
-          q.scales.data_ptr(), None, None)
+    g, b = _param(gamma, cols, dev, "gamma"), _param(beta, cols, dev, "beta")
+    q = _packed(x, rows, cols)
+    rc = _lib.layer_norm_fwd_mxfp4(x.data_ptr(), ld, g, b, rows, cols, eps, xd, q.codes.data_ptr(),
+                                   q.scales.data_ptr(), None, None, _stream(dev.index) if stream is None else stream)
+    if rc:
+        _fail("layer_norm_fwd_mxfp4", rc)
+    if stream is not None:
+        _hold(dev, stream, q.codes, q.scales)
     return q
 
 
@@ -171,54 +190,84 @@ def layer_norm_bwd_nhwc(dy, x, gamma, mean, rstd, dx_dtype=None, stream=None):
     float32 [C] or None; mean, rstd: the forward's statistics.  dx: contiguous,
     in ``dx_dtype`` (default: x's dtype); dgamma and dbeta: float32 [C].
     """
+    if _torch is None:
+        _setup()
     rows, cols, ld = _rows_of(x, "x")
+    dev = x.device
     if dy.shape != x.shape:
         raise ValueError("dy must have x's shape")
-    _, _, ldy = _rows_of(dy, "dy")
-    _same_device(x, dy=dy)
-    dx_dtype = x.dtype if dx_dtype is None else dx_dtype
+    ldy = _rows_of(dy, "dy")[2]
+    _same_device(dev, dy, "dy")
+    if _device() != dev.index:
+        return _elsewhere(dev, layer_norm_bwd_nhwc, dy, x, gamma, mean, rstd, dx_dtype, stream)
+    if dx_dtype is None:
+        dx_dtype = x.dtype
     dd, xd, od = _dtype(dy.dtype, "dy"), _dtype(x.dtype, "x"), _dtype(dx_dtype, "dx_dtype")
-    g = _param(gamma, cols, x, "gamma")
-    m, r = _param(mean.reshape(-1), rows, x, "mean"), _param(rstd.reshape(-1), rows, x, "rstd")
-    c = _Call(x, stream)
+    g = _param(gamma, cols, dev, "gamma")
+    m = _param(mean if mean.dim() == 1 else mean.reshape(-1), rows, dev, "mean")
+    r = _param(rstd if rstd.dim() == 1 else rstd.reshape(-1), rows, dev, "rstd")
     rc, need = abi.layer_norm_bwd_workspace(rows, cols)
-    _check(rc, "layer_norm_bwd_workspace")
-    f32 = c.torch.float32
-    dx, dgamma, dbeta = c.empty(x.shape, dx_dtype), c.empty((cols,), f32), c.empty((cols,), f32)
-    ws = c.empty((need,), c.torch.uint8)
-    c.run(abi.layer_norm_bwd, dy.data_ptr(), ldy, x.data_ptr(), ld, g, m, r, rows, cols, dd, xd, od, dx.data_ptr(),
-          dgamma.data_ptr(), dbeta.data_ptr(), ws.data_ptr(), need)
+    if rc:
+        _fail("layer_norm_bwd_workspace", rc)
+    dx = _like(x, dx_dtype)
+    dgamma, dbeta = x.new_empty((cols,), dtype=_f32), x.new_empty((cols,), dtype=_f32)
+    ws = x.new_empty((need,), dtype=_u8)
+    rc = _lib.layer_norm_bwd(dy.data_ptr(), ldy, x.data_ptr(), ld, g, m, r, rows, cols, dd, xd, od, dx.data_ptr(),
+                             dgamma.data_ptr(), dbeta.data_ptr(), ws.data_ptr(), need,
+                             _stream(dev.index) if stream is None else stream)
+    if rc:
+        _fail("layer_norm_bwd", rc)
+    if stream is not None:
+        _hold(dev, stream, dx, dgamma, dbeta, ws)
     return dx, dgamma, dbeta
 
 
 def mxfp4_quantize_nhwc(x, transpose=False, stream=None):
     """x [..., C] as MXFP4 rows (an ``Mxfp4Tensor``); ``transpose``: the rows of
     its transpose, so that blocks of 32 run down the columns of x."""
+    if _torch is None:
+        _setup()
     rows, cols, ld = _rows_of(x, "x")
+    dev = x.device
+    if _device() != dev.index:
+        return _elsewhere(dev, mxfp4_quantize_nhwc, x, transpose, stream)
     xd = _dtype(x.dtype, "x")
-    c = _Call(x, stream)
-    q = _packed(c, cols, rows) if transpose else _packed(c, rows, cols)
-    c.run(abi.mxfp4_quantize, x.data_ptr(), ld, rows, cols, xd, 1 if transpose else 0, q.codes.data_ptr(),
-          q.scales.data_ptr())
+    q = _packed(x, cols, rows) if transpose else _packed(x, rows, cols)
+    rc = _lib.mxfp4_quantize(x.data_ptr(), ld, rows, cols, xd, 1 if transpose else 0, q.codes.data_ptr(),
+                             q.scales.data_ptr(), _stream(dev.index) if stream is None else stream)
+    if rc:
+        _fail("mxfp4_quantize", rc)
+    if stream is not None:
+        _hold(dev, stream, q.codes, q.scales)
     return q
 
 
 def _check_packed(q, what):
-    import torch
-
-    nb = -(-q.cols // 32)
-    for t, shape in ((q.codes, (q.rows, nb * 16)), (q.scales, (-(-nb // 4), q.rows, 4))):
-        if t.dtype != torch.uint8 or not t.is_cuda or tuple(t.shape) != shape or not t.is_contiguous():
-            raise ValueError("%s is not a packed operand of %d rows and %d columns" % (what, q.rows, q.cols))
+    codes, scales, rows, cols = q
+    nb = -(-cols // 32)
+    if codes.dtype is not _u8 or scales.dtype is not _u8 or not codes.is_cuda or codes.device != scales.device \
+            or codes.shape != (rows, nb * 16) or scales.shape != (-(-nb // 4), rows, 4) \
+            or not codes.is_contiguous() or not scales.is_contiguous():
+        raise ValueError("%s is not a packed operand of %d rows and %d columns" % (what, rows, cols))
 
 
 def mxfp4_dequantize_nhwc(q, dtype, stream=None):
     """The values [rows, cols] that packed rows stand for, in ``dtype``."""
+    if _torch is None:
+        _setup()
     _check_packed(q, "q")
     d = _dtype(dtype, "dtype")
-    c = _Call(q.codes, stream)
-    out = c.empty((q.rows, q.cols), dtype)
-    c.run(abi.mxfp4_dequantize, q.codes.data_ptr(), q.scales.data_ptr(), q.rows, q.cols, d, out.data_ptr())
+    codes, scales, rows, cols = q
+    dev = codes.device
+    if _device() != dev.index:
+        return _elsewhere(dev, mxfp4_dequantize_nhwc, q, dtype, stream)
+    out = codes.new_empty((rows, cols), dtype=dtype)
+    rc = _lib.mxfp4_dequantize(codes.data_ptr(), scales.data_ptr(), rows, cols, d, out.data_ptr(),
+                               _stream(dev.index) if stream is None else stream)
+    if rc:
+        _fail("mxfp4_dequantize", rc)
+    if stream is not None:
+        _hold(dev, stream, out)
     return out
 
 
@@ -230,32 +279,41 @@ def mxfp4_linear_nhwc(x, w, bias=None, out_dtype=None, stream=None):
     columns; w: an ``Mxfp4Tensor`` of N rows and K columns; bias: float32 [N] or
     None.  out: contiguous, in ``out_dtype`` (default: x's dtype, bfloat16 for packed x).
     """
+    if _torch is None:
+        _setup()
     _check_packed(w, "w")
-    like = w.codes
-    c = _Call(like, stream)
-    torch = c.torch
+    codes, scales, N, wk = w
+    dev = codes.device
+    if _device() != dev.index:
+        return _elsewhere(dev, mxfp4_linear_nhwc, x, w, bias, out_dtype, stream)
     if isinstance(x, Mxfp4Tensor):
         _check_packed(x, "x")
-        M, K, ld, xd, shape = x.rows, x.cols, x.cols, CONVIMG_MXFP4, (x.rows,)
-        xp, sp = x.codes.data_ptr(), x.scales.data_ptr()
-        _same_device(like, x=x.codes)
-        out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
+        xc, xs, M, K = x
+        _same_device(dev, xc, "x")
+        if out_dtype is None:
+            out_dtype = _torch.bfloat16
+        ld, xd, xp, sp, shape = K, CONVIMG_MXFP4, xc.data_ptr(), xs.data_ptr(), (M, N)
     else:
         M, K, ld = _rows_of(x, "x")
-        xd, shape, xp, sp = _dtype(x.dtype, "x"), x.shape[:-1], x.data_ptr(), None
-        _same_device(like, x=x)
-        out_dtype = x.dtype if out_dtype is None else out_dtype
-    if K != w.cols:
-        raise ValueError("x has %d columns, w %d" % (K, w.cols))
-    N = w.rows
+        _same_device(dev, x, "x")
+        xd, xp, sp, shape = _dtype(x.dtype, "x"), x.data_ptr(), None, (*x.shape[:-1], N)
+        if out_dtype is None:
+            out_dtype = x.dtype
+    if K != wk:
+        raise ValueError("x has %d columns, w %d" % (K, wk))
     od = _dtype(out_dtype, "out_dtype")
-    b = _param(bias, N, like, "bias")
+    b = _param(bias, N, dev, "bias")
     rc, need = abi.mxfp4_linear_workspace(M, N, K, xd)
-    _check(rc, "mxfp4_linear_workspace")
-    out = c.empty((*shape, N), out_dtype)
-    ws = c.empty((need,), torch.uint8) if need else None
-    c.run(abi.mxfp4_linear_fwd, xp, ld, sp, xd, like.data_ptr(), w.scales.data_ptr(), b, M, N, K, od, out.data_ptr(),
-          ws.data_ptr() if need else None, need)
+    if rc:
+        _fail("mxfp4_linear_workspace", rc)
+    out = codes.new_empty(shape, dtype=out_dtype)
+    ws = codes.new_empty((need,)) if need else None
+    rc = _lib.mxfp4_linear_fwd(xp, ld, sp, xd, codes.data_ptr(), scales.data_ptr(), b, M, N, K, od, out.data_ptr(),
+                               ws.data_ptr() if need else None, need, _stream(dev.index) if stream is None else stream)
+    if rc:
+        _fail("mxfp4_linear_fwd", rc)
+    if stream is not None:
+        _hold(dev, stream, out, ws)
     return out
 
 
@@ -266,22 +324,34 @@ def mxfp4_linear_bwd_nhwc(dy, x, w, dx_dtype=None, stream=None):
     before quantisation, of one dtype.  dx: x's shape in ``dx_dtype`` (default:
     x's dtype); dw: float32 [N, K]; db: float32 [N].
     """
+    if _torch is None:
+        _setup()
     M, N, ldy = _rows_of(dy, "dy")
     mx, K, ldx = _rows_of(x, "x")
-    if w.dim() != 2 or mx != M or dy.shape[:-1] != x.shape[:-1] or tuple(w.shape) != (N, K):
+    if w.dim() != 2 or mx != M or dy.shape[:-1] != x.shape[:-1] or w.shape != (N, K):
         raise ValueError("dy must be [..., N], x [..., K] and w [N, K]")
     if x.dtype != w.dtype:
         raise TypeError("x and w must have one dtype")
-    _, _, ldw = _rows_of(w, "w")
-    _same_device(dy, x=x, w=w)
-    dx_dtype = x.dtype if dx_dtype is None else dx_dtype
+    ldw = _rows_of(w, "w")[2]
+    dev = dy.device
+    _same_device(dev, x, "x")
+    _same_device(dev, w, "w")
+    if _device() != dev.index:
+        return _elsewhere(dev, mxfp4_linear_bwd_nhwc, dy, x, w, dx_dtype, stream)
+    if dx_dtype is None:
+        dx_dtype = x.dtype
     dd, xd, od = _dtype(dy.dtype, "dy"), _dtype(x.dtype, "x"), _dtype(dx_dtype, "dx_dtype")
     rc, need = abi.mxfp4_linear_bwd_workspace(M, N, K)
-    _check(rc, "mxfp4_linear_bwd_workspace")
-    c = _Call(dy, stream)
-    f32 = c.torch.float32
-    dx, dw, db = c.empty(x.shape, dx_dtype), c.empty((N, K), f32), c.empty((N,), f32)
-    ws = c.empty((need,), c.torch.uint8)
-    c.run(abi.mxfp4_linear_bwd, dy.data_ptr(), ldy, dd, x.data_ptr(), ldx, w.data_ptr(), ldw, xd, M, N, K, od,
-          dx.data_ptr(), dw.data_ptr(), db.data_ptr(), ws.data_ptr(), need)
+    if rc:
+        _fail("mxfp4_linear_bwd_workspace", rc)
+    dx = _like(x, dx_dtype)
+    dw, db = dy.new_empty((N, K), dtype=_f32), dy.new_empty((N,), dtype=_f32)
+    ws = dy.new_empty((need,), dtype=_u8)
+    rc = _lib.mxfp4_linear_bwd(dy.data_ptr(), ldy, dd, x.data_ptr(), ldx, w.data_ptr(), ldw, xd, M, N, K, od,
+                               dx.data_ptr(), dw.data_ptr(), db.data_ptr(), ws.data_ptr(), need,
+                               _stream(dev.index) if stream is None else stream)
+    if rc:
+        _fail("mxfp4_linear_bwd", rc)
+    if stream is not None:
+        _hold(dev, stream, dx, dw, db, ws)
     return dx, dw, db
