@@ -42,8 +42,6 @@ struct LnFwdArgs {
     float eps;
 };
 
-struct Mx4 {};
-
 // Writes eight normalised values of a row: of type Y, or as MXFP4 (four
 // neighbouring lanes hold one block; all of them reach this together).
 template <typename Y>

@@ -17,7 +17,7 @@
 // Sums are fp32.
 #include <type_traits>
 
-#include "mxfp4_gemm.hpp"
+#include "mxfp4_few.hpp"
 
 namespace convimg {
 
@@ -69,19 +69,29 @@ void quantize_cols(const void *x, long long ldx, int rows, int cols, int dtype, 
     });
 }
 
-long long tile_count(int M, int N, int t) { return (long long)((M + t - 1) / t) * ((N + t - 1) / t); }
+long long tile_count(int M, int N, int bm, int bn) { return (long long)((M + bm - 1) / bm) * ((N + bn - 1) / bn); }
 
-// Calls f with the tile edge for a launch whose tiles of an edge number
-// count(edge): the largest that still gives most CUs one.
+// Calls f with the shape for a launch that has count(BM, BN) tiles, rows of
+// the output (the most of any product in it) and kb blocks along K.  The
+// largest square tile that still gives most CUs one; else, where there are
+// few rows, tiles of as few; K tiles of 128 in small tiles (those of 256 take
+// whole cache lines, but hide less of the latency such launches consist of)
+// and groups of waves along a long K.
 template <typename C, typename F>
-void with_tile(C &&count, F &&f)
+void with_shape(C &&count, int rows, int kb, F &&f)
 {
-    if (count(256) >= 192)
-        f(std::integral_constant<int, 256>{});
-    else if (count(128) >= 192)
-        f(std::integral_constant<int, 128>{});
+    if (count(256, 256) >= 192)
+        f(GemmShape<256, 256, 2, 2, 256, 2, 1>{});
+    else if (count(128, 128) >= 192)
+        f(GemmShape<128, 128, 2, 2, 256, 2, 1>{});
+    else if (rows <= 32 && kb > 16)
+        f(GemmShape<32, 32, 1, 1, 256, 2, 8>{});
+    else if (rows <= 64 && kb > 16)
+        f(GemmShape<64, 32, 2, 1, 256, 2, 4>{});
+    else if (count(64, 64) > 512 || kb <= 16)
+        f(GemmShape<64, 64, 2, 2, 128, 4, 1>{});
     else
-        f(std::integral_constant<int, 64>{});
+        f(GemmShape<64, 64, 2, 2, 128, 4, 4>{});
 }
 
 MxGemmArgs gemm_args(MxOperand a, MxOperand b, const float *bias, int M, int N, int K, void *out)
@@ -89,20 +99,36 @@ MxGemmArgs gemm_args(MxOperand a, MxOperand b, const float *bias, int M, int N, 
     return {a.codes, b.codes, a.scales, b.scales, bias, out, M, N, mx_blocks(K), 0, 0};
 }
 
-unsigned gemm_grid(MxGemmArgs &g, int tile)
+unsigned gemm_grid(MxGemmArgs &g, int bm, int bn)
 {
-    g.tm = (g.M + tile - 1) / tile;
-    g.tn = (g.N + tile - 1) / tile;
+    g.tm = (g.M + bm - 1) / bm;
+    g.tn = (g.N + bn - 1) / bn;
     return eights((long long)g.tm * g.tn);
 }
 
 void gemm(MxGemmArgs g, int out_dtype, hipStream_t stream)
 {
     with_dtype(out_dtype, [&](auto o) {
-        with_tile([&](int t) { return tile_count(g.M, g.N, t); }, [&](auto tile) {
-            constexpr int T = decltype(tile)::value;
-            const unsigned grid = gemm_grid(g, T);
-            hipLaunchKernelGGL((mx_gemm_tile<T, T, 256, 2, decltype(o)>), dim3(grid), dim3(kMxThreads), 0, stream, g);
+        with_shape([&](int bm, int bn) { return tile_count(g.M, g.N, bm, bn); }, g.M, g.kb, [&](auto shape) {
+            typedef decltype(shape) S;
+            const unsigned grid = gemm_grid(g, S::BM, S::BN);
+            hipLaunchKernelGGL((mx_gemm_tile<S, decltype(o)>), dim3(grid), dim3(S::threads), 0, stream, g);
+        });
+    });
+}
+
+// Dense rows that the product's workgroups quantise for themselves: one
+// launch in place of two, while that costs each workgroup little.
+bool few_dense(int M, int K) { return M <= kMxFewM && (long long)M * K <= kMxFewSize; }
+
+void gemm_few(const MxFewArgs &g, int x_dtype, int out_dtype, hipStream_t stream)
+{
+    // a wave for every pair of scale dwords, up to eight
+    const int pairs = (g.kb + 7) / 8, waves = pairs < kMxFewWaves ? pairs : kMxFewWaves;
+    with_dtype(x_dtype, [&](auto x) {
+        with_dtype(out_dtype, [&](auto o) {
+            hipLaunchKernelGGL((mx_gemm_few<decltype(x), decltype(o)>), dim3((g.N + 15) / 16), dim3(waves * 64), 0,
+                               stream, g);
         });
     });
 }
@@ -254,7 +280,7 @@ int mxfp4_linear_workspace(int M, int N, int K, int x_dtype, size_t *bytes)
         return rc;
     if (x_dtype != CONVIMG_MXFP4 && !dtype_ok(x_dtype))
         return CONVIMG_ERR_DTYPE;
-    *bytes = x_dtype == CONVIMG_MXFP4 ? 0 : packed_bytes(M, K);
+    *bytes = x_dtype == CONVIMG_MXFP4 || few_dense(M, K) ? 0 : packed_bytes(M, K);
     return CONVIMG_OK;
 }
 
@@ -291,6 +317,10 @@ int mxfp4_linear_fwd(const void *x, long long ldx, const void *x_scales, int x_d
         return CONVIMG_ERR_ALIAS;
     MxOperand a = {(const unsigned char *)x, (const unsigned char *)x_scales};
     const MxOperand b = {(const unsigned char *)w_codes, (const unsigned char *)w_scales};
+    if (dense && need == 0) {
+        gemm_few({x, b.codes, b.scales, bias, out, ldx, M, N, K, mx_blocks(K)}, x_dtype, out_dtype, stream);
+        return launched();
+    }
     if (dense) {
         unsigned char *c = (unsigned char *)ws, *s = c + align256(mx_code_bytes(M, K));
         quantize(x, ldx, M, K, x_dtype, c, s, stream);
@@ -377,11 +407,13 @@ int mxfp4_linear_bwd(const void *dy, long long lddy, int dy_dtype, const void *x
     MxGemmArgs g_dx = gemm_args(qdy, qwt, nullptr, M, K, N, dx), g_dw = gemm_args(qdyt, qxt, nullptr, N, K, M, dw);
     const MxSumArgs sum = {part, db, (M + kMxTile - 1) / kMxTile, N};
     with_dtype(dx_dtype, [&](auto o) {
-        with_tile([&](int t) { return tile_count(M, K, t) + tile_count(N, K, t); }, [&](auto tile) {
-            constexpr int T = decltype(tile)::value;
-            const unsigned n_dx = gemm_grid(g_dx, T), n_dw = gemm_grid(g_dw, T), n_db = db ? (N + 63) / 64 : 0;
-            hipLaunchKernelGGL((mx_gemm_bwd<T, T, 256, 2, decltype(o)>), dim3(n_dw + n_dx + n_db), dim3(kMxThreads), 0,
-                               stream, g_dw, g_dx, sum, n_dw, n_dx);
+        auto count = [&](int bm, int bn) { return tile_count(M, K, bm, bn) + tile_count(N, K, bm, bn); };
+        with_shape(count, M > N ? M : N, M > N ? g_dw.kb : g_dx.kb, [&](auto shape) {
+            typedef decltype(shape) S;
+            const unsigned n_dx = gemm_grid(g_dx, S::BM, S::BN), n_dw = gemm_grid(g_dw, S::BM, S::BN),
+                           n_db = db ? (N + 63) / 64 : 0;
+            hipLaunchKernelGGL((mx_gemm_bwd<S, decltype(o)>), dim3(n_dw + n_dx + n_db), dim3(S::threads), 0, stream,
+                               g_dw, g_dx, sum, n_dw, n_dx);
         });
     });
     return launched();

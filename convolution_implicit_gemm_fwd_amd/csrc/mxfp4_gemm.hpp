@@ -74,67 +74,94 @@ __device__ __forceinline__ void mx_tile(const MxGemmArgs &g, int id, int &m, int
     m = group * 8 + in - n * rows;
 }
 
-template <int BM, int BN, int BK, int STAGES, int OS>
+// A kernel's shape: tile, waves along M and N, K tile, stages, groups of waves
+// along K.
+template <int BM_, int BN_, int WM_, int WN_, int BK_, int STAGES_, int KG_>
+struct GemmShape {
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, BK = BK_, STAGES = STAGES_, KG = KG_;
+    // LDS: rows of codes, and scale dwords in slots of 64 rows
+    static constexpr int SLOTS = (BM + 63) / 64 + (BN + 63) / 64;
+    static constexpr int CODES = (BM + BN) * (BK / 2), STAGE = CODES + SLOTS * 256 * (BK / 128);
+    static constexpr int threads = WM * WN * KG * 64;
+};
+
+template <typename S, int OS>
 constexpr int mx_gemm_lds()
 {
-    constexpr int ring = STAGES * (BM + BN) * (BK / 2 + BK / 32), rows = 4 * 32 * (BN / 2 * OS + 16);
+    constexpr int ring = S::KG * S::STAGES * S::STAGE, rows = S::WM * S::WN * 32 * (S::BN / S::WN * OS + 16);
     return ring > rows ? ring : rows;
 }
 
-// BM x BN tiles, four waves 2 x 2, K tiles of BK in a ring of STAGES.
-template <int BM, int BN, int BK, int STAGES, typename O>
+// BM x BN tiles, WM x WN waves, K tiles of BK in a ring of STAGES.  With KG
+// groups of such waves each takes one run of the K tiles, in a ring of its
+// own, and their sums meet in LDS at the end: where there are few output
+// tiles this keeps more copies in flight a CU.
+template <typename S, typename O>
 __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsigned char *smem)
 {
-    constexpr int FM = BM / 64, FN = BN / 64;               // 32 x 32 blocks of a wave
+    constexpr int BM = S::BM, BN = S::BN, BK = S::BK, WM = S::WM, NW = S::WM * S::WN, STAGES = S::STAGES, KG = S::KG;
+    constexpr int TM = BM / S::WM, TN = BN / S::WN;         // a wave's tile
+    constexpr int FM = TM / 32, FN = TN / 32;               // 32 x 32 blocks of a wave
     constexpr int ROWS = BM + BN;
     constexpr int C = BK / 32, Q = BK / 128, H = BK / 64;   // blocks, scale dwords and product steps of a K tile
-    constexpr int CODES = ROWS * C * 16, STAGE = CODES + ROWS * Q * 4;
+    constexpr int CODES = S::CODES, STAGE = S::STAGE;
     constexpr int RPC = 64 / C;                             // rows a wave's copy
-    constexpr int CP = ROWS / (4 * RPC);                    // code copies a wave and stage
-    constexpr int SP = ROWS >= 256 ? ROWS / 256 : 1;        // scale copies (64 rows) a wave and dword
+    constexpr int CP = ROWS / (NW * RPC);                   // code copies a wave and stage
+    constexpr int SA = (BM + 63) / 64, SLOTS = S::SLOTS;    // slots of 64 rows' scale dwords: a's, then b's
+    constexpr int SP = (SLOTS + NW - 1) / NW;               // scale copies (a slot each) a wave and dword
     constexpr int PER = CP + SP * Q, EARLY = PER / 2;
     constexpr int OS = sizeof(typename O::raw);
-    constexpr int PITCH = FN * 32 * OS + 16;                // epilogue: 32 rows a wave
+    constexpr int PITCH = TN * OS + 16;                     // epilogue: 32 rows a wave
     static_assert((STAGES & (STAGES - 1)) == 0 && (STAGES - 2) * PER + EARLY < 64, "ring of stages");
     static_assert(C == 4 || C == 8, "64 or 128 bytes a row");
+    static_assert(BM % (NW * RPC) == 0 && BN % (NW * RPC) == 0,
+                  "a pass of copies stays in one operand");
 
     const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = wave & 1, wn = wave >> 1;
+    const int thread = threadIdx.x % (NW * 64);
+    const int wave = __builtin_amdgcn_readfirstlane(thread >> 6);
+    const int group = KG > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / (NW * 64)) : 0;
+    unsigned char *const lds = smem;
+    smem += group * (STAGES * STAGE);
+    const int wm = wave % WM, wn = wave / WM;
     const int half = lane >> 5, l32 = lane & 31;
     int tm, tn;
     mx_tile(g, id, tm, tn);
     const int m0 = tm * BM, n0 = tn * BN;
-    const int quads = (g.kb + 3) / 4, nk = (g.kb + C - 1) / C;
+    const int quads = (g.kb + 3) / 4;
+    // K tiles t0 .. t0 + nk - 1, blocks below kend; the groups run as many
+    // steps each, the last ones on zeros
+    const int nk = ((g.kb + C - 1) / C + KG - 1) / KG, t0 = group * nk;
+    const int kend = KG > 1 ? min(g.kb, (t0 + nk) * C) : g.kb;
 
     const unsigned ca = (unsigned)g.M * g.kb * 16u, cb = (unsigned)g.N * g.kb * 16u;
     const unsigned na = (unsigned)g.M * quads * 4u, nb = (unsigned)g.N * quads * 4u;
     const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void *)g.a, 0, ca, kMxRsrcWord3);
     const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc((void *)g.b, 0, cb, kMxRsrcWord3);
 
-    // Copies of codes: this lane's row of the wave's RPC, and the physical
-    // 16-byte chunk lane % C of that row.  Chunk c of row r lies at
-    // c ^ key(r): 16 rows' equal chunks then cover all banks.
+    // Copies of codes: this lane's row of each pass, and the physical 16-byte
+    // chunk lane % C of that row.  Chunk c of row r lies at c ^ key(r): 16
+    // rows' equal chunks then cover all banks.
     auto key = [](int r) { return C == 4 ? (r >> 2) & 3 : (r >> 1) & 7; };
-    const int crow = wave * RPC + lane / C;
-    const int chunk = (lane & (C - 1)) ^ key(crow);
     unsigned coff[CP];
+    int cblk[CP];
 #pragma unroll
     for (int p = 0; p < CP; ++p) {
-        const int r = p * 4 * RPC + crow;      // (4 RPC rows a pass keep the key)
-        const bool isa = p * 4 * RPC < BM;
+        const int r = (p * NW + wave) * RPC + lane / C;
+        const bool isa = p * NW * RPC < BM;
         const int row = isa ? m0 + r : n0 + r - BM;
-        coff[p] = row < (isa ? g.M : g.N) ? (unsigned)row * (unsigned)g.kb * 16u + chunk * 16 : kMxOutOfRange;
+        cblk[p] = (lane & (C - 1)) ^ key(r);
+        coff[p] = row < (isa ? g.M : g.N) ? (unsigned)row * (unsigned)g.kb * 16u + cblk[p] * 16 : kMxOutOfRange;
     }
-    // Copies of scales: 64 rows a wave instruction.
+    // Copies of scales: a slot of 64 rows a wave instruction.
     __amdgpu_buffer_rsrc_t rs[SP];
     unsigned soff[SP], sstep[SP];
-    int sgroup[SP];
+    int slot[SP];
 #pragma unroll
     for (int p = 0; p < SP; ++p) {
-        sgroup[p] = (p * 4 + wave) % (ROWS / 64);
-        const bool isa = sgroup[p] * 64 < BM;
-        const int row = isa ? m0 + sgroup[p] * 64 + lane : n0 + sgroup[p] * 64 - BM + lane;
+        slot[p] = (p * NW + wave) % SLOTS;
+        const bool isa = slot[p] < SA;
+        const int row = isa ? m0 + slot[p] * 64 + lane : n0 + (slot[p] - SA) * 64 + lane;
         const int rows = isa ? g.M : g.N;
         rs[p] = __builtin_amdgcn_make_buffer_rsrc((void *)(isa ? g.sa : g.sb), 0, isa ? na : nb, kMxRsrcWord3);
         soff[p] = row < rows ? (unsigned)row * 4u : kMxOutOfRange;
@@ -146,11 +173,11 @@ __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsign
     auto issue1 = [&](int t, int c) {
         unsigned char *s = smem + (t & (STAGES - 1)) * STAGE;
         if (c < CP) {
-            mx_dma16(c * 4 * RPC < BM ? ra : rb, s + c * 4096 + wave * 1024,
-                     t * C + chunk < g.kb ? coff[c] + t * (C * 16u) : kMxOutOfRange);
+            mx_dma16(c * NW * RPC < BM ? ra : rb, s + (c * NW + wave) * 1024,
+                     t * C + cblk[c] < kend ? coff[c] + t * (C * 16u) : kMxOutOfRange);
         } else {
             const int p = (c - CP) / Q, q = (c - CP) % Q;
-            mx_dma4(rs[p], s + CODES + q * ROWS * 4 + sgroup[p] * 256, soff[p] + (t * Q + q) * sstep[p]);
+            mx_dma4(rs[p], s + CODES + (q * SLOTS + slot[p]) * 256, soff[p] + (t * Q + q) * sstep[p]);
         }
     };
 
@@ -163,9 +190,9 @@ __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsign
         for (int j = 0; j < FN; ++j)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-                const int n = n0 + wn * (BN / 2) + j * 32 + (e >> 2) * 8 + half * 4 + (e & 3);
-                acc[0][j][e] = __uint_as_float(
-                    __builtin_amdgcn_raw_buffer_load_b32(rbias, n < g.N ? n * 4u : kMxOutOfRange, 0, 0));
+                const int n = n0 + wn * TN + j * 32 + (e >> 2) * 8 + half * 4 + (e & 3);
+                acc[0][j][e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+                    rbias, n < g.N && group == 0 ? n * 4u : kMxOutOfRange, 0, 0));
             }
 #pragma unroll
         for (int i = 1; i < FM; ++i)
@@ -178,23 +205,23 @@ __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsign
     for (int t = 0; t < STAGES; ++t)
 #pragma unroll
         for (int c = 0; c < (t < STAGES - 1 ? PER : EARLY); ++c)
-            issue1(t, c);
+            issue1(t0 + t, c);
 
     // Step h of a K tile takes blocks 2 h (lanes 0 .. 31) and 2 h + 1 of each row.
-    const int arow = wm * (BM / 2) + l32, brow = BM + wn * (BN / 2) + l32, k32 = key(l32);
+    const int arow = wm * TM + l32, brow = wn * TN + l32, k32 = key(l32);
     i32x4_t a[2][FM], b[2][FN];
     auto frag1 = [&](int t, int h, int k) {
         const unsigned char *s = smem + (t & (STAGES - 1)) * STAGE + (((2 * h + half) ^ k32) * 16);
         if (k < FN)
-            b[h & 1][k] = *(const i32x4_t *)(s + (brow + k * 32) * (C * 16));
+            b[h & 1][k] = *(const i32x4_t *)(s + (BM + brow + k * 32) * (C * 16));
         else
             a[h & 1][k - FN] = *(const i32x4_t *)(s + (arow + (k - FN) * 32) * (C * 16));
     };
     unsigned wa[Q][FM], wb[Q][FN];
     auto scale1 = [&](int t, int q, int k) {
-        const unsigned char *s = smem + (t & (STAGES - 1)) * STAGE + CODES + q * ROWS * 4;
+        const unsigned char *s = smem + (t & (STAGES - 1)) * STAGE + CODES + q * SLOTS * 256;
         if (k < FN)
-            wb[q][k] = *(const unsigned *)(s + (brow + k * 32) * 4);
+            wb[q][k] = *(const unsigned *)(s + SA * 256 + (brow + k * 32) * 4);
         else
             wa[q][k - FN] = *(const unsigned *)(s + (arow + (k - FN) * 32) * 4);
     };
@@ -211,13 +238,13 @@ __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsign
     mx_barrier();
 #pragma unroll
     for (int k = 0; k < FR; ++k) {
-        frag1(0, 0, k);
+        frag1(t0, 0, k);
 #pragma unroll
         for (int q = 0; q < Q; ++q)
-            scale1(0, q, k);
+            scale1(t0, q, k);
     }
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    int t = 0;
+    int t = t0;
     do {      // nk > 0
         int sa[Q][FM], sb[Q][FN];
 #pragma unroll
@@ -259,15 +286,46 @@ __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsign
         }
         // (a fence: the compiler would sink the reads to the next iteration)
         __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    } while (++t < nk);
+    } while (++t < t0 + nk);
 
     // Rows of the output through LDS, 32 at a time and wave, so that stores
     // are 16 bytes a lane along the row.
     mx_wait_vm<0>();
     mx_wait_lds();
     mx_barrier();
-    unsigned char *mine = smem + wave * 32 * PITCH;
-    constexpr int CHUNKS = FN * 32 * OS / 16, EPC = 16 / OS;      // 16-byte chunks a row, elements a chunk
+    if constexpr (KG > 1) {
+        // [block of 16 values][group - 1][the group's thread]
+        f32x4_t *sums = (f32x4_t *)lds;
+#pragma unroll
+        for (int b = 0; b < FM * FN; ++b) {
+            f32x16_t &v = acc[b / FN][b % FN];
+            if (b > 0)
+                mx_barrier();
+            if (group > 0)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    sums[((group - 1) * 4 + q) * (NW * 64) + thread] =
+                        f32x4_t{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+            mx_wait_lds();
+            mx_barrier();
+            if (group == 0)
+#pragma unroll
+                for (int k = 0; k < KG - 1; ++k)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const f32x4_t u = sums[(k * 4 + q) * (NW * 64) + thread];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            v[4 * q + e] += u[e];
+                    }
+            mx_wait_lds();
+        }
+        mx_barrier();      // the sums have been read; the output's rows take their place
+        if (group > 0)
+            return;
+    }
+    unsigned char *mine = lds + wave * 32 * PITCH;
+    constexpr int CHUNKS = TN * OS / 16, EPC = 16 / OS;      // 16-byte chunks a row, elements a chunk
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
 #pragma unroll
@@ -286,9 +344,9 @@ __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsign
         mx_wait_lds();
         __builtin_amdgcn_wave_barrier();
         constexpr int RP = 64 / CHUNKS;      // rows a wave instruction
-        const int k = lane % CHUNKS, n = n0 + wn * (BN / 2) + k * EPC;
-        const int rows = min(g.M - m0 - wm * (BM / 2) - i * 32, 32);
-        typename O::raw *o = (typename O::raw *)g.out + (long long)(m0 + wm * (BM / 2) + i * 32) * g.N + n;
+        const int k = lane % CHUNKS, n = n0 + wn * TN + k * EPC;
+        const int rows = min(g.M - m0 - wm * TM - i * 32, 32);
+        typename O::raw *o = (typename O::raw *)g.out + (long long)(m0 + wm * TM + i * 32) * g.N + n;
         if (n + EPC <= g.N) {
 #pragma unroll
             for (int p = 0; p < 32 / RP; ++p) {
@@ -311,13 +369,13 @@ __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsign
     }
 }
 
-template <int BM, int BN, int BK, int STAGES, typename O>
-__global__ __launch_bounds__(kMxThreads) void mx_gemm_tile(MxGemmArgs g)
+template <typename S, typename O>
+__global__ __launch_bounds__(S::threads) void mx_gemm_tile(MxGemmArgs g)
 {
-    __shared__ __attribute__((aligned(16))) unsigned char smem[mx_gemm_lds<BM, BN, BK, STAGES, sizeof(typename O::raw)>()];
+    __shared__ __attribute__((aligned(16))) unsigned char smem[mx_gemm_lds<S, sizeof(typename O::raw)>()];
     const unsigned id = mx_xcd_tile(blockIdx.x, gridDim.x);
     if (id < (unsigned)g.tm * g.tn)
-        mx_gemm_body<BM, BN, BK, STAGES, O>(g, id, smem);
+        mx_gemm_body<S, O>(g, id, smem);
 }
 
 // Column sums from partial sums [parts][cols], 64 columns a workgroup.
@@ -333,30 +391,34 @@ __device__ __forceinline__ void mx_sum_parts(const MxSumArgs &a, unsigned block,
     float s = 0.f;
     if (c < a.cols)
 #pragma unroll 4
-        for (int p = w; p < a.parts; p += 4)
+        for (int p = w; p < a.parts; p += (int)blockDim.x / 64)
             s += a.part[(long long)p * a.cols + c];
     lds[threadIdx.x] = s;
     __syncthreads();
-    if (w == 0 && c < a.cols)
-        a.out[c] = (lds[threadIdx.x] + lds[threadIdx.x + 64]) + (lds[threadIdx.x + 128] + lds[threadIdx.x + 192]);
+    if (w == 0 && c < a.cols) {
+        s = 0.f;
+        for (int k = threadIdx.x; k < (int)blockDim.x; k += 64)
+            s += lds[k];
+        a.out[c] = s;
+    }
 }
 
 // Both products of the backward pass and the sums of db in one launch; the
 // first `dw_blocks` workgroups take dw's tiles (fp32), the next `dx_blocks`
 // those of dx, the others 64 columns of db each.
-template <int BM, int BN, int BK, int STAGES, typename O>
-__global__ __launch_bounds__(kMxThreads) void mx_gemm_bwd(MxGemmArgs dw, MxGemmArgs dx, MxSumArgs db,
+template <typename S, typename O>
+__global__ __launch_bounds__(S::threads) void mx_gemm_bwd(MxGemmArgs dw, MxGemmArgs dx, MxSumArgs db,
                                                           unsigned dw_blocks, unsigned dx_blocks)
 {
-    __shared__ __attribute__((aligned(16))) unsigned char smem[mx_gemm_lds<BM, BN, BK, STAGES, 4>()];
+    __shared__ __attribute__((aligned(16))) unsigned char smem[mx_gemm_lds<S, 4>()];
     if (blockIdx.x < dw_blocks) {
         const unsigned id = mx_xcd_tile(blockIdx.x, dw_blocks);
         if (id < (unsigned)dw.tm * dw.tn)
-            mx_gemm_body<BM, BN, BK, STAGES, Fp32>(dw, id, smem);
+            mx_gemm_body<S, Fp32>(dw, id, smem);
     } else if (blockIdx.x < dw_blocks + dx_blocks) {
         const unsigned id = mx_xcd_tile(blockIdx.x - dw_blocks, dx_blocks);
         if (id < (unsigned)dx.tm * dx.tn)
-            mx_gemm_body<BM, BN, BK, STAGES, O>(dx, id, smem);
+            mx_gemm_body<S, O>(dx, id, smem);
     } else {
         mx_sum_parts(db, blockIdx.x - dw_blocks - dx_blocks, (float *)smem);
     }

@@ -34,6 +34,7 @@ struct Fp32 {
     typedef float raw;
     static constexpr int code = CONVIMG_FP32;
 };
+struct Mx4 {};      // packed MXFP4 rows
 
 inline size_t dtype_bytes(int dtype) { return dtype == CONVIMG_FP32 ? 4 : 2; }
 inline bool dtype_ok(int dtype) { return dtype == CONVIMG_BF16 || dtype == CONVIMG_FP16 || dtype == CONVIMG_FP32; }
