@@ -71,27 +71,48 @@ void quantize_cols(const void *x, long long ldx, int rows, int cols, int dtype, 
 
 long long tile_count(int M, int N, int bm, int bn) { return (long long)((M + bm - 1) / bm) * ((N + bn - 1) / bn); }
 
-// Calls f with the shape for a launch that has count(BM, BN) tiles, rows of
-// the output (the most of any product in it) and kb blocks along K.  The
-// largest square tile that still gives most CUs one; else, where there are
-// few rows, tiles of as few; K tiles of 128 in small tiles (those of 256 take
-// whole cache lines, but hide less of the latency such launches consist of)
-// and groups of waves along a long K.
-template <typename C, typename F>
-void with_shape(C &&count, int rows, int kb, F &&f)
+auto tiles_of(int M, int N)
 {
-    if (count(256, 256) >= 192)
-        f(GemmShape<256, 256, 2, 2, 256, 2, 1>{});
-    else if (count(128, 128) >= 192)
-        f(GemmShape<128, 128, 2, 2, 256, 2, 1>{});
-    else if (rows <= 32 && kb > 16)
-        f(GemmShape<32, 32, 1, 1, 256, 2, 8>{});
-    else if (rows <= 64 && kb > 16)
-        f(GemmShape<64, 32, 2, 1, 256, 2, 4>{});
-    else if (count(64, 64) > 512 || kb <= 16)
-        f(GemmShape<64, 64, 2, 2, 128, 4, 1>{});
-    else
-        f(GemmShape<64, 64, 2, 2, 128, 4, 4>{});
+    return [=](int bm, int bn) { return tile_count(M, N, bm, bn); };
+}
+
+// The shape for a launch that has count(BM, BN) tiles and kb blocks along K: the largest tile that still gives most of the 256 CUs one.
+// Measured on both sides of each bound (M x N x K, us):
+//   256 x 256 from 144 tiles: 3000^3 28.9 (144 tiles) against 31.7 in 128 x
+//     128; 2048x4096x4096 (128 tiles) 31.8 against 23.9.
+//   128 x 128 from 192: 1024x4096x4096 (256) 16.7 against 20.6 in 128 x 64.
+//   128 x 64, two groups of waves, from 192: 512x4096x4096 (256) 11.2 against
+//     15.1 in 128 x 128 and 12.8 in 64 x 64; 256x4096x4096 (128) 10.6 against 8.6.
+//   64 x 64 from 192, and where K is at most 1024: 512^3 3.4 against 4.0 in 32 x 32;
+//     K tiles of 128, which hide more of the latency that such launches consist
+//     of than whole cache lines save (37x8000x4096 8.0, against 10.8 us in tiles of 256).
+//   64 x 32, four groups, from 192: 128x4096x4096 (256) 7.0 against 7.7 in 32 x 32.
+//   else 32 x 32: 64x4096x4096 6.3 against 6.9 in 64 x 32.
+template <typename C>
+int shape_of(C &&count, int kb)
+{
+    if (count(256, 256) >= 144)
+        return 0;
+    if (count(128, 128) >= 192)
+        return 1;
+    if (count(128, 64) >= 192 && kb > 32)
+        return 2;
+    if (count(64, 64) >= 192 || kb <= 32)
+        return 3;
+    return count(64, 32) >= 192 ? 4 : 5;
+}
+
+template <typename F>
+void with_shape(int shape, F &&f)
+{
+    switch (shape) {
+    case 0: f(GemmShape<256, 256, 2, 2, 256, 2, 1>{}); break;
+    case 1: f(GemmShape<128, 128, 2, 2, 256, 2, 1>{}); break;
+    case 2: f(GemmShape<128, 64, 2, 2, 256, 2, 2>{}); break;
+    case 3: f(GemmShape<64, 64, 2, 2, 128, 4, 1>{}); break;
+    case 4: f(GemmShape<64, 32, 2, 1, 256, 2, 4>{}); break;
+    default: f(GemmShape<32, 32, 1, 1, 256, 2, 4>{}); break;
+    }
 }
 
 MxGemmArgs gemm_args(MxOperand a, MxOperand b, const float *bias, int M, int N, int K, void *out)
@@ -109,7 +130,7 @@ unsigned gemm_grid(MxGemmArgs &g, int bm, int bn)
 void gemm(MxGemmArgs g, int out_dtype, hipStream_t stream)
 {
     with_dtype(out_dtype, [&](auto o) {
-        with_shape([&](int bm, int bn) { return tile_count(g.M, g.N, bm, bn); }, g.M, g.kb, [&](auto shape) {
+        with_shape(shape_of(tiles_of(g.M, g.N), g.kb), [&](auto shape) {
             typedef decltype(shape) S;
             const unsigned grid = gemm_grid(g, S::BM, S::BN);
             hipLaunchKernelGGL((mx_gemm_tile<S, decltype(o)>), dim3(grid), dim3(S::threads), 0, stream, g);
@@ -395,27 +416,37 @@ int mxfp4_linear_bwd(const void *dy, long long lddy, int dy_dtype, const void *x
                           (unsigned char *)along.scales,
                           sums};
     };
-    const long long t_dy = mx_tiles(M, N), t_w = mx_tiles(N, K), t_all = t_dy + t_w + mx_tiles(M, K);
+    const long long t_dy = mx_tiles(M, N), t_w = mx_tiles(N, K), t_x = mx_tiles(M, K);
     const MxTileArgs a_dy = tiles(dy, lddy, M, N, qdyt, qdy, part), a_w = tiles(w, ldw, N, K, qwt, {}, nullptr),
                      a_x = tiles(x, ldx, M, K, qxt, {}, nullptr);
     with_dtype(dy_dtype, [&](auto d) {
         with_dtype(dtype, [&](auto t) {
-            hipLaunchKernelGGL((mx_quantize_bwd<decltype(d), decltype(t)>), dim3(eights(t_all)), dim3(kMxThreads), 0,
-                               stream, a_dy, a_w, a_x, (unsigned)t_dy, (unsigned)t_w, (unsigned)t_all);
+            hipLaunchKernelGGL((mx_quantize_bwd<decltype(d), decltype(t)>), dim3(eights(t_dy) + eights(t_w) + eights(t_x)),
+                               dim3(kMxThreads), 0, stream, a_dy, a_w, a_x, (unsigned)t_dy, (unsigned)t_w,
+                               (unsigned)t_x);
         });
     });
     MxGemmArgs g_dx = gemm_args(qdy, qwt, nullptr, M, K, N, dx), g_dw = gemm_args(qdyt, qxt, nullptr, N, K, M, dw);
     const MxSumArgs sum = {part, db, (M + kMxTile - 1) / kMxTile, N};
+    // One launch for both products where they want tiles of like size; else
+    // the smaller one's few large tiles would be the last to end.
+    int s_dw = shape_of(tiles_of(N, K), g_dw.kb);
+    const int s_dx = shape_of(tiles_of(M, K), g_dx.kb);
+    const bool both = s_dw - s_dx < 2 && s_dx - s_dw < 2;
+    if (both)
+        s_dw = shape_of([&](int bm, int bn) { return tile_count(M, K, bm, bn) + tile_count(N, K, bm, bn); },
+                        M > N ? g_dw.kb : g_dx.kb);
     with_dtype(dx_dtype, [&](auto o) {
-        auto count = [&](int bm, int bn) { return tile_count(M, K, bm, bn) + tile_count(N, K, bm, bn); };
-        with_shape(count, M > N ? M : N, M > N ? g_dw.kb : g_dx.kb, [&](auto shape) {
+        with_shape(s_dw, [&](auto shape) {
             typedef decltype(shape) S;
-            const unsigned n_dx = gemm_grid(g_dx, S::BM, S::BN), n_dw = gemm_grid(g_dw, S::BM, S::BN),
+            const unsigned n_dx = both ? gemm_grid(g_dx, S::BM, S::BN) : 0, n_dw = gemm_grid(g_dw, S::BM, S::BN),
                            n_db = db ? (N + 63) / 64 : 0;
             hipLaunchKernelGGL((mx_gemm_bwd<S, decltype(o)>), dim3(n_dw + n_dx + n_db), dim3(S::threads), 0, stream,
                                g_dw, g_dx, sum, n_dw, n_dx);
         });
     });
+    if (!both)
+        gemm(g_dx, dx_dtype, stream);
     return launched();
 }
 

@@ -2,8 +2,8 @@
 // weights in one launch.
 //
 // Reading the weights once is all the work, so a workgroup takes 16 columns
-// of the output, its waves share the contracted axis, and each wave keeps two
-// stages of 256 k in flight to LDS: whole cache lines, eight lanes a row
+// of the output, its waves share the contracted axis, and each wave keeps
+// three stages of 256 k in flight to LDS: whole cache lines, eight lanes a row
 // (loading the matrix instruction's operands straight into registers puts
 // neighbouring lanes on different rows and reaches half the rate).  Every
 // workgroup quantises the rows into LDS for itself while its first weights
@@ -19,7 +19,7 @@
 
 namespace convimg {
 
-constexpr int kMxFewWaves = 8, kMxFewRing = 2;
+constexpr int kMxFewWaves = 8, kMxFewRing = 3;
 constexpr int kMxFewM = 4, kMxFewSize = 1 << 15;      // rows and elements at most
 
 // LDS: a row of codes ends in 16 bytes that set the rows' banks apart.
@@ -68,25 +68,45 @@ __global__ __launch_bounds__(kMxFewWaves * 64) void mx_gemm_few(MxFewArgs g)
 
     const int pitch = quads * 64 + 16, last = quads * 128, nt = blockDim.x * 8;
     unsigned char *scales = rows + g.M * pitch;
-    Raw8<X> raw = load_raw8<X>((const typename X::raw *)g.x, threadIdx.x * 8, g.K);
+    // (the rows are fetched before the weights, as loads return in order; what
+    // does not fit these registers is late)
+    constexpr int AHEAD = 4;
+    const int per = (last + nt - 1) / nt;      // a row's passes of all threads
+    Raw8<X> raw[AHEAD];
+    auto load_row = [&](int i, Raw8<X> &r) {
+        const int m = i / per, c = (i - m * per) * nt + threadIdx.x * 8;
+        r = load_raw8<X>((const typename X::raw *)g.x + m * g.ldx, c, g.K);
+    };
+    auto quantise = [&](int i, const Raw8<X> &r) {
+        const int m = i / per, c = (i - m * per) * nt + threadIdx.x * 8;
+        float v[8];
+        unpack8<X>(r, v);
+        unsigned top = 0;
 #pragma unroll
-    for (int u = 0; u < kMxFewRing; ++u)
-        fetch(u * waves + wave, u);
-    for (int m = 0; m < g.M; ++m)
-        for (int c = threadIdx.x * 8; c < last; c += nt) {
-            if (m > 0 || c >= nt)
-                raw = load_raw8<X>((const typename X::raw *)g.x + m * g.ldx, c, g.K);
-            float v[8];
-            unpack8<X>(raw, v);
-            unsigned top = 0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                top = mx_top(top, v[e]);
-            const unsigned byte = mx_scale_byte(quad_max(top));
+        for (int e = 0; e < 8; ++e)
+            top = mx_top(top, v[e]);
+        const unsigned byte = mx_scale_byte(quad_max(top));
+        if (c < last) {
             *(unsigned *)(rows + m * pitch + c / 2) = mx_encode8(v, mx_scale_value(byte));
             if ((c & 31) == 0)
                 scales[((c >> 7) * g.M + m) * 4 + ((c >> 5) & 3)] = (unsigned char)byte;
         }
+    };
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+        if (i < g.M * per)
+            load_row(i, raw[i]);
+#pragma unroll
+    for (int u = 0; u < kMxFewRing; ++u)
+        fetch(u * waves + wave, u);
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+        if (i < g.M * per)
+            quantise(i, raw[i]);
+    for (int i = AHEAD; i < g.M * per; ++i) {
+        load_row(i, raw[0]);
+        quantise(i, raw[0]);
+    }
     mx_wait_lds();
     mx_barrier();
 

@@ -69,7 +69,7 @@ template <typename T>
 constexpr int mx_tile_pitch() { return kMxTile * (int)sizeof(typename T::raw) + 16; }
 
 template <typename T>
-constexpr int mx_tile_lds() { return kMxTile * (mx_tile_pitch<T>() + kMxOutPitch + 16); }
+constexpr int mx_tile_lds() { return kMxTile * mx_tile_pitch<T>(); }      // (the results, 96 bytes a column, take its place)
 
 inline long long mx_tiles(int rows, int cols)
 {
@@ -100,8 +100,8 @@ template <typename T, bool ROWS>
 __device__ __forceinline__ void mx_quantize_tile(const MxTileArgs &a, unsigned tile, unsigned char *lds)
 {
     constexpr int PITCH = mx_tile_pitch<T>(), ES = sizeof(typename T::raw);
-    unsigned char *out = lds + kMxTile * PITCH;
-    float *sums = (float *)(out + kMxTile * kMxOutPitch);      // [4 waves][128]
+    static_assert(kMxTile * (kMxOutPitch + 16) <= mx_tile_lds<T>(), "results fit the tile");
+    float *sums = (float *)(lds + kMxTile * kMxOutPitch);      // [4 waves][128]
     const int across = (a.cols + kMxTile - 1) / kMxTile;
     const int tr = (int)(tile / across), tc = (int)(tile - (unsigned)tr * across);
     const int r0 = tr * kMxTile, c0 = tc * kMxTile;
@@ -119,8 +119,11 @@ __device__ __forceinline__ void mx_quantize_tile(const MxTileArgs &a, unsigned t
     __syncthreads();
 
     // down: a wave takes 32 rows, a lane two columns of them
+    u32v4_t down[2];
+    unsigned byte[2];
+    float s[2] = {0.f, 0.f};
     {
-        float v[2][32], s[2] = {0.f, 0.f};
+        float v[2][32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
             typename T::raw w[2];
@@ -131,14 +134,8 @@ __device__ __forceinline__ void mx_quantize_tile(const MxTileArgs &a, unsigned t
             s[1] += v[1][e];
         }
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            u32v4_t q;
-            const unsigned byte = mx_encode32(v[k], q);
-            *(u32v4_t *)(out + (lane * 2 + k) * kMxOutPitch + wave * 16) = q;
-            out[(lane * 2 + k) * kMxOutPitch + 64 + wave] = (unsigned char)byte;
-            if constexpr (ROWS)
-                sums[wave * kMxTile + lane * 2 + k] = s[k];
-        }
+        for (int k = 0; k < 2; ++k)
+            byte[k] = mx_encode32(v[k], down[k]);
     }
     // along: a thread takes two blocks of a row
     if constexpr (ROWS) {
@@ -165,12 +162,21 @@ __device__ __forceinline__ void mx_quantize_tile(const MxTileArgs &a, unsigned t
         if (row < a.rows && (t & 1) == 0)
             *(unsigned *)(a.rscales + ((long long)tc * a.rows + row) * 4) = bytes;
     }
+    __syncthreads();      // the tile has been read
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int c = lane * 2 + k;
+        *(u32v4_t *)(lds + c * kMxOutPitch + wave * 16) = down[k];
+        lds[c * kMxOutPitch + 64 + wave] = (unsigned char)byte[k];
+        if constexpr (ROWS)
+            sums[wave * kMxTile + c] = s[k];
+    }
     __syncthreads();
 
     // the columns' results, two lanes a column
     {
         const int col = c0 + (t >> 1), nb = mx_blocks(a.rows), b0 = tr * 4 + (t & 1) * 2;
-        const unsigned char *o = out + (t >> 1) * kMxOutPitch;
+        const unsigned char *o = lds + (t >> 1) * kMxOutPitch;
         if (col < a.cols) {
 #pragma unroll
             for (int k = 0; k < 2; ++k)
@@ -208,16 +214,24 @@ __global__ __launch_bounds__(kMxThreads) void mx_quantize_cols(MxTileArgs a, uns
 // column sums, w and x down their columns.
 template <typename DY, typename X>
 __global__ __launch_bounds__(kMxThreads) void mx_quantize_bwd(MxTileArgs dy, MxTileArgs w, MxTileArgs x,
-                                                              unsigned dy_tiles, unsigned w_tiles, unsigned tiles)
+                                                              unsigned dy_tiles, unsigned w_tiles, unsigned x_tiles)
 {
     constexpr int LDS = mx_tile_lds<DY>() > mx_tile_lds<X>() ? mx_tile_lds<DY>() : mx_tile_lds<X>();
     __shared__ __attribute__((aligned(16))) unsigned char lds[LDS];
-    const unsigned tile = mx_xcd_tile(blockIdx.x, gridDim.x);
-    if (tile < dy_tiles)
-        mx_quantize_tile<DY, true>(dy, tile, lds);
-    else if (tile < tiles)
-        mx_quantize_tile<X, false>(tile < dy_tiles + w_tiles ? w : x,
-                                   tile - (tile < dy_tiles + w_tiles ? dy_tiles : dy_tiles + w_tiles), lds);
+    // (each operand's tiles spread over all XCDs; the blocks of each are a
+    // multiple of 8)
+    const unsigned dy_blocks = (dy_tiles + 7) & ~7u, w_blocks = (w_tiles + 7) & ~7u;
+    if (blockIdx.x < dy_blocks) {
+        const unsigned tile = mx_xcd_tile(blockIdx.x, dy_blocks);
+        if (tile < dy_tiles)
+            mx_quantize_tile<DY, true>(dy, tile, lds);
+        return;
+    }
+    const unsigned b = blockIdx.x - dy_blocks;
+    const bool is_w = b < w_blocks;
+    const unsigned tile = is_w ? mx_xcd_tile(b, w_blocks) : mx_xcd_tile(b - w_blocks, (x_tiles + 7) & ~7u);
+    if (tile < (is_w ? w_tiles : x_tiles))
+        mx_quantize_tile<X, false>(is_w ? w : x, tile, lds);
 }
 
 // MXFP4 rows to values: a thread takes 8 columns.

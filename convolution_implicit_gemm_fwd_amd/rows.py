@@ -13,6 +13,7 @@ once and call the C entry points directly.
 """
 from __future__ import annotations
 
+from functools import lru_cache
 from typing import NamedTuple
 
 from . import abi
@@ -44,6 +45,22 @@ def _setup():
     _stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) \
         or (lambda index: torch.cuda.current_stream(index).cuda_stream)
     _torch = torch
+
+
+def _query(fn):
+    """A workspace's bytes by sizes and types."""
+    @lru_cache(maxsize=1024)
+    def bytes_of(*args):
+        rc, n = fn(*args)
+        if rc:
+            _fail(fn.__name__, rc)
+        return n
+    return bytes_of
+
+
+_norm_bwd_bytes = _query(abi.layer_norm_bwd_workspace)
+_linear_bytes = _query(abi.mxfp4_linear_workspace)
+_linear_bwd_bytes = _query(abi.mxfp4_linear_bwd_workspace)
 
 
 def _dtype(t, what):
@@ -206,9 +223,7 @@ def layer_norm_bwd_nhwc(dy, x, gamma, mean, rstd, dx_dtype=None, stream=None):
     g = _param(gamma, cols, dev, "gamma")
     m = _param(mean if mean.dim() == 1 else mean.reshape(-1), rows, dev, "mean")
     r = _param(rstd if rstd.dim() == 1 else rstd.reshape(-1), rows, dev, "rstd")
-    rc, need = abi.layer_norm_bwd_workspace(rows, cols)
-    if rc:
-        _fail("layer_norm_bwd_workspace", rc)
+    need = _norm_bwd_bytes(rows, cols)
     dx = _like(x, dx_dtype)
     dgamma, dbeta = x.new_empty((cols,), dtype=_f32), x.new_empty((cols,), dtype=_f32)
     ws = x.new_empty((need,), dtype=_u8)
@@ -303,9 +318,7 @@ def mxfp4_linear_nhwc(x, w, bias=None, out_dtype=None, stream=None):
         raise ValueError("x has %d columns, w %d" % (K, wk))
     od = _dtype(out_dtype, "out_dtype")
     b = _param(bias, N, dev, "bias")
-    rc, need = abi.mxfp4_linear_workspace(M, N, K, xd)
-    if rc:
-        _fail("mxfp4_linear_workspace", rc)
+    need = _linear_bytes(M, N, K, xd)
     out = codes.new_empty(shape, dtype=out_dtype)
     ws = codes.new_empty((need,)) if need else None
     rc = _lib.mxfp4_linear_fwd(xp, ld, sp, xd, codes.data_ptr(), scales.data_ptr(), b, M, N, K, od, out.data_ptr(),
@@ -341,9 +354,7 @@ def mxfp4_linear_bwd_nhwc(dy, x, w, dx_dtype=None, stream=None):
     if dx_dtype is None:
         dx_dtype = x.dtype
     dd, xd, od = _dtype(dy.dtype, "dy"), _dtype(x.dtype, "x"), _dtype(dx_dtype, "dx_dtype")
-    rc, need = abi.mxfp4_linear_bwd_workspace(M, N, K)
-    if rc:
-        _fail("mxfp4_linear_bwd_workspace", rc)
+    need = _linear_bwd_bytes(M, N, K)
     dx = _like(x, dx_dtype)
     dw, db = dy.new_empty((N, K), dtype=_f32), dy.new_empty((N,), dtype=_f32)
     ws = dy.new_empty((need,), dtype=_u8)
