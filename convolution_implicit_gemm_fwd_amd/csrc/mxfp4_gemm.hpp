@@ -56,11 +56,16 @@ __device__ __forceinline__ void mx_dma4(__amdgpu_buffer_rsrc_t r, unsigned char 
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)lds, 4, off, 0, 0, 0);
 }
 
-template <int SEL>
-__device__ __forceinline__ f32x16_t mx_mfma32(i32x4_t b, i32x4_t a, f32x16_t c, int sb, int sa)
+// Byte `sel` (known when compiled) of each scale dword.
+__device__ __forceinline__ f32x16_t mx_mfma32(int sel, i32x4_t b, i32x4_t a, f32x16_t c, int sb, int sa)
 {
     const i32x8_t b8 = {b[0], b[1], b[2], b[3], 0, 0, 0, 0}, a8 = {a[0], a[1], a[2], a[3], 0, 0, 0, 0};
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b8, a8, c, 4, 4, SEL, sb, SEL, sa);
+    switch (sel) {
+    case 0: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b8, a8, c, 4, 4, 0, sb, 0, sa);
+    case 1: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b8, a8, c, 4, 4, 1, sb, 1, sa);
+    case 2: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b8, a8, c, 4, 4, 2, sb, 2, sa);
+    default: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b8, a8, c, 4, 4, 3, sb, 3, sa);
+    }
 }
 
 // Tile number `id` (mx_xcd_tile: each XCD takes one run of them, so that its
@@ -109,10 +114,15 @@ __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsign
     constexpr int CP = ROWS / (NW * RPC);                   // code copies a wave and stage
     constexpr int SA = (BM + 63) / 64, SLOTS = S::SLOTS;    // slots of 64 rows' scale dwords: a's, then b's
     constexpr int SP = (SLOTS + NW - 1) / NW;               // scale copies (a slot each) a wave and dword
-    constexpr int PER = CP + SP * Q, EARLY = PER / 2;
+    constexpr int PER = CP + SP * Q;
+    // Copies of a later tile that a K tile's last step issues, its first and
+    // (the rest) its second: early enough to land, and spread, as each takes
+    // several instructions (8192^3: 310 us with 8, 8 and 4 of 20, 313 with 10
+    // and 10, 337 with all in the last step, 328 with none in it).
+    constexpr int E0 = PER * 2 / 5, E1 = H > 2 ? PER * 2 / 5 : PER - E0;
     constexpr int OS = sizeof(typename O::raw);
     constexpr int PITCH = TN * OS + 16;                     // epilogue: 32 rows a wave
-    static_assert((STAGES & (STAGES - 1)) == 0 && (STAGES - 2) * PER + EARLY < 64, "ring of stages");
+    static_assert((STAGES & (STAGES - 1)) == 0 && (STAGES - 2) * PER + E0 < 64, "ring of stages");
     static_assert(C == 4 || C == 8, "64 or 128 bytes a row");
     static_assert(BM % (NW * RPC) == 0 && BN % (NW * RPC) == 0,
                   "a pass of copies stays in one operand");
@@ -204,26 +214,30 @@ __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsign
 #pragma unroll
     for (int t = 0; t < STAGES; ++t)
 #pragma unroll
-        for (int c = 0; c < (t < STAGES - 1 ? PER : EARLY); ++c)
+        for (int c = 0; c < (t < STAGES - 1 ? PER : E0); ++c)
             issue1(t0 + t, c);
 
-    // Step h of a K tile takes blocks 2 h (lanes 0 .. 31) and 2 h + 1 of each row.
+    // Step h of a K tile takes two blocks of each row.  Of eight, lanes 0 .. 31
+    // take block h and the others block 4 + h, so that each half needs one
+    // scale dword, byte h of it; of four, blocks 2 h and 2 h + 1 and byte 2 h,
+    // the upper half's dword shifted down by a byte.
     const int arow = wm * TM + l32, brow = wn * TN + l32, k32 = key(l32);
     i32x4_t a[2][FM], b[2][FN];
     auto frag1 = [&](int t, int h, int k) {
-        const unsigned char *s = smem + (t & (STAGES - 1)) * STAGE + (((2 * h + half) ^ k32) * 16);
+        const int blk = C == 8 ? half * 4 + h : h * 2 + half;
+        const unsigned char *s = smem + (t & (STAGES - 1)) * STAGE + ((blk ^ k32) * 16);
         if (k < FN)
             b[h & 1][k] = *(const i32x4_t *)(s + (BM + brow + k * 32) * (C * 16));
         else
             a[h & 1][k - FN] = *(const i32x4_t *)(s + (arow + (k - FN) * 32) * (C * 16));
     };
-    unsigned wa[Q][FM], wb[Q][FN];
-    auto scale1 = [&](int t, int q, int k) {
-        const unsigned char *s = smem + (t & (STAGES - 1)) * STAGE + CODES + q * SLOTS * 256;
+    unsigned wa[FM], wb[FN];
+    auto scale1 = [&](int t, int k) {
+        const unsigned char *s = smem + (t & (STAGES - 1)) * STAGE + CODES + (C == 8 ? half * (SLOTS * 256) : 0);
         if (k < FN)
-            wb[q][k] = *(const unsigned *)(s + SA * 256 + (brow + k * 32) * 4);
+            wb[k] = *(const unsigned *)(s + SA * 256 + (brow + k * 32) * 4);
         else
-            wa[q][k - FN] = *(const unsigned *)(s + (arow + (k - FN) * 32) * 4);
+            wa[k - FN] = *(const unsigned *)(s + (arow + (k - FN) * 32) * 4);
     };
 
     // While the products of one step run, the next step's operands are read
@@ -234,39 +248,34 @@ __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsign
     // read by then and tile t + 1 has landed; the copies of tile t + STAGES
     // follow it, the second half of them in the next step.
     constexpr int NM = FM * FN, FR = FM + FN;
-    mx_wait_vm<(STAGES - 2) * PER + EARLY>();
+    mx_wait_vm<(STAGES - 2) * PER + E0>();
     mx_barrier();
 #pragma unroll
     for (int k = 0; k < FR; ++k) {
         frag1(t0, 0, k);
-#pragma unroll
-        for (int q = 0; q < Q; ++q)
-            scale1(t0, q, k);
+        scale1(t0, k);
     }
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
     int t = t0;
     do {      // nk > 0
-        int sa[Q][FM], sb[Q][FN];
+        int sa[FM], sb[FN];
+        const int shift = C == 8 ? 0 : 8 * half;
 #pragma unroll
-        for (int q = 0; q < Q; ++q) {
+        for (int i = 0; i < FM; ++i)
+            sa[i] = (int)(wa[i] >> shift);
 #pragma unroll
-            for (int i = 0; i < FM; ++i)
-                sa[q][i] = (int)(wa[q][i] >> (8 * half));
-#pragma unroll
-            for (int j = 0; j < FN; ++j)
-                sb[q][j] = (int)(wb[q][j] >> (8 * half));
-        }
+        for (int j = 0; j < FN; ++j)
+            sb[j] = (int)(wb[j] >> shift);
 #pragma unroll
         for (int h = 0; h < H; ++h) {
             const bool last = h == H - 1;
-            const int reads = last ? FR * (1 + Q) : FR;
-            const int copies = h == 0 ? PER - EARLY : last ? EARLY : 0;
+            const int reads = last ? 2 * FR : FR;
+            const int c0 = last ? 0 : h == 0 ? E0 : E0 + E1, copies = last ? E0 : h == 0 ? E1 : h == 1 ? PER - E0 - E1 : 0;
             const int pieces = reads + copies;
 #pragma unroll
             for (int m = 0; m < NM; ++m) {
                 const int i = m / FN, j = m % FN;
-                acc[i][j] = h & 1 ? mx_mfma32<2>(b[1][j], a[1][i], acc[i][j], sb[h / 2][j], sa[h / 2][i])
-                                  : mx_mfma32<0>(b[0][j], a[0][i], acc[i][j], sb[h / 2][j], sa[h / 2][i]);
+                acc[i][j] = mx_mfma32(C == 8 ? h : 2 * h, b[h & 1][j], a[h & 1][i], acc[i][j], sb[j], sa[i]);
                 if (last && m == 0) {
                     mx_wait_vm<(STAGES - 2) * PER>();
                     mx_wait_lds();
@@ -277,9 +286,9 @@ __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsign
                     if (k < FR)
                         frag1(last ? t + 1 : t, last ? 0 : h + 1, k);
                     else if (k < reads)
-                        scale1(t + 1, (k - FR) / FR, (k - FR) % FR);
+                        scale1(t + 1, k - FR);
                     else
-                        issue1(h == 0 ? t + STAGES - 1 : t + STAGES, k - reads + (h == 0 ? EARLY : 0));
+                        issue1(last ? t + STAGES : t + STAGES - 1, k - reads + c0);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }

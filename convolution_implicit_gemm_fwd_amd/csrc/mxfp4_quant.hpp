@@ -21,32 +21,44 @@ struct MxQuantArgs {
     int lg;                // log2 of the threads a row
 };
 
-// Rows to MXFP4: a thread takes 8 columns.
+// Rows to MXFP4: a thread takes 8 columns, of up to four groups at once.
 template <typename T>
 __global__ __launch_bounds__(kMxThreads) void mx_quantize_rows(MxQuantArgs a)
 {
+    constexpr int U = 4;
     const int tpr = 1 << a.lg;
     const long long row = (long long)blockIdx.x * (kMxThreads >> a.lg) + (threadIdx.x >> a.lg);
     if (row >= a.rows)
         return;
     const typename T::raw *x = (const typename T::raw *)a.x + row * a.ldx;
     const int kp = (a.cols + 31) & ~31;
-    for (int c = (threadIdx.x & (tpr - 1)) * 8; c < kp; c += tpr * 8) {
-        float v[8];
-        load8<T>(x, c, a.cols, v);
-        unsigned top = 0;
+    for (int c0 = (threadIdx.x & (tpr - 1)) * 8; c0 < kp; c0 += U * tpr * 8) {
+        Raw8<T> raw[U];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            top = mx_top(top, v[e]);
-        top = quad_max(top);
-        const unsigned byte = mx_scale_byte(top);
-        ((unsigned *)a.codes)[row * (kp / 8) + c / 8] = mx_encode8(v, mx_scale_value(byte));
-        if ((c & 31) == 0) {
-            unsigned char *s = a.scales + ((long long)(c >> 7) * a.rows + row) * 4;
-            s[(c >> 5) & 3] = (unsigned char)byte;
-            if (c + 32 == kp)      // bytes of blocks past the row's last one are 0
-                for (int b = ((c >> 5) & 3) + 1; b < 4; ++b)
-                    s[b] = 0;
+        for (int u = 0; u < U; ++u)
+            if (c0 + u * tpr * 8 < kp)
+                raw[u] = load_raw8<T>(x, c0 + u * tpr * 8, a.cols);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int c = c0 + u * tpr * 8;
+            if (c >= kp)
+                break;
+            float v[8];
+            unpack8<T>(raw[u], v);
+            unsigned top = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                top = mx_top(top, v[e]);
+            top = quad_max(top);
+            const unsigned byte = mx_scale_byte(top);
+            ((unsigned *)a.codes)[row * (kp / 8) + c / 8] = mx_encode8(v, mx_scale_value(byte));
+            if ((c & 31) == 0) {
+                unsigned char *s = a.scales + ((long long)(c >> 7) * a.rows + row) * 4;
+                s[(c >> 5) & 3] = (unsigned char)byte;
+                if (c + 32 == kp)      // bytes of blocks past the row's last one are 0
+                    for (int b = ((c >> 5) & 3) + 1; b < 4; ++b)
+                        s[b] = 0;
+            }
         }
     }
 }
