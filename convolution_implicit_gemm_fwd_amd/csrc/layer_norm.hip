@@ -231,7 +231,8 @@ struct LnBwdArgs {
     const void *dy, *x;
     const float *gamma, *mean, *rstd;
     void *dx;
-    float *part;           // [parts][2][cols]: sums of dy n and of dy; NULL to skip them
+    float *part_g, *part_b;      // sums of dy n and of dy, a row of `cols` every part_ld floats; NULL to skip them
+    long long part_ld;
     long long rows, lddy, ldx;
     int cols, dx_dtype, parts;
 };
@@ -308,9 +309,8 @@ __global__ __launch_bounds__(kLnThreads) void ln_bwd_cols_wide(LnBwdArgs a)
             db[e] += h[e];
         }
     }
-    float *p = a.part + (long long)blockIdx.y * 2 * a.cols;
-    store8<Fp32>(p, c, a.cols, dg);
-    store8<Fp32>(p + a.cols, c, a.cols, db);
+    store8<Fp32>(a.part_g + blockIdx.y * a.part_ld, c, a.cols, dg);
+    store8<Fp32>(a.part_b + blockIdx.y * a.part_ld, c, a.cols, db);
 }
 
 // Two sums over the TPR threads of a row at once.
@@ -411,15 +411,15 @@ __global__ __launch_bounds__(row_threads(TPR)) void ln_bwd_rows(LnBwdArgs a)
                 store8_as(a.dx_dtype, a.dx, row, (i * TPR + l) * 8, a.cols, h[i]);
         }
     }
-    if (!a.part)
+    if (!a.part_g)
         return;
-    float *p = a.part + (long long)blockIdx.x * 2 * a.cols;
+    float *pg = a.part_g + blockIdx.x * a.part_ld, *pb = a.part_b + blockIdx.x * a.part_ld;
     if constexpr (TPR > 64) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
             if ((i * TPR + l) * 8 < a.cols) {
-                store8<Fp32>(p, (i * TPR + l) * 8, a.cols, dg[i]);
-                store8<Fp32>(p + a.cols, (i * TPR + l) * 8, a.cols, db[i]);
+                store8<Fp32>(pg, (i * TPR + l) * 8, a.cols, dg[i]);
+                store8<Fp32>(pb, (i * TPR + l) * 8, a.cols, db[i]);
             }
     } else {
         // the wave's row groups, then the four waves
@@ -434,9 +434,9 @@ __global__ __launch_bounds__(row_threads(TPR)) void ln_bwd_rows(LnBwdArgs a)
                 }
             }
         __syncthreads();
-        for (int c = threadIdx.x; c < 2 * a.cols; c += kLnThreads) {
-            const int w = c < a.cols ? 0 : 1, k = c - w * a.cols;
-            p[c] = (sums[0][w][k] + sums[1][w][k]) + (sums[2][w][k] + sums[3][w][k]);
+        for (int c = threadIdx.x; c < a.cols; c += kLnThreads) {
+            pg[c] = (sums[0][0][c] + sums[1][0][c]) + (sums[2][0][c] + sums[3][0][c]);
+            pb[c] = (sums[0][1][c] + sums[1][1][c]) + (sums[2][1][c] + sums[3][1][c]);
         }
     }
 }
@@ -578,7 +578,9 @@ int ln_fwd_call(const LnFwdArgs &a, int x_dtype, int y_dtype, hipStream_t stream
 // Partial sums of the parameters' gradients, one a workgroup of the
 // backward pass: enough workgroups to keep the memory busy, few enough that
 // the partial sums (2 cols fp32 each, written and read) stay small beside
-// dy, x and dx.
+// dy, x and dx.  A single one writes the gradients itself: so do up to four
+// groups of rows, for which a second launch (4 us) would cost more than the
+// other workgroups save.
 int ln_parts(long long rows, int cols)
 {
     int per = 1;
@@ -587,8 +589,10 @@ int ln_parts(long long rows, int cols)
             per = row_threads(decltype(t)::value) / decltype(t)::value;
     });
     const long long groups = (rows + per - 1) / per;
+    if (groups <= 4)
+        return 1;
     const int most = cols <= 512 ? 1024 : cols <= 8192 ? 512 : 256;
-    return (int)(groups < 1 ? 1 : groups < most ? groups : most);
+    return (int)(groups < most ? groups : most);
 }
 
 template <typename DY, typename X>
@@ -600,7 +604,7 @@ void ln_bwd_launch(const LnBwdArgs &a, hipStream_t stream)
             if (a.rows > 0)
                 hipLaunchKernelGGL((ln_bwd_dx_wide<DY, X>), dim3(ln_grid(a.rows)), dim3(kLnThreads),
                                    0, stream, a);
-            if (a.part)
+            if (a.part_g)
                 hipLaunchKernelGGL((ln_bwd_cols_wide<DY, X>),
                                    dim3((a.cols + 8 * kLnThreads - 1) / (8 * kLnThreads), a.parts), dim3(kLnThreads),
                                    0, stream, a);
@@ -694,17 +698,19 @@ int layer_norm_bwd(const void *dy, long long lddy, const void *x, long long ldx,
             if (row_overlaps(out[i], nout[i], out[j], nout[j]))
                 return CONVIMG_ERR_ALIAS;
     }
-    const LnBwdArgs a = {dy,   x,    gamma, mean, rstd,     dx,   dgamma ? (float *)ws : nullptr,
-                         rows, lddy, ldx,   cols, dx_dtype, ln_parts(rows, cols)};
+    const int parts = ln_parts(rows, cols);
+    float *pg = parts > 1 && dgamma ? (float *)ws : dgamma, *pb = parts > 1 && dgamma ? pg + cols : dbeta;
+    const LnBwdArgs a = {dy,   x,    gamma, mean, rstd,     dx,   pg,   pb, 2LL * cols,
+                         rows, lddy, ldx,   cols, dx_dtype, parts};
     if (rows == 0 && !dgamma)
         return CONVIMG_OK;
-    // (with no rows the one partial sum is 0)
+    // (with no rows the one sum is 0)
     with_dtype(dy_dtype, [&](auto d) {
         with_dtype(x_dtype, [&](auto t) { ln_bwd_launch<decltype(d), decltype(t)>(a, stream); });
     });
-    if (dgamma)
+    if (dgamma && parts > 1)
         hipLaunchKernelGGL(ln_bwd_reduce, dim3((unsigned)((2LL * cols + kLnRedCols - 1) / kLnRedCols)),
-                           dim3(kLnRedThreads), 0, stream, a.part, dgamma, dbeta, cols, a.parts);
+                           dim3(kLnRedThreads), 0, stream, pg, dgamma, dbeta, cols, parts);
     return hipGetLastError() == hipSuccess ? CONVIMG_OK : CONVIMG_ERR_LAUNCH;
 }
 
