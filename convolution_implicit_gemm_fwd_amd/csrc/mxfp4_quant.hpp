@@ -119,15 +119,28 @@ __device__ __forceinline__ void mx_quantize_tile(const MxTileArgs &a, unsigned t
     const int r0 = tr * kMxTile, c0 = tc * kMxTile;
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
 
-    // 16 threads a row of the tile, zeros past the matrix
+    // 16 threads a row of the tile, zeros past the matrix.  Whole tiles, which
+    // need no test a load, have all loads in flight at once.
+    const bool whole = r0 + kMxTile <= a.rows && c0 + kMxTile <= a.cols;
+    const int lr = t >> 4, lc = (t & 15) * 8;
+    Raw8<T> v[8];
+    if (whole) {
+        const typename T::raw *x = (const typename T::raw *)a.x + (long long)(r0 + lr) * a.ldx + c0 + lc;
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
-        const int r = p * 16 + (t >> 4), c = (t & 15) * 8;
-        Raw8<T> v = {};
-        if (r0 + r < a.rows)
-            v = load_raw8<T>((const typename T::raw *)a.x + (long long)(r0 + r) * a.ldx, c0 + c, a.cols);
-        *(Raw8<T> *)(lds + r * PITCH + c * ES) = v;
+        for (int p = 0; p < 8; ++p)
+            v[p] = load_raw8<T>(x + (long long)p * 16 * a.ldx, 0, 8);
+    } else {
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+            v[p] = {};
+            if (r0 + lr + p * 16 < a.rows)
+                v[p] = load_raw8<T>((const typename T::raw *)a.x + (long long)(r0 + lr + p * 16) * a.ldx, c0 + lc,
+                                    a.cols);
+        }
     }
+#pragma unroll
+    for (int p = 0; p < 8; ++p)
+        *(Raw8<T> *)(lds + (p * 16 + lr) * PITCH + lc * ES) = v[p];
     __syncthreads();
 
     // down: a wave takes 32 rows, a lane two columns of them
