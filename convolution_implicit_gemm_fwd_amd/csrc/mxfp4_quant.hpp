@@ -115,7 +115,12 @@ __device__ __forceinline__ void mx_quantize_tile(const MxTileArgs &a, unsigned t
     static_assert(kMxTile * (kMxOutPitch + 16) <= mx_tile_lds<T>(), "results fit the tile");
     float *sums = (float *)(lds + kMxTile * kMxOutPitch);      // [4 waves][128]
     const int across = (a.cols + kMxTile - 1) / kMxTile;
-    const int tr = (int)(tile / across), tc = (int)(tile - (unsigned)tr * across);
+    // Two rows of tiles side by side: the halves of a cache line of codes, down
+    // and along, are written by tiles that run at about the same time.
+    const int tiles_down = (a.rows + kMxTile - 1) / kMxTile;
+    const int pr = (int)(tile / (2u * across)), in = (int)(tile - (unsigned)pr * 2u * across);
+    const bool two = pr * 2 + 1 < tiles_down;
+    const int tr = pr * 2 + (two ? in & 1 : 0), tc = two ? in >> 1 : in;
     const int r0 = tr * kMxTile, c0 = tc * kMxTile;
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
 
