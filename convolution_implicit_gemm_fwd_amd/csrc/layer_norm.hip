@@ -42,32 +42,25 @@ struct LnFwdArgs {
     float eps;
 };
 
-// Writes eight normalised values of a row: of type Y, or as MXFP4 (four
-// neighbouring lanes hold one block; all of them reach this together).
-template <typename Y>
+// Writes eight normalised values of a row: of type Y, or as MXFP4, whose
+// blocks and scale dwords are held by W = 4, 8 or 16 neighbouring lanes, which
+// all reach this together.
+template <typename Y, int W>
 __device__ __forceinline__ void ln_emit(const LnFwdArgs &a, long long row, int col, const float (&v)[8])
 {
-    // (past the row there is nothing; the lanes of a block agree on this)
-    if (col >= ((a.cols + 31) & ~31))
-        return;
     if constexpr (__is_same(Y, Mx4)) {
         unsigned top = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             top = mx_top(top, v[e]);
-        top = quad_max(top);
-        const unsigned byte = mx_scale_byte(top);
+        const unsigned byte = mx_scale_byte(quad_max(top));
         const int kp = (a.cols + 31) & ~31;
-        ((unsigned *)a.y)[row * (kp / 8) + col / 8] = mx_encode8(v, mx_scale_value(byte));
-        unsigned char *s = (unsigned char *)(a.scales + (long long)(col >> 7) * a.rows + row);
-        if ((col & 31) == 0) {
-            s[(col >> 5) & 3] = (unsigned char)byte;
-            // bytes of blocks past the row's last one are 0
-            if (col + 32 == kp)
-                for (int b = ((col >> 5) & 3) + 1; b < 4; ++b)
-                    s[b] = 0;
-        }
-    } else {
+        if (col < kp)
+            ((unsigned *)a.y)[row * (kp / 8) + col / 8] = mx_encode8(v, mx_scale_value(byte));
+        const unsigned word = mx_scale_word<W>(byte, col >> 5);
+        if ((col & 127) == 0 && col < kp)
+            a.scales[(long long)(col >> 7) * a.rows + row] = word;
+    } else if (col < a.cols) {
         store8<Y>((typename Y::raw *)a.y + row * a.cols, col, a.cols, v);
     }
 }
@@ -127,7 +120,11 @@ __global__ __launch_bounds__(row_threads(TPR)) void ln_fwd_rows(LnFwdArgs a)
     float gm[V][8], bt[V][8];
     Raw8<X> raw[V];
     const long long step = (long long)gridDim.x * RPB;
-    long long row = (long long)blockIdx.x * RPB + threadIdx.x / TPR;
+    // (MXFP4: neighbouring rows' scales share cache lines, so their workgroups
+    // share an XCD, of the 8 that take workgroups in turn; the grid is then a
+    // multiple of 8)
+    const unsigned place = __is_same(Y, Mx4) ? (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3) : blockIdx.x;
+    long long row = (long long)place * RPB + threadIdx.x / TPR;
     auto fetch = [&](long long r) {
         if (r < a.rows)
 #pragma unroll
@@ -180,7 +177,7 @@ __global__ __launch_bounds__(row_threads(TPR)) void ln_fwd_rows(LnFwdArgs a)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 v[i][e] = v[i][e] * rstd * gm[i][e] + bt[i][e];
-            ln_emit<Y>(a, row, (i * TPR + l) * 8, v[i]);
+            ln_emit<Y, (TPR < 16 ? TPR : 16)>(a, row, (i * TPR + l) * 8, v[i]);
         }
     }
 }
@@ -217,12 +214,12 @@ __global__ __launch_bounds__(kLnThreads) void ln_fwd_wide(LnFwdArgs a)
             if (a.rstd)
                 a.rstd[row] = rstd;
         }
-        // whole blocks of 32 columns, so that the lanes of a block stay together
-        const int kp = (a.cols + 31) & ~31;
-        for (int c = threadIdx.x * 8; c < kp; c += kLnThreads * 8) {
+        // whole runs of 128 columns, so that the lanes of a scale dword stay together
+        const int end = (a.cols + 127) & ~127;
+        for (int c = threadIdx.x * 8; c < end; c += kLnThreads * 8) {
             load8<X>(x, c, a.cols, v);
             ln_affine(a, c, mean, rstd, v);
-            ln_emit<Y>(a, row, c, v);
+            ln_emit<Y, 16>(a, row, c, v);
         }
     }
 }
@@ -528,11 +525,12 @@ unsigned ln_grid(long long rows) { return (unsigned)(rows < (1 << 22) ? rows : (
 
 // Workgroups of the forward pass: at most what 256 CUs hold of 2048 threads,
 // which walk the rows.
-unsigned ln_fwd_grid(long long rows, int tpr)
+unsigned ln_fwd_grid(long long rows, int tpr, bool eights)
 {
     const long long per = row_threads(tpr) / tpr, n = (rows + per - 1) / per;
     const long long most = 256 * 2048 / row_threads(tpr);
-    return (unsigned)(n < most ? n : most);
+    const unsigned g = (unsigned)(n < most ? n : most);
+    return eights ? (g + 7) & ~7u : g;
 }
 
 template <typename X, typename Y>
@@ -543,7 +541,7 @@ void ln_fwd_launch(const LnFwdArgs &a, hipStream_t stream)
         if constexpr (TPR == 0)
             hipLaunchKernelGGL((ln_fwd_wide<X, Y>), dim3(ln_grid(a.rows)), dim3(kLnThreads), 0, stream, a);
         else
-            hipLaunchKernelGGL((ln_fwd_rows<X, Y, TPR, V>), dim3(ln_fwd_grid(a.rows, TPR)),
+            hipLaunchKernelGGL((ln_fwd_rows<X, Y, TPR, V>), dim3(ln_fwd_grid(a.rows, TPR, std::is_same<Y, Mx4>::value)),
                                dim3(row_threads(TPR)), 0, stream, a);
     });
 }

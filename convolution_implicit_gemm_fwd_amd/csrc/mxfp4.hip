@@ -35,6 +35,8 @@ size_t packed_bytes(int rows, int cols)
     return align256(mx_code_bytes(rows, cols)) + align256(mx_scale_bytes(rows, cols));
 }
 
+unsigned eights(long long n) { return (unsigned)((n + 7) / 8 * 8); }
+
 // Threads a row (log2): enough for its columns, eight a thread, up to a
 // workgroup; at least the four lanes of a block.
 int row_lg(int cols)
@@ -52,11 +54,9 @@ void quantize(const void *x, long long ldx, int rows, int cols, int dtype, unsig
 {
     const MxQuantArgs a = {x, codes, scales, ldx, rows, cols, row_lg(cols)};
     with_dtype(dtype, [&](auto t) {
-        hipLaunchKernelGGL(mx_quantize_rows<decltype(t)>, dim3(row_grid(rows, a.lg)), dim3(kMxThreads), 0, stream, a);
+        hipLaunchKernelGGL(mx_quantize_rows<decltype(t)>, dim3(eights(row_grid(rows, a.lg))), dim3(kMxThreads), 0, stream, a);
     });
 }
-
-unsigned eights(long long n) { return (unsigned)((n + 7) / 8 * 8); }
 
 void quantize_cols(const void *x, long long ldx, int rows, int cols, int dtype, unsigned char *codes,
                    unsigned char *scales, hipStream_t stream)

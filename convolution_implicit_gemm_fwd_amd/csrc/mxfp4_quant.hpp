@@ -21,27 +21,38 @@ struct MxQuantArgs {
     int lg;                // log2 of the threads a row
 };
 
-// Rows to MXFP4: a thread takes 8 columns, of up to four groups at once.
+// Place of a workgroup in a launch whose grid is a multiple of 8: each of the
+// 8 XCDs, which take workgroups in turn, gets one run of places, so that the
+// parts of a cache line that neighbours write or read meet in one L2.
+__device__ __forceinline__ unsigned mx_xcd_tile(unsigned block, unsigned blocks)
+{
+    return (block & 7) * (blocks >> 3) + (block >> 3);
+}
+
+// Rows to MXFP4: a thread takes 8 columns, of up to four groups at once;
+// 1 << lg threads a row, at least 16 where a row has more than 64 columns, so
+// that a scale dword is written whole.
 template <typename T>
 __global__ __launch_bounds__(kMxThreads) void mx_quantize_rows(MxQuantArgs a)
 {
     constexpr int U = 4;
     const int tpr = 1 << a.lg;
-    const long long row = (long long)blockIdx.x * (kMxThreads >> a.lg) + (threadIdx.x >> a.lg);
+    const long long row =
+        (long long)mx_xcd_tile(blockIdx.x, gridDim.x) * (kMxThreads >> a.lg) + (threadIdx.x >> a.lg);
     if (row >= a.rows)
         return;
     const typename T::raw *x = (const typename T::raw *)a.x + row * a.ldx;
-    const int kp = (a.cols + 31) & ~31;
-    for (int c0 = (threadIdx.x & (tpr - 1)) * 8; c0 < kp; c0 += U * tpr * 8) {
+    const int kp = (a.cols + 31) & ~31, end = a.lg >= 4 ? (a.cols + 127) & ~127 : tpr * 8;
+    for (int c0 = (threadIdx.x & (tpr - 1)) * 8; c0 < end; c0 += U * tpr * 8) {
         Raw8<T> raw[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (c0 + u * tpr * 8 < kp)
+            if (c0 + u * tpr * 8 < end)
                 raw[u] = load_raw8<T>(x, c0 + u * tpr * 8, a.cols);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int c = c0 + u * tpr * 8;
-            if (c >= kp)
+            if (c >= end)      // (lanes of 128 columns agree on this)
                 break;
             float v[8];
             unpack8<T>(raw[u], v);
@@ -51,14 +62,13 @@ __global__ __launch_bounds__(kMxThreads) void mx_quantize_rows(MxQuantArgs a)
                 top = mx_top(top, v[e]);
             top = quad_max(top);
             const unsigned byte = mx_scale_byte(top);
-            ((unsigned *)a.codes)[row * (kp / 8) + c / 8] = mx_encode8(v, mx_scale_value(byte));
-            if ((c & 31) == 0) {
-                unsigned char *s = a.scales + ((long long)(c >> 7) * a.rows + row) * 4;
-                s[(c >> 5) & 3] = (unsigned char)byte;
-                if (c + 32 == kp)      // bytes of blocks past the row's last one are 0
-                    for (int b = ((c >> 5) & 3) + 1; b < 4; ++b)
-                        s[b] = 0;
-            }
+            if (c < kp)
+                ((unsigned *)a.codes)[row * (kp / 8) + c / 8] = mx_encode8(v, mx_scale_value(byte));
+            const unsigned word = a.lg >= 4   ? mx_scale_word<16>(byte, c >> 5)
+                                  : a.lg == 3 ? mx_scale_word<8>(byte, c >> 5)
+                                              : mx_scale_word<4>(byte, c >> 5);
+            if ((c & 127) == 0)
+                ((unsigned *)a.scales)[(long long)(c >> 7) * a.rows + row] = word;
         }
     }
 }
@@ -221,14 +231,6 @@ __device__ __forceinline__ void mx_quantize_tile(const MxTileArgs &a, unsigned t
                 a.part[(long long)tr * a.cols + c0 + t] =
                     (sums[t] + sums[kMxTile + t]) + (sums[2 * kMxTile + t] + sums[3 * kMxTile + t]);
     }
-}
-
-// Tile of a workgroup among `tiles`: each of the 8 XCDs, which take
-// workgroups in turn, gets one run, so that the halves of a cache line that
-// neighbouring tiles write meet in one L2.
-__device__ __forceinline__ unsigned mx_xcd_tile(unsigned block, unsigned blocks)
-{
-    return (block & 7) * (blocks >> 3) + (block >> 3);
 }
 
 template <typename T>

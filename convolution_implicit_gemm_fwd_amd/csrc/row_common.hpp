@@ -264,6 +264,20 @@ __device__ __forceinline__ unsigned mx_scale_byte(unsigned top_bits)
     return e == 255 ? 255u : (unsigned)(e > 2 ? e - 2 : 0);
 }
 
+// The scale dword of 128 columns (four blocks) that W / 4 quads of lanes hold,
+// W 4, 8 or 16; `byte` is the scale byte of the lane's block `blk`.  All W
+// lanes take part and get it.
+template <int W>
+__device__ __forceinline__ unsigned mx_scale_word(unsigned byte, int blk)
+{
+    unsigned w = byte << (8 * (blk & 3));
+    if constexpr (W >= 8)
+        w |= (unsigned)__builtin_amdgcn_mov_dpp((int)w, 0x141, 0xf, 0xf, true);      // half row mirrored
+    if constexpr (W >= 16)
+        w |= (unsigned)__builtin_amdgcn_mov_dpp((int)w, 0x140, 0xf, 0xf, true);      // row mirrored
+    return w;
+}
+
 // 2^(byte - 127) for bytes 0 .. 254, NaN for 255: the fp32 exponent field,
 // with 2^-127 a subnormal.
 __device__ __forceinline__ float mx_scale_value(unsigned byte)
