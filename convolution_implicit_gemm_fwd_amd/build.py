@@ -1,8 +1,9 @@
-"""Build libconvimg.so (HIP, gfx950) in-tree.
+"""Build libconvimg.so (HIP, gfx950) and _rows.so in-tree.
 
 ``python -m convolution_implicit_gemm_fwd_amd.build`` compiles the HIP
 translation units with hipcc for gfx950 only (each with its own extra flags)
-and links them into one shared library next to this file.
+and links them into one shared library next to this file; and the host-only
+module that calls it from torch (csrc/rows_ext.cpp) with the C++ compiler.
 """
 from __future__ import annotations
 
@@ -16,6 +17,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libconvimg.so")
+EXT = os.path.join(PKG, "_rows.so")
 # (source, extra hipcc flags): the weight-backward kernel keeps its MFMA
 # accumulators in VGPRs (fewer register copies in its loop, measured)
 UNITS = [(os.path.join(CSRC, "conv2d_fwd.hip"), []),
@@ -43,6 +45,21 @@ def hipcc() -> str:
         if c and os.path.exists(c):
             return c
     raise RuntimeError("hipcc not found; the HIP library cannot be built")
+
+
+def ext_command(out: str):
+    """The command that compiles the torch module (host code only)."""
+    import importlib.util
+    import sysconfig
+
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cxx = os.environ.get("CXX") or shutil.which("g++") or "/opt/rocm/llvm/bin/clang++"
+    return [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM",
+            "-isystem", os.path.join(torch, "include"),
+            "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+            "-isystem", "/opt/rocm/include", "-isystem", sysconfig.get_paths()["include"], "-I", INCLUDE,
+            os.path.join(CSRC, "rows_ext.cpp"), "-o", out, "-L" + os.path.join(torch, "lib"),
+            "-ltorch_python", "-ltorch_hip", "-ltorch_cpu", "-lc10", "-lc10_hip"]
 
 
 def build(verbose: bool = False, extra_flags=()) -> str:
@@ -74,6 +91,12 @@ def build(verbose: bool = False, extra_flags=()) -> str:
                 print(" ".join(cmd), flush=True)
             procs.append(subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT,
                                           text=True))
+        ext_tmp = EXT + ".tmp" + tag
+        objs.append(ext_tmp)
+        cmd = ext_command(ext_tmp)
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        procs.append(subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True))
         failed = []
         for p in procs:
             out, _ = p.communicate()
@@ -83,10 +106,11 @@ def build(verbose: bool = False, extra_flags=()) -> str:
             elif verbose and msgs:
                 print("\n".join(msgs))
         if failed:
-            raise RuntimeError("hipcc failed:\n" + "\n".join(failed))
+            raise RuntimeError("the compiler failed:\n" + "\n".join(failed))
         tmp = LIB + ".tmp" + tag
-        run([hipcc(), "--offload-arch=" + ARCH, "-shared", "-fPIC", *objs, "-o", tmp])
+        run([hipcc(), "--offload-arch=" + ARCH, "-shared", "-fPIC", *objs[:len(UNITS)], "-o", tmp])
         os.replace(tmp, LIB)
+        os.replace(ext_tmp, EXT)
     finally:
         for o in objs:
             if os.path.exists(o):

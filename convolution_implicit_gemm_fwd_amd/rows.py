@@ -7,9 +7,10 @@ a matrix).  Calls run on ``stream`` (default: torch's current stream of the
 first tensor's device) without waiting; torch supplies device memory and the
 stream only.
 
-A small call costs the host more than the GPU (a launch is about 4 us, the
-kernel of one 4096-wide token 2 us), so the functions here look each thing up
-once and call the C entry points directly.
+A small call costs the host more than the GPU (a launch is about 3 us, the
+kernel of one 4096-wide token 2 us), so the common case (tensors as they
+should be, on the current device and stream) takes its whole way in compiled
+code (csrc/rows_ext.cpp); everything else, errors included, is handled here.
 """
 from __future__ import annotations
 
@@ -30,14 +31,22 @@ class Mxfp4Tensor(NamedTuple):
 
 
 _torch = None
+_new = tuple.__new__
 
 
 def _setup():
     """torch, the loaded library and what every call takes from them."""
-    global _torch, _lib, _codes, _f32, _u8, _device, _stream, _empty
+    global _torch, _fast, _lib, _codes, _f32, _u8, _device, _stream, _empty
+    import ctypes
+
     import torch
 
     _lib = abi.load()
+    from . import _rows as _fast
+    for name in ("layer_norm_fwd", "layer_norm_fwd_mxfp4", "layer_norm_bwd", "layer_norm_bwd_workspace",
+                 "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_linear_fwd", "mxfp4_linear_workspace",
+                 "mxfp4_linear_bwd", "mxfp4_linear_bwd_workspace"):
+        _fast.bind(name, ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value)
     _codes = {torch.bfloat16: CONVIMG_BF16, torch.float32: CONVIMG_FP32, torch.float16: CONVIMG_FP16}
     _f32, _u8 = torch.float32, torch.uint8
     _device = torch.cuda.current_device
@@ -152,6 +161,10 @@ def layer_norm_nhwc(x, gamma=None, beta=None, eps=1e-5, out_dtype=None, stats=Fa
     """
     if _torch is None:
         _setup()
+    if stream is None:
+        r = _fast.layer_norm(x, gamma, beta, eps, out_dtype, stats)
+        if r is not None:
+            return r
     rows, cols, ld = _rows_of(x, "x")
     dev = x.device
     if _device() != dev.index:
@@ -186,6 +199,10 @@ def layer_norm_mxfp4_nhwc(x, gamma=None, beta=None, eps=1e-5, stream=None):
     ``Mxfp4Tensor``, the input of ``mxfp4_linear_nhwc``."""
     if _torch is None:
         _setup()
+    if stream is None:
+        r = _fast.layer_norm_mxfp4(x, gamma, beta, eps)
+        if r is not None:
+            return _new(Mxfp4Tensor, r)
     rows, cols, ld = _rows_of(x, "x")
     dev = x.device
     if _device() != dev.index:
@@ -211,6 +228,10 @@ def layer_norm_bwd_nhwc(dy, x, gamma, mean, rstd, dx_dtype=None, stream=None):
     """
     if _torch is None:
         _setup()
+    if stream is None:
+        r = _fast.layer_norm_bwd(dy, x, gamma, mean, rstd, dx_dtype)
+        if r is not None:
+            return r
     rows, cols, ld = _rows_of(x, "x")
     dev = x.device
     if dy.shape != x.shape:
@@ -244,6 +265,10 @@ def mxfp4_quantize_nhwc(x, transpose=False, stream=None):
     its transpose, so that blocks of 32 run down the columns of x."""
     if _torch is None:
         _setup()
+    if stream is None:
+        r = _fast.quantize(x, transpose)
+        if r is not None:
+            return _new(Mxfp4Tensor, r)
     rows, cols, ld = _rows_of(x, "x")
     dev = x.device
     if _device() != dev.index:
@@ -272,6 +297,10 @@ def mxfp4_dequantize_nhwc(q, dtype, stream=None):
     """The values [rows, cols] that packed rows stand for, in ``dtype``."""
     if _torch is None:
         _setup()
+    if stream is None:
+        r = _fast.dequantize(q, dtype)
+        if r is not None:
+            return r
     _check_packed(q, "q")
     d = _dtype(dtype, "dtype")
     codes, scales, rows, cols = q
@@ -298,6 +327,10 @@ def mxfp4_linear_nhwc(x, w, bias=None, out_dtype=None, stream=None):
     """
     if _torch is None:
         _setup()
+    if stream is None:
+        r = _fast.linear(x, w, bias, out_dtype)
+        if r is not None:
+            return r
     _check_packed(w, "w")
     codes, scales, N, wk = w
     dev = codes.device
@@ -341,6 +374,10 @@ def mxfp4_linear_bwd_nhwc(dy, x, w, dx_dtype=None, stream=None):
     """
     if _torch is None:
         _setup()
+    if stream is None:
+        r = _fast.linear_bwd(dy, x, w, dx_dtype)
+        if r is not None:
+            return r
     M, N, ldy = _rows_of(dy, "dy")
     mx, K, ldx = _rows_of(x, "x")
     if w.dim() != 2 or mx != M or dy.shape[:-1] != x.shape[:-1] or w.shape != (N, K):
