@@ -64,7 +64,7 @@ void quantize_cols(const void *x, long long ldx, int rows, int cols, int dtype, 
     const MxTileArgs a = {x, ldx, rows, cols, codes, scales, nullptr, nullptr, nullptr};
     const long long tiles = mx_tiles(rows, cols);
     with_dtype(dtype, [&](auto t) {
-        hipLaunchKernelGGL(mx_quantize_cols<decltype(t)>, dim3(eights(tiles)), dim3(kMxThreads), 0, stream, a,
+        hipLaunchKernelGGL(mx_quantize_cols<decltype(t)>, dim3(eights(tiles)), dim3(kMxTileThreads), 0, stream, a,
                            (unsigned)tiles);
     });
 }
@@ -422,7 +422,7 @@ int mxfp4_linear_bwd(const void *dy, long long lddy, int dy_dtype, const void *x
     with_dtype(dy_dtype, [&](auto d) {
         with_dtype(dtype, [&](auto t) {
             hipLaunchKernelGGL((mx_quantize_bwd<decltype(d), decltype(t)>), dim3(eights(t_dy) + eights(t_w) + eights(t_x)),
-                               dim3(kMxThreads), 0, stream, a_dy, a_w, a_x, (unsigned)t_dy, (unsigned)t_w,
+                               dim3(kMxTileThreads), 0, stream, a_dy, a_w, a_x, (unsigned)t_dy, (unsigned)t_w,
                                (unsigned)t_x);
         });
     });

@@ -87,7 +87,7 @@ struct MxTileArgs {
     float *part;           // [tiles down][cols]
 };
 
-constexpr int kMxTile = 128;
+constexpr int kMxTile = 128, kMxTileThreads = 512;
 constexpr int kMxOutPitch = 64 + 16;      // LDS bytes of a column's result: four blocks of codes, their scales
 
 template <typename T>
@@ -139,94 +139,80 @@ __device__ __forceinline__ void mx_quantize_tile(const MxTileArgs &a, unsigned t
 
     // 16 threads a row of the tile, zeros past the matrix.  Whole tiles, which
     // need no test a load, have all loads in flight at once.
+    constexpr int PASSES = kMxTile * 16 / kMxTileThreads, LR = kMxTileThreads / 16;
     const bool whole = r0 + kMxTile <= a.rows && c0 + kMxTile <= a.cols;
     const int lr = t >> 4, lc = (t & 15) * 8;
-    Raw8<T> v[8];
+    Raw8<T> raw[PASSES];
     if (whole) {
         const typename T::raw *x = (const typename T::raw *)a.x + (long long)(r0 + lr) * a.ldx + c0 + lc;
 #pragma unroll
-        for (int p = 0; p < 8; ++p)
-            v[p] = load_raw8<T>(x + (long long)p * 16 * a.ldx, 0, 8);
+        for (int p = 0; p < PASSES; ++p)
+            raw[p] = load_raw8<T>(x + (long long)p * LR * a.ldx, 0, 8);
     } else {
 #pragma unroll
-        for (int p = 0; p < 8; ++p) {
-            v[p] = {};
-            if (r0 + lr + p * 16 < a.rows)
-                v[p] = load_raw8<T>((const typename T::raw *)a.x + (long long)(r0 + lr + p * 16) * a.ldx, c0 + lc,
-                                    a.cols);
+        for (int p = 0; p < PASSES; ++p) {
+            raw[p] = {};
+            if (r0 + lr + p * LR < a.rows)
+                raw[p] = load_raw8<T>((const typename T::raw *)a.x + (long long)(r0 + lr + p * LR) * a.ldx, c0 + lc,
+                                      a.cols);
         }
     }
 #pragma unroll
-    for (int p = 0; p < 8; ++p)
-        *(Raw8<T> *)(lds + (p * 16 + lr) * PITCH + lc * ES) = v[p];
+    for (int p = 0; p < PASSES; ++p)
+        *(Raw8<T> *)(lds + (p * LR + lr) * PITCH + lc * ES) = raw[p];
     __syncthreads();
 
-    // down: a wave takes 32 rows, a lane two columns of them
-    u32v4_t down[2];
-    unsigned byte[2];
-    float s[2] = {0.f, 0.f};
+    // down: a wave takes 32 rows of 64 columns, a lane one column
+    const int blk = wave & 3, c = (wave >> 2) * 64 + lane;
+    u32v4_t down;
+    unsigned byte;
+    float sum = 0.f;
     {
-        float v[2][32];
+        float v[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-            typename T::raw w[2];
-            __builtin_memcpy(w, __builtin_assume_aligned(lds + (wave * 32 + e) * PITCH + lane * 2 * ES, 2 * ES), 2 * ES);
-            v[0][e] = load1<T>(&w[0]);
-            v[1][e] = load1<T>(&w[1]);
-            s[0] += v[0][e];
-            s[1] += v[1][e];
+            v[e] = load1<T>((const typename T::raw *)(lds + (blk * 32 + e) * PITCH + c * ES));
+            sum += v[e];
         }
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-            byte[k] = mx_encode32(v[k], down[k]);
+        byte = mx_encode32(v, down);
     }
-    // along: a thread takes two blocks of a row
+    // along: a thread takes a block of a row
     if constexpr (ROWS) {
-        const int row = r0 + (t >> 1), nb = mx_blocks(a.cols), b0 = tc * 4 + (t & 1) * 2;
-        unsigned bytes = 0;
+        const int row = r0 + (t >> 2), nb = mx_blocks(a.cols), b0 = tc * 4 + (t & 3);
+        float v[32];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            float v[32];
+        for (int i = 0; i < 4; ++i) {
+            const Raw8<T> w = *(const Raw8<T> *)(lds + (t >> 2) * PITCH + ((t & 3) * 32 + i * 8) * ES);
+            float u[8];
+            unpack8<T>(w, u);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const Raw8<T> w = *(const Raw8<T> *)(lds + (t >> 1) * PITCH + ((t & 1) * 64 + k * 32 + i * 8) * ES);
-                float u[8];
-                unpack8<T>(w, u);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v[i * 8 + e] = u[e];
-            }
-            u32v4_t q;
-            bytes |= mx_encode32(v, q) << (8 * k);
-            if (row < a.rows && b0 + k < nb)
-                *(u32v4_t *)(a.rcodes + ((long long)row * nb + b0 + k) * 16) = q;
+            for (int e = 0; e < 8; ++e)
+                v[i * 8 + e] = u[e];
         }
-        bytes |= (unsigned)__builtin_amdgcn_mov_dpp((int)bytes, 0xB1, 0xf, 0xf, true) << 16;
-        if (row < a.rows && (t & 1) == 0)
-            *(unsigned *)(a.rscales + ((long long)tc * a.rows + row) * 4) = bytes;
+        u32v4_t q;
+        unsigned word = mx_encode32(v, q) << (8 * (t & 3));
+        if (row < a.rows && b0 < nb)
+            *(u32v4_t *)(a.rcodes + ((long long)row * nb + b0) * 16) = q;
+        word |= (unsigned)__builtin_amdgcn_mov_dpp((int)word, 0xB1, 0xf, 0xf, true);
+        word |= (unsigned)__builtin_amdgcn_mov_dpp((int)word, 0x4E, 0xf, 0xf, true);
+        if (row < a.rows && (t & 3) == 0)
+            *(unsigned *)(a.rscales + ((long long)tc * a.rows + row) * 4) = word;
     }
     __syncthreads();      // the tile has been read
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int c = lane * 2 + k;
-        *(u32v4_t *)(lds + c * kMxOutPitch + wave * 16) = down[k];
-        lds[c * kMxOutPitch + 64 + wave] = (unsigned char)byte[k];
-        if constexpr (ROWS)
-            sums[wave * kMxTile + c] = s[k];
-    }
+    *(u32v4_t *)(lds + c * kMxOutPitch + blk * 16) = down;
+    lds[c * kMxOutPitch + 64 + blk] = (unsigned char)byte;
+    if constexpr (ROWS)
+        sums[blk * kMxTile + c] = sum;
     __syncthreads();
 
-    // the columns' results, two lanes a column
+    // the columns' results, four lanes a column
     {
-        const int col = c0 + (t >> 1), nb = mx_blocks(a.rows), b0 = tr * 4 + (t & 1) * 2;
-        const unsigned char *o = lds + (t >> 1) * kMxOutPitch;
+        const int col = c0 + (t >> 2), nb = mx_blocks(a.rows), b0 = tr * 4 + (t & 3);
+        const unsigned char *o = lds + (t >> 2) * kMxOutPitch;
         if (col < a.cols) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-                if (b0 + k < nb)
-                    *(u32v4_t *)(a.ccodes + ((long long)col * nb + b0 + k) * 16) =
-                        *(const u32v4_t *)(o + ((t & 1) * 2 + k) * 16);
-            if ((t & 1) == 0)
+            if (b0 < nb)
+                *(u32v4_t *)(a.ccodes + ((long long)col * nb + b0) * 16) = *(const u32v4_t *)(o + (t & 3) * 16);
+            if ((t & 3) == 0)
                 *(unsigned *)(a.cscales + ((long long)tr * a.cols + col) * 4) = *(const unsigned *)(o + 64);
         }
         if constexpr (ROWS)
@@ -237,7 +223,7 @@ __device__ __forceinline__ void mx_quantize_tile(const MxTileArgs &a, unsigned t
 }
 
 template <typename T>
-__global__ __launch_bounds__(kMxThreads) void mx_quantize_cols(MxTileArgs a, unsigned tiles)
+__global__ __launch_bounds__(kMxTileThreads) void mx_quantize_cols(MxTileArgs a, unsigned tiles)
 {
     __shared__ __attribute__((aligned(16))) unsigned char lds[mx_tile_lds<T>()];
     const unsigned tile = mx_xcd_tile(blockIdx.x, gridDim.x);
@@ -249,7 +235,7 @@ __global__ __launch_bounds__(kMxThreads) void mx_quantize_cols(MxTileArgs a, uns
 // column sums, w and x down their columns (8192x4096x4096 bf16: 48 us for 233
 // MB, 4.8 TB/s).
 template <typename DY, typename X>
-__global__ __launch_bounds__(kMxThreads) void mx_quantize_bwd(MxTileArgs dy, MxTileArgs w, MxTileArgs x,
+__global__ __launch_bounds__(kMxTileThreads) void mx_quantize_bwd(MxTileArgs dy, MxTileArgs w, MxTileArgs x,
                                                               unsigned dy_tiles, unsigned w_tiles, unsigned x_tiles)
 {
     constexpr int LDS = mx_tile_lds<DY>() > mx_tile_lds<X>() ? mx_tile_lds<DY>() : mx_tile_lds<X>();
