@@ -107,6 +107,38 @@ __device__ __forceinline__ float row_sum(float v, float *lds)
     }
 }
 
+// The columns of thread l of a row: V groups of eight, TPR groups apart.  With
+// WINDOW the group that the row's end cuts is its last eight columns instead,
+// so that loads and stores stay whole; the columns that it shares with its
+// neighbour are computed twice, alike, and counted once in the row's sums.
+template <int TPR, int V, bool WINDOW>
+struct RowCols {
+    int col[V];       // first column, at least `cols` for none
+    int first[V];     // first of the eight that counts
+
+    __device__ __forceinline__ RowCols(int l, int cols)
+    {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = (i * TPR + l) * 8;
+            col[i] = WINDOW && c < cols ? min(c, cols - 8) : c;
+            first[i] = c < cols ? c - col[i] : 8;
+        }
+    }
+    __device__ __forceinline__ bool counts(int i, int e) const { return e >= first[i]; }
+
+    template <typename T>
+    __device__ __forceinline__ Raw8<T> load(const typename T::raw *row, int i, int cols) const
+    {
+        return load_raw8<T, TPR == 4>(row, col[i], cols);
+    }
+    template <typename T>
+    __device__ __forceinline__ void unpack(const Raw8<T> &r, int i, int cols, float (&v)[8]) const
+    {
+        unpack8<T>(WINDOW ? r : tail8<T, TPR == 4>(r, col[i], cols), v);
+    }
+};
+
 // Rows that fit the registers of TPR threads, 8 V columns each; a workgroup
 // takes row_threads(TPR) / TPR rows at once, reads each once, and the next
 // ones before it sums the present ones.  Bound by memory: 16384 x 4096 bf16
@@ -118,8 +150,10 @@ __global__ __launch_bounds__(row_threads(TPR)) void ln_fwd_rows(LnFwdArgs a)
 {
     __shared__ float lds[2][16];
     constexpr int RPB = row_threads(TPR) / TPR;
+    constexpr bool WINDOW = TPR > 4 && !__is_same(Y, Mx4);
     const int l = threadIdx.x % TPR;
     const float inv = 1.f / (float)a.cols;
+    const RowCols<TPR, V, WINDOW> at(l, a.cols);
     float gm[V][8], bt[V][8];
     Raw8<X> raw[V];
     const long long step = (long long)gridDim.x * RPB;
@@ -132,7 +166,7 @@ __global__ __launch_bounds__(row_threads(TPR)) void ln_fwd_rows(LnFwdArgs a)
         if (r < a.rows)
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                raw[i] = load_raw8<X>((const typename X::raw *)a.x + r * a.ldx, (i * TPR + l) * 8, a.cols);
+                raw[i] = at.template load<X>((const typename X::raw *)a.x + r * a.ldx, i, a.cols);
     };
     fetch(row);
 #pragma unroll
@@ -143,29 +177,29 @@ __global__ __launch_bounds__(row_threads(TPR)) void ln_fwd_rows(LnFwdArgs a)
             bt[i][e] = 0.f;
         }
         if (a.gamma)
-            load8<Fp32>(a.gamma, (i * TPR + l) * 8, a.cols, gm[i]);
+            at.template unpack<Fp32>(at.template load<Fp32>(a.gamma, i, a.cols), i, a.cols, gm[i]);
         if (a.beta)
-            load8<Fp32>(a.beta, (i * TPR + l) * 8, a.cols, bt[i]);
+            at.template unpack<Fp32>(at.template load<Fp32>(a.beta, i, a.cols), i, a.cols, bt[i]);
     }
     for (; row < a.rows; row += step) {
         float v[V][8], s = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            unpack8<X>(raw[i], v[i]);
+            at.template unpack<X>(raw[i], i, a.cols, v[i]);
         fetch(row + step);
 #pragma unroll
         for (int i = 0; i < V; ++i)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                s += v[i][e];
+                s += !WINDOW || at.counts(i, e) ? v[i][e] : 0.f;
         const float mean = row_sum<TPR>(s, lds[0]) * inv;
         s = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                v[i][e] = (i * TPR + l) * 8 + e < a.cols ? v[i][e] - mean : 0.f;
-                s += v[i][e] * v[i][e];
+                v[i][e] = WINDOW || at.col[i] + e < a.cols ? v[i][e] - mean : 0.f;
+                s += !WINDOW || at.counts(i, e) ? v[i][e] * v[i][e] : 0.f;
             }
         const float rstd = 1.f / sqrtf(row_sum<TPR>(s, lds[1]) * inv + a.eps);
         if (l == 0) {
@@ -176,11 +210,11 @@ __global__ __launch_bounds__(row_threads(TPR)) void ln_fwd_rows(LnFwdArgs a)
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            // (past the row v, beta and so the result are 0)
+            // (in MXFP4's last block v, beta and so the result are 0 past the row)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 v[i][e] = v[i][e] * rstd * gm[i][e] + bt[i][e];
-            ln_emit<Y, (TPR < 16 ? TPR : 16)>(a, row, (i * TPR + l) * 8, v[i]);
+            ln_emit<Y, (TPR < 16 ? TPR : 16)>(a, row, at.col[i], v[i]);
         }
     }
 }
@@ -349,15 +383,17 @@ template <typename DY, typename X, int TPR, int V>
 __global__ __launch_bounds__(row_threads(TPR)) void ln_bwd_rows(LnBwdArgs a)
 {
     constexpr int RPB = row_threads(TPR) / TPR;
+    constexpr bool WINDOW = TPR > 4;
     __shared__ float lds[2][16][2];
     __shared__ float sums[TPR > 64 ? 1 : 4][2][TPR > 64 ? 1 : TPR * 8 * V];
     const int l = threadIdx.x % TPR;
     const float inv = 1.f / (float)a.cols;
+    const RowCols<TPR, V, WINDOW> at(l, a.cols);
     float gm[V][8], dg[V][8] = {}, db[V][8] = {};
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         if (a.gamma)
-            load8<Fp32>(a.gamma, (i * TPR + l) * 8, a.cols, gm[i]);
+            at.template unpack<Fp32>(at.template load<Fp32>(a.gamma, i, a.cols), i, a.cols, gm[i]);
         else
 #pragma unroll
             for (int e = 0; e < 8; ++e)
@@ -375,8 +411,8 @@ __global__ __launch_bounds__(row_threads(TPR)) void ln_bwd_rows(LnBwdArgs a)
         rstd = a.rstd[r];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            rx[i] = load_raw8<X>((const typename X::raw *)a.x + r * a.ldx, (i * TPR + l) * 8, a.cols);
-            rd[i] = load_raw8<DY>((const typename DY::raw *)a.dy + r * a.lddy, (i * TPR + l) * 8, a.cols);
+            rx[i] = at.template load<X>((const typename X::raw *)a.x + r * a.ldx, i, a.cols);
+            rd[i] = at.template load<DY>((const typename DY::raw *)a.dy + r * a.lddy, i, a.cols);
         }
     };
     fetch(row);
@@ -385,21 +421,21 @@ __global__ __launch_bounds__(row_threads(TPR)) void ln_bwd_rows(LnBwdArgs a)
         const float m = mean, r = rstd;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            unpack8<X>(rx[i], n[i]);
-            unpack8<DY>(rd[i], h[i]);
+            at.template unpack<X>(rx[i], i, a.cols, n[i]);
+            at.template unpack<DY>(rd[i], i, a.cols, h[i]);
         }
         fetch(row + step);
 #pragma unroll
         for (int i = 0; i < V; ++i)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                // (past the row h is 0 and n finite, unless the statistics are not)
-                n[i][e] = (i * TPR + l) * 8 + e < a.cols ? (n[i][e] - m) * r : 0.f;
+                // (past the row h is 0)
+                n[i][e] = WINDOW || at.col[i] + e < a.cols ? (n[i][e] - m) * r : 0.f;
                 dg[i][e] += h[i][e] * n[i][e];
                 db[i][e] += h[i][e];
                 h[i][e] *= gm[i][e];
-                s1 += h[i][e];
-                s2 += h[i][e] * n[i][e];
+                s1 += !WINDOW || at.counts(i, e) ? h[i][e] : 0.f;
+                s2 += !WINDOW || at.counts(i, e) ? h[i][e] * n[i][e] : 0.f;
             }
         row_sum2<TPR>(s1, s2, lds[k]);
         s1 *= inv;
@@ -409,8 +445,8 @@ __global__ __launch_bounds__(row_threads(TPR)) void ln_bwd_rows(LnBwdArgs a)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 h[i][e] = r * (h[i][e] - s1 - n[i][e] * s2);
-            if ((i * TPR + l) * 8 < a.cols)
-                store8_as(a.dx_dtype, a.dx, row, (i * TPR + l) * 8, a.cols, h[i]);
+            if (at.col[i] < a.cols)
+                store8_as(a.dx_dtype, a.dx, row, at.col[i], a.cols, h[i]);
         }
     }
     if (!a.part_g)
@@ -419,9 +455,9 @@ __global__ __launch_bounds__(row_threads(TPR)) void ln_bwd_rows(LnBwdArgs a)
     if constexpr (TPR > 64) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if ((i * TPR + l) * 8 < a.cols) {
-                store8<Fp32>(pg, (i * TPR + l) * 8, a.cols, dg[i]);
-                store8<Fp32>(pb, (i * TPR + l) * 8, a.cols, db[i]);
+            if (at.col[i] < a.cols) {
+                store8<Fp32>(pg, at.col[i], a.cols, dg[i]);
+                store8<Fp32>(pb, at.col[i], a.cols, db[i]);
             }
     } else {
         // the wave's row groups, then the four waves
@@ -431,8 +467,8 @@ __global__ __launch_bounds__(row_threads(TPR)) void ln_bwd_rows(LnBwdArgs a)
             for (int e = 0; e < 8; ++e) {
                 const float g = stride_sum<TPR>(dg[i][e]), b = stride_sum<TPR>(db[i][e]);
                 if ((threadIdx.x & 63) < TPR) {
-                    sums[threadIdx.x >> 6][0][(i * TPR + l) * 8 + e] = g;
-                    sums[threadIdx.x >> 6][1][(i * TPR + l) * 8 + e] = b;
+                    sums[threadIdx.x >> 6][0][at.col[i] + e] = g;
+                    sums[threadIdx.x >> 6][1][at.col[i] + e] = b;
                 }
             }
         __syncthreads();
@@ -584,7 +620,9 @@ int ln_fwd_call(const LnFwdArgs &a, int x_dtype, int y_dtype, hipStream_t stream
 // the partial sums (2 cols fp32 each, written and read) stay small beside
 // dy, x and dx.  A single one writes the gradients itself: so do up to four
 // groups of rows, for which a second launch (4 us) would cost more than the
-// other workgroups save.
+// other workgroups save.  512 workgroups of 256 threads, 256 of more (65536 x
+// 128 16.9 us, 17.8 with 1024; 65536 x 1024 75 us, 88 with 1024; 16384 x 4096
+// 79 us, 81 with 512; 8192 x 8192 81 us, 91 with 512).
 int ln_parts(long long rows, int cols)
 {
     int per = 1;
@@ -595,7 +633,7 @@ int ln_parts(long long rows, int cols)
     const long long groups = (rows + per - 1) / per;
     if (groups <= 4)
         return 1;
-    const int most = cols <= 512 ? 1024 : cols <= 8192 ? 512 : 256;
+    const int most = cols <= 2048 || cols > 8192 ? 512 : 256;
     return (int)(groups < most ? groups : most);
 }
 

@@ -84,7 +84,7 @@ __global__ __launch_bounds__(kMxFewWaves * 64) void mx_gemm_few(MxFewArgs g)
     auto quantise = [&](int i, const Raw8<X> &r) {
         const int m = i / per, c = (i - m * per) * nt + threadIdx.x * 8;
         float v[8];
-        unpack8<X>(r, v);
+        unpack8<X>(tail8<X>(r, c, g.K), v);
         unsigned top = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e)

@@ -58,7 +58,7 @@ __global__ __launch_bounds__(kMxThreads) void mx_quantize_rows(MxQuantArgs a)
             if (c >= end)      // (lanes of 128 columns agree on this)
                 break;
             float v[8];
-            unpack8<T>(raw[u], v);
+            unpack8<T>(tail8<T>(raw[u], c, a.cols), v);
             unsigned top = 0;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
@@ -156,6 +156,9 @@ __device__ __forceinline__ void mx_quantize_tile(const MxTileArgs &a, unsigned t
                 raw[p] = load_raw8<T>((const typename T::raw *)a.x + (long long)(r0 + lr + p * LR) * a.ldx, c0 + lc,
                                       a.cols);
         }
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p)
+            raw[p] = tail8<T>(raw[p], c0 + lc, a.cols);
     }
 #pragma unroll
     for (int p = 0; p < PASSES; ++p)

@@ -81,19 +81,24 @@ struct Raw8 {
     u32v4_t w[T::code == CONVIMG_FP32 ? 2 : 1];
 };
 
-// The first is element `col`; of the eight those below `cols` exist, the
-// others read as 0.
-template <typename T>
+// Loads the eight from element `col` of a row of `cols`.  At the end of the
+// row, the row's last eight elements instead, which keeps the load whole (a
+// lane that loads single elements waits for them, and so for everything that
+// the wave has in flight); tail8 moves them into place when they are used.
+// Nothing is loaded past the row.  SHORT: rows may have fewer than eight.
+template <typename T, bool SHORT = true>
 __device__ __forceinline__ Raw8<T> load_raw8(const typename T::raw *row, int col, int cols)
 {
-    Raw8<T> r;
-    if (col + 8 <= cols) {
-        if constexpr (T::code == CONVIMG_FP32) {
-            const u32v4_a4_t *p = (const u32v4_a4_t *)(row + col);
-            r.w[0] = p[0];
-            r.w[1] = p[1];
-        } else {
-            r.w[0] = *(const u32v4_a2_t *)(row + col);
+    Raw8<T> r = {};
+    if (!SHORT || cols >= 8) {
+        if (col < cols) {
+            const typename T::raw *p = row + min(col, cols - 8);
+            if constexpr (T::code == CONVIMG_FP32) {
+                r.w[0] = ((const u32v4_a4_t *)p)[0];
+                r.w[1] = ((const u32v4_a4_t *)p)[1];
+            } else {
+                r.w[0] = *(const u32v4_a2_t *)p;
+            }
         }
         return r;
     }
@@ -105,6 +110,32 @@ __device__ __forceinline__ Raw8<T> load_raw8(const typename T::raw *row, int col
             e[k] = row[col + k];
     }
     __builtin_memcpy(&r, e, sizeof(r));
+    return r;
+}
+
+// What load_raw8 loaded, element `col` first and zeros past the row.
+template <typename T, bool SHORT = true>
+__device__ __forceinline__ Raw8<T> tail8(Raw8<T> r, int col, int cols)
+{
+    if ((cols & 7) == 0 || (SHORT && cols < 8))
+        return r;
+    const int past = col < cols ? max(col + 8 - cols, 0) : 0;      // elements to move down by
+    constexpr int W = sizeof(r) / 4;
+    unsigned w[W + 1];
+    w[W] = 0;
+    __builtin_memcpy(w, &r, sizeof(r));
+    // (by 4, 2 and 1 elements; for 16-bit types 2, 1 and half a word)
+#pragma unroll
+    for (int e = 4; e >= 1; e >>= 1) {
+        const bool on = (past & e) != 0;
+        const int n = e * W / 8;
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            const unsigned v = n > 0 ? (i + n < W ? w[i + n] : 0u) : (w[i] >> 16) | (w[i + 1] << 16);
+            w[i] = on ? v : w[i];
+        }
+    }
+    __builtin_memcpy(&r, w, sizeof(r));
     return r;
 }
 
@@ -131,10 +162,10 @@ __device__ __forceinline__ void unpack8(const Raw8<T> &r, float (&v)[8])
     }
 }
 
-template <typename T>
+template <typename T, bool SHORT = true>
 __device__ __forceinline__ void load8(const typename T::raw *row, int col, int cols, float (&v)[8])
 {
-    unpack8<T>(load_raw8<T>(row, col, cols), v);
+    unpack8<T>(tail8<T, SHORT>(load_raw8<T, SHORT>(row, col, cols), col, cols), v);
 }
 
 template <typename T>
