@@ -198,28 +198,43 @@ __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsign
         }
     };
 
-    // The sums start from the bias.
+    // The first K tile's copies, the bias (the sums start from it), the others'.
+#pragma unroll
+    for (int c = 0; c < PER; ++c)
+        issue1(t0, c);
     f32x16_t acc[FM][FN];
     {
-        const __amdgpu_buffer_rsrc_t rbias =
-            __builtin_amdgcn_make_buffer_rsrc((void *)g.bias, 0, g.bias ? (unsigned)g.N * 4u : 0u, kMxRsrcWord3);
+        const __amdgpu_buffer_rsrc_t rbias = __builtin_amdgcn_make_buffer_rsrc(
+            (void *)g.bias, 0, g.bias && group == 0 ? (unsigned)g.N * 4u : 0u, kMxRsrcWord3);
+        const int n = n0 + wn * TN + half * 4;
+        if (n0 + BN <= g.N) {
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
+            for (int j = 0; j < FN; ++j)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int n = n0 + wn * TN + j * 32 + (e >> 2) * 8 + half * 4 + (e & 3);
-                acc[0][j][e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
-                    rbias, n < g.N && group == 0 ? n * 4u : kMxOutOfRange, 0, 0));
-            }
+                for (int q = 0; q < 4; ++q) {
+                    const u32v4_t v = __builtin_amdgcn_raw_buffer_load_b128(rbias, (n + j * 32 + q * 8) * 4u, 0, 0);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        acc[0][j][4 * q + e] = __uint_as_float(v[e]);
+                }
+        } else {
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int c = n + j * 32 + (e >> 2) * 8 + (e & 3);
+                    acc[0][j][e] = __uint_as_float(
+                        __builtin_amdgcn_raw_buffer_load_b32(rbias, c < g.N ? c * 4u : kMxOutOfRange, 0, 0));
+                }
+        }
 #pragma unroll
         for (int i = 1; i < FM; ++i)
 #pragma unroll
             for (int j = 0; j < FN; ++j)
                 acc[i][j] = acc[0][j];
     }
-
 #pragma unroll
-    for (int t = 0; t < STAGES; ++t)
+    for (int t = 1; t < STAGES; ++t)
 #pragma unroll
         for (int c = 0; c < (t < STAGES - 1 ? PER : E0); ++c)
             issue1(t0 + t, c);
@@ -304,8 +319,8 @@ __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsign
         __atomic_signal_fence(__ATOMIC_SEQ_CST);
     } while (++t < t0 + nk);
 
-    // Rows of the output through LDS, 32 at a time and wave, so that stores
-    // are 16 bytes a lane along the row.
+    // Rows of the output through LDS, as many blocks of 32 a wave as it holds,
+    // so that stores are 16 bytes a lane along the row.
     mx_wait_vm<0>();
     mx_wait_lds();
     mx_barrier();
@@ -340,48 +355,59 @@ __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsign
         if (group > 0)
             return;
     }
-    unsigned char *mine = lds + wave * 32 * PITCH;
     constexpr int CHUNKS = TN * OS / 16, EPC = 16 / OS;      // 16-byte chunks a row, elements a chunk
+    constexpr int RP = 64 / CHUNKS;                          // rows a wave instruction
+    constexpr int FIT = STAGES * STAGE / (NW * 32 * PITCH), G = FIT < 1 ? 1 : FIT < FM ? FIT : FM;      // blocks at once
+    static_assert(FM % G == 0 || G == 1, "whole groups");
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
+    for (int i0 = 0; i0 < FM; i0 += G) {
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
+        for (int i = 0; i < G; ++i) {
+            unsigned char *mine = lds + (i * NW + wave) * 32 * PITCH;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                unsigned char *p = mine + l32 * PITCH + (j * 32 + q * 8 + half * 4) * OS;
-                const float *v = (const float *)&acc[i][j] + q * 4;
-                if constexpr (OS == 4)
-                    *(f32x4_t *)p = f32x4_t{v[0], v[1], v[2], v[3]};
-                else if constexpr (O::code == CONVIMG_BF16)
-                    *(uint2 *)p = uint2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-                else
-                    *(uint2 *)p = uint2{pack_fp16(v[0], v[1]), pack_fp16(v[2], v[3])};
-            }
-        mx_wait_lds();
-        __builtin_amdgcn_wave_barrier();
-        constexpr int RP = 64 / CHUNKS;      // rows a wave instruction
-        const int k = lane % CHUNKS, n = n0 + wn * TN + k * EPC;
-        const int rows = min(g.M - m0 - wm * TM - i * 32, 32);
-        typename O::raw *o = (typename O::raw *)g.out + (long long)(m0 + wm * TM + i * 32) * g.N + n;
-        if (n + EPC <= g.N) {
+            for (int j = 0; j < FN; ++j)
 #pragma unroll
-            for (int p = 0; p < 32 / RP; ++p) {
-                const int r = p * RP + lane / CHUNKS;
-                const u32v4_t v = *(const u32v4_t *)(mine + r * PITCH + k * 16);
-                if (r < rows) {
+                for (int q = 0; q < 4; ++q) {
+                    unsigned char *p = mine + l32 * PITCH + (j * 32 + q * 8 + half * 4) * OS;
+                    const float *v = (const float *)&acc[i0 + i][j] + q * 4;
                     if constexpr (OS == 4)
-                        *(u32v4_a4_t *)(o + (long long)r * g.N) = v;
+                        *(f32x4_t *)p = f32x4_t{v[0], v[1], v[2], v[3]};
+                    else if constexpr (O::code == CONVIMG_BF16)
+                        *(uint2 *)p = uint2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
                     else
-                        *(u32v4_a2_t *)(o + (long long)r * g.N) = v;
+                        *(uint2 *)p = uint2{pack_fp16(v[0], v[1]), pack_fp16(v[2], v[3])};
                 }
-            }
-        } else if (n < g.N) {
-            for (int r = lane / CHUNKS; r < rows; r += RP)
-                for (int e = 0; n + e < g.N; ++e)
-                    o[(long long)r * g.N + e] = ((const typename O::raw *)(mine + r * PITCH + k * 16))[e];
         }
         mx_wait_lds();
         __builtin_amdgcn_wave_barrier();
+        const int k = lane % CHUNKS, n = n0 + wn * TN + k * EPC;
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            const unsigned char *mine = lds + (i * NW + wave) * 32 * PITCH;
+            const int m = m0 + wm * TM + (i0 + i) * 32, rows = min(g.M - m, 32);
+            typename O::raw *o = (typename O::raw *)g.out + (long long)m * g.N + n;
+            if (n + EPC <= g.N) {
+#pragma unroll
+                for (int p = 0; p < 32 / RP; ++p) {
+                    const int r = p * RP + lane / CHUNKS;
+                    const u32v4_t v = *(const u32v4_t *)(mine + r * PITCH + k * 16);
+                    if (r < rows) {
+                        if constexpr (OS == 4)
+                            *(u32v4_a4_t *)(o + (long long)r * g.N) = v;
+                        else
+                            *(u32v4_a2_t *)(o + (long long)r * g.N) = v;
+                    }
+                }
+            } else if (n < g.N) {
+                for (int r = lane / CHUNKS; r < rows; r += RP)
+                    for (int e = 0; n + e < g.N; ++e)
+                        o[(long long)r * g.N + e] = ((const typename O::raw *)(mine + r * PITCH + k * 16))[e];
+            }
+        }
+        if (i0 + G < FM) {
+            mx_wait_lds();
+            __builtin_amdgcn_wave_barrier();
+        }
     }
 }
 
