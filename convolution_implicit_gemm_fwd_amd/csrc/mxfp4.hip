@@ -93,6 +93,10 @@ auto tiles_of(int M, int N)
 //     that one stores while others load: 8192x8192x256 30.5 us against 38.3 in
 //     256 x 256, x512 38.1 against 42.1, x1024 59.9 against 55.6; 3136x2048x512
 //     (400 tiles) 8.7 against 8.3 in the longer stages.
+//   Where K is at most 2048 and the last round of 256 x 256 tiles would leave
+//     more than 15 % of all rounds idle, 128 x 128, which overlap anyway:
+//     7000x7000x1000 47.5 us against 61.0, 6000x6000x2000 62.4 against 65.6;
+//     without that rest 8192x4096x2048 48.5 against 48.0.
 enum Shape { k256, k128, k128Short, k128x64, k64, k64x32, k32 };
 
 template <typename C>
@@ -101,7 +105,8 @@ Shape shape_of(C &&count, int kb)
     const long long n = count(128, 128);
     if (n >= 192 && (kb <= 8 || (kb <= 16 && n >= 2048)))
         return k128Short;
-    if (count(256, 256) >= 144)
+    const long long big = count(256, 256), rounds = (big + 255) / 256;
+    if (big >= 144 && !(kb <= 64 && n >= 1024 && big * 100 < rounds * 256 * 85))
         return k256;
     if (n >= 192)
         return k128;
