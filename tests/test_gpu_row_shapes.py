@@ -24,7 +24,8 @@ def _gpu():
 
 # tiles of 256, of 128, 128 x 64 with two groups of waves, 64, 64 x 32 and 32 with four groups; K that fills the last
 # K tile, ends inside it, inside a scale dword, or leaves the last groups nothing
-@pytest.mark.parametrize("M,N,K", [(3100, 3100, 1030), (4200, 4150, 300), (3100, 3100, 256), (3073, 3201, 130), (1800, 1700, 288), (1667, 2000, 1000), (500, 4099, 1056),
+@pytest.mark.parametrize("M,N,K", [(3100, 3100, 1030), (4200, 4150, 300), (3100, 3100, 256), (3073, 3201, 130), (1800, 1700, 288),
+                                   (1667, 2000, 1000), (500, 4099, 1056),
                                    (1000, 1600, 1250), (900, 900, 513), (129, 6500, 2050), (65, 4100, 1100), (40, 8100, 1030),
                                    (33, 300, 4127), (7, 50, 1057), (256, 129, 8200), (5, 33, 33000)])
 def test_linear_shapes(M, N, K):
