@@ -3,9 +3,13 @@ linear layer, on channels-last tensors [..., C].
 
 Every dimension before the last is a row index; the last dimension must be
 contiguous and the rows evenly spaced (any NHWC tensor, or a column slice of
-a matrix).  Calls run on ``stream`` (default: torch's current stream of the
-first tensor's device) without waiting; torch supplies device memory and the
-stream only.
+a matrix).  Calls run on ``stream`` (a stream's handle; default: torch's current
+stream of the first tensor's device) without waiting; torch supplies device
+memory and the stream only.  A call on another stream than the current one is
+made as under ``torch.cuda.stream``: its outputs and workspace come from that
+stream's memory, and the caller orders that stream behind whatever made the
+inputs, keeps the inputs until it has run the call, and orders what reads the
+outputs behind it.
 
 A small call costs the host more than the GPU (a launch is about 3 us, the
 kernel of one 4096-wide token 2 us), so the common case (tensors as they
@@ -136,14 +140,30 @@ def _fail(name, rc):
     raise RuntimeError("%s failed: %s (status %d)" % (name, abi.conv2d_strerror(rc), rc))
 
 
-def _hold(device, stream, *tensors):
-    """Tensors allocated on torch's current stream and used on another: the
-    allocator must not hand the memory out before that stream is done."""
-    if stream != _stream(device.index):
-        ext = _torch.cuda.ExternalStream(stream, device=device)
-        for t in tensors:
-            if t is not None:
-                t.record_stream(ext)
+def _on(stream, t, f, *args):
+    """The call on the stream of this handle, where that is not the current one
+    of t's device with the stream made the current one: a block of the present
+    current stream's memory may be in use by work that is still queued there.
+    The results go back to that stream, so their memory is not used again
+    before it is past them."""
+    if not t.is_cuda:
+        return f(*args)        # (refused there)
+    device = t.device
+    if _device() != device.index:
+        return _elsewhere(device, _on, stream, t, f, *args)
+    if stream == _stream(device.index):
+        return f(*args)
+    # (set and set back: 4 us less than torch.cuda.stream, which looks up the device and the stream twice)
+    home = _torch.cuda.current_stream(device.index)
+    _torch.cuda.set_stream(_torch.cuda.ExternalStream(stream, device=device))
+    try:
+        r = f(*args)
+    finally:
+        _torch.cuda.set_stream(home)
+    for o in r if isinstance(r, tuple) else (r,):
+        if isinstance(o, _torch.Tensor):
+            o.record_stream(home)
+    return r
 
 
 def _same_device(device, t, what):
@@ -161,14 +181,15 @@ def layer_norm_nhwc(x, gamma=None, beta=None, eps=1e-5, out_dtype=None, stats=Fa
     """
     if _torch is None:
         _setup()
-    if stream is None:
-        r = _fast.layer_norm(x, gamma, beta, eps, out_dtype, stats)
-        if r is not None:
-            return r
+    if stream is not None:
+        return _on(stream, x, layer_norm_nhwc, x, gamma, beta, eps, out_dtype, stats)
+    r = _fast.layer_norm(x, gamma, beta, eps, out_dtype, stats)
+    if r is not None:
+        return r
     rows, cols, ld = _rows_of(x, "x")
     dev = x.device
     if _device() != dev.index:
-        return _elsewhere(dev, layer_norm_nhwc, x, gamma, beta, eps, out_dtype, stats, stream)
+        return _elsewhere(dev, layer_norm_nhwc, x, gamma, beta, eps, out_dtype, stats)
     if out_dtype is None:
         out_dtype = x.dtype
     xd, yd = _dtype(x.dtype, "x"), _dtype(out_dtype, "out_dtype")
@@ -180,11 +201,9 @@ def layer_norm_nhwc(x, gamma=None, beta=None, eps=1e-5, out_dtype=None, stats=Fa
         rstd = _torch.empty_like(mean)
         mp, rp = mean.data_ptr(), rstd.data_ptr()
     rc = _lib.layer_norm_fwd(x.data_ptr(), ld, g, b, rows, cols, eps, xd, yd, y.data_ptr(), mp, rp,
-                             _stream(dev.index) if stream is None else stream)
+                             _stream(dev.index))
     if rc:
         _fail("layer_norm_fwd", rc)
-    if stream is not None:
-        _hold(dev, stream, y, mean, rstd)
     return (y, mean, rstd) if stats else y
 
 
@@ -199,23 +218,22 @@ def layer_norm_mxfp4_nhwc(x, gamma=None, beta=None, eps=1e-5, stream=None):
     ``Mxfp4Tensor``, the input of ``mxfp4_linear_nhwc``."""
     if _torch is None:
         _setup()
-    if stream is None:
-        r = _fast.layer_norm_mxfp4(x, gamma, beta, eps)
-        if r is not None:
-            return _new(Mxfp4Tensor, r)
+    if stream is not None:
+        return _on(stream, x, layer_norm_mxfp4_nhwc, x, gamma, beta, eps)
+    r = _fast.layer_norm_mxfp4(x, gamma, beta, eps)
+    if r is not None:
+        return _new(Mxfp4Tensor, r)
     rows, cols, ld = _rows_of(x, "x")
     dev = x.device
     if _device() != dev.index:
-        return _elsewhere(dev, layer_norm_mxfp4_nhwc, x, gamma, beta, eps, stream)
+        return _elsewhere(dev, layer_norm_mxfp4_nhwc, x, gamma, beta, eps)
     xd = _dtype(x.dtype, "x")
     g, b = _param(gamma, cols, dev, "gamma"), _param(beta, cols, dev, "beta")
     q = _packed(dev, rows, cols)
     rc = _lib.layer_norm_fwd_mxfp4(x.data_ptr(), ld, g, b, rows, cols, eps, xd, q.codes.data_ptr(),
-                                   q.scales.data_ptr(), None, None, _stream(dev.index) if stream is None else stream)
+                                   q.scales.data_ptr(), None, None, _stream(dev.index))
     if rc:
         _fail("layer_norm_fwd_mxfp4", rc)
-    if stream is not None:
-        _hold(dev, stream, q.codes, q.scales)
     return q
 
 
@@ -228,10 +246,11 @@ def layer_norm_bwd_nhwc(dy, x, gamma, mean, rstd, dx_dtype=None, stream=None):
     """
     if _torch is None:
         _setup()
-    if stream is None:
-        r = _fast.layer_norm_bwd(dy, x, gamma, mean, rstd, dx_dtype)
-        if r is not None:
-            return r
+    if stream is not None:
+        return _on(stream, x, layer_norm_bwd_nhwc, dy, x, gamma, mean, rstd, dx_dtype)
+    r = _fast.layer_norm_bwd(dy, x, gamma, mean, rstd, dx_dtype)
+    if r is not None:
+        return r
     rows, cols, ld = _rows_of(x, "x")
     dev = x.device
     if dy.shape != x.shape:
@@ -239,7 +258,7 @@ def layer_norm_bwd_nhwc(dy, x, gamma, mean, rstd, dx_dtype=None, stream=None):
     ldy = _rows_of(dy, "dy")[2]
     _same_device(dev, dy, "dy")
     if _device() != dev.index:
-        return _elsewhere(dev, layer_norm_bwd_nhwc, dy, x, gamma, mean, rstd, dx_dtype, stream)
+        return _elsewhere(dev, layer_norm_bwd_nhwc, dy, x, gamma, mean, rstd, dx_dtype)
     if dx_dtype is None:
         dx_dtype = x.dtype
     dd, xd, od = _dtype(dy.dtype, "dy"), _dtype(x.dtype, "x"), _dtype(dx_dtype, "dx_dtype")
@@ -252,11 +271,9 @@ def layer_norm_bwd_nhwc(dy, x, gamma, mean, rstd, dx_dtype=None, stream=None):
     ws = _empty(need, dtype=_u8, device=dev)
     rc = _lib.layer_norm_bwd(dy.data_ptr(), ldy, x.data_ptr(), ld, g, m, r, rows, cols, dd, xd, od, dx.data_ptr(),
                              dgamma.data_ptr(), dbeta.data_ptr(), ws.data_ptr(), need,
-                             _stream(dev.index) if stream is None else stream)
+                             _stream(dev.index))
     if rc:
         _fail("layer_norm_bwd", rc)
-    if stream is not None:
-        _hold(dev, stream, dx, dgamma, dbeta, ws)
     return dx, dgamma, dbeta
 
 
@@ -265,22 +282,21 @@ def mxfp4_quantize_nhwc(x, transpose=False, stream=None):
     its transpose, so that blocks of 32 run down the columns of x."""
     if _torch is None:
         _setup()
-    if stream is None:
-        r = _fast.quantize(x, transpose)
-        if r is not None:
-            return _new(Mxfp4Tensor, r)
+    if stream is not None:
+        return _on(stream, x, mxfp4_quantize_nhwc, x, transpose)
+    r = _fast.quantize(x, transpose)
+    if r is not None:
+        return _new(Mxfp4Tensor, r)
     rows, cols, ld = _rows_of(x, "x")
     dev = x.device
     if _device() != dev.index:
-        return _elsewhere(dev, mxfp4_quantize_nhwc, x, transpose, stream)
+        return _elsewhere(dev, mxfp4_quantize_nhwc, x, transpose)
     xd = _dtype(x.dtype, "x")
     q = _packed(dev, cols, rows) if transpose else _packed(dev, rows, cols)
     rc = _lib.mxfp4_quantize(x.data_ptr(), ld, rows, cols, xd, 1 if transpose else 0, q.codes.data_ptr(),
-                             q.scales.data_ptr(), _stream(dev.index) if stream is None else stream)
+                             q.scales.data_ptr(), _stream(dev.index))
     if rc:
         _fail("mxfp4_quantize", rc)
-    if stream is not None:
-        _hold(dev, stream, q.codes, q.scales)
     return q
 
 
@@ -297,23 +313,22 @@ def mxfp4_dequantize_nhwc(q, dtype, stream=None):
     """The values [rows, cols] that packed rows stand for, in ``dtype``."""
     if _torch is None:
         _setup()
-    if stream is None:
-        r = _fast.dequantize(q, dtype)
-        if r is not None:
-            return r
+    if stream is not None:
+        return _on(stream, q[0], mxfp4_dequantize_nhwc, q, dtype)
+    r = _fast.dequantize(q, dtype)
+    if r is not None:
+        return r
     _check_packed(q, "q")
     d = _dtype(dtype, "dtype")
     codes, scales, rows, cols = q
     dev = codes.device
     if _device() != dev.index:
-        return _elsewhere(dev, mxfp4_dequantize_nhwc, q, dtype, stream)
+        return _elsewhere(dev, mxfp4_dequantize_nhwc, q, dtype)
     out = _empty(rows, cols, dtype=dtype, device=dev)
     rc = _lib.mxfp4_dequantize(codes.data_ptr(), scales.data_ptr(), rows, cols, d, out.data_ptr(),
-                               _stream(dev.index) if stream is None else stream)
+                               _stream(dev.index))
     if rc:
         _fail("mxfp4_dequantize", rc)
-    if stream is not None:
-        _hold(dev, stream, out)
     return out
 
 
@@ -327,15 +342,16 @@ def mxfp4_linear_nhwc(x, w, bias=None, out_dtype=None, stream=None):
     """
     if _torch is None:
         _setup()
-    if stream is None:
-        r = _fast.linear(x, w, bias, out_dtype)
-        if r is not None:
-            return r
+    if stream is not None:
+        return _on(stream, w[0], mxfp4_linear_nhwc, x, w, bias, out_dtype)
+    r = _fast.linear(x, w, bias, out_dtype)
+    if r is not None:
+        return r
     _check_packed(w, "w")
     codes, scales, N, wk = w
     dev = codes.device
     if _device() != dev.index:
-        return _elsewhere(dev, mxfp4_linear_nhwc, x, w, bias, out_dtype, stream)
+        return _elsewhere(dev, mxfp4_linear_nhwc, x, w, bias, out_dtype)
     if isinstance(x, Mxfp4Tensor):
         _check_packed(x, "x")
         xc, xs, M, K = x
@@ -357,11 +373,9 @@ def mxfp4_linear_nhwc(x, w, bias=None, out_dtype=None, stream=None):
     out = _empty(*shape, dtype=out_dtype, device=dev)
     ws = _empty(need, dtype=_u8, device=dev) if need else None
     rc = _lib.mxfp4_linear_fwd(xp, ld, sp, xd, codes.data_ptr(), scales.data_ptr(), b, M, N, K, od, out.data_ptr(),
-                               ws.data_ptr() if need else None, need, _stream(dev.index) if stream is None else stream)
+                               ws.data_ptr() if need else None, need, _stream(dev.index))
     if rc:
         _fail("mxfp4_linear_fwd", rc)
-    if stream is not None:
-        _hold(dev, stream, out, ws)
     return out
 
 
@@ -374,10 +388,11 @@ def mxfp4_linear_bwd_nhwc(dy, x, w, dx_dtype=None, stream=None):
     """
     if _torch is None:
         _setup()
-    if stream is None:
-        r = _fast.linear_bwd(dy, x, w, dx_dtype)
-        if r is not None:
-            return r
+    if stream is not None:
+        return _on(stream, dy, mxfp4_linear_bwd_nhwc, dy, x, w, dx_dtype)
+    r = _fast.linear_bwd(dy, x, w, dx_dtype)
+    if r is not None:
+        return r
     M, N, ldy = _rows_of(dy, "dy")
     mx, K, ldx = _rows_of(x, "x")
     if w.dim() != 2 or mx != M or dy.shape[:-1] != x.shape[:-1] or w.shape != (N, K):
@@ -389,7 +404,7 @@ def mxfp4_linear_bwd_nhwc(dy, x, w, dx_dtype=None, stream=None):
     _same_device(dev, x, "x")
     _same_device(dev, w, "w")
     if _device() != dev.index:
-        return _elsewhere(dev, mxfp4_linear_bwd_nhwc, dy, x, w, dx_dtype, stream)
+        return _elsewhere(dev, mxfp4_linear_bwd_nhwc, dy, x, w, dx_dtype)
     if dx_dtype is None:
         dx_dtype = x.dtype
     dd, xd, od = _dtype(dy.dtype, "dy"), _dtype(x.dtype, "x"), _dtype(dx_dtype, "dx_dtype")
@@ -399,9 +414,7 @@ def mxfp4_linear_bwd_nhwc(dy, x, w, dx_dtype=None, stream=None):
     ws = _empty(need, dtype=_u8, device=dev)
     rc = _lib.mxfp4_linear_bwd(dy.data_ptr(), ldy, dd, x.data_ptr(), ldx, w.data_ptr(), ldw, xd, M, N, K, od,
                                dx.data_ptr(), dw.data_ptr(), db.data_ptr(), ws.data_ptr(), need,
-                               _stream(dev.index) if stream is None else stream)
+                               _stream(dev.index))
     if rc:
         _fail("mxfp4_linear_bwd", rc)
-    if stream is not None:
-        _hold(dev, stream, dx, dw, db, ws)
     return dx, dw, db

@@ -1,0 +1,106 @@
+"""What the row operators' torch wrappers hand to the C library, on the CPU: a stand-in for the library records the
+addresses it gets, tensors of host memory pass for device tensors, and a stand-in for torch's streams tells which one is
+current."""
+import ctypes
+import gc
+import types
+
+import pytest
+import torch
+
+from convolution_implicit_gemm_fwd_amd import rows as R
+
+HOME, SIDE = 0, 0x5000      # stream handles
+
+
+class Dev(torch.Tensor):
+    """A host tensor that passes for a device tensor."""
+    is_cuda = property(lambda self: True)
+
+    def record_stream(self, stream):
+        Dev.recorded.append((self.data_ptr(), stream.cuda_stream))
+
+
+def dev(t):
+    return t.as_subclass(Dev)
+
+
+class Stream:
+    def __init__(self, cuda_stream, device=None):
+        self.cuda_stream = cuda_stream
+
+
+class Machine:
+    """Streams, allocations and library calls as the wrappers make them."""
+
+    def __init__(self, monkeypatch):
+        self.current, self.made, self.calls = HOME, {}, []
+        Dev.recorded = []
+        machine = self
+
+        def set_stream(stream):
+            machine.current = stream.cuda_stream
+
+        def made(t):
+            t = dev(t)
+            self.made[t.data_ptr()] = self.current
+            return t
+
+        cuda = types.SimpleNamespace(set_stream=set_stream, ExternalStream=Stream, device=None,
+                                     current_stream=lambda device=None: Stream(self.current))
+        R._torch or R._setup()
+        for name, value in dict(
+                _torch=types.SimpleNamespace(cuda=cuda, empty_like=lambda t, dtype=None: made(torch.empty_like(t, dtype=dtype)),
+                                             Tensor=torch.Tensor, bfloat16=torch.bfloat16),
+                _empty=lambda *a, **k: made(torch.empty(*a, **k)), _device=lambda: None, _stream=lambda index: self.current,
+                _fast=types.SimpleNamespace(**{n: lambda *a: None for n in (
+                    "layer_norm", "layer_norm_mxfp4", "layer_norm_bwd", "quantize", "dequantize", "linear", "linear_bwd")}),
+                _lib=types.SimpleNamespace(**{n: self.entry(n) for n in (
+                    "layer_norm_fwd", "layer_norm_fwd_mxfp4", "layer_norm_bwd", "mxfp4_quantize", "mxfp4_dequantize",
+                    "mxfp4_linear_fwd", "mxfp4_linear_bwd")})).items():
+            monkeypatch.setattr(R, name, value)
+
+    def entry(self, name):
+        def call(*args):
+            self.calls.append((name, args))
+            return self.check(name, args) or 0
+        return call
+
+    def check(self, name, args):
+        pass
+
+
+@pytest.fixture
+def machine(monkeypatch):
+    return Machine(monkeypatch)
+
+
+def calls():
+    x, w, dy = dev(torch.ones(300, 256)), dev(torch.ones(128, 256)), dev(torch.ones(300, 128))
+    mean, rstd = dev(torch.ones(300)), dev(torch.ones(300))
+    q = R.Mxfp4Tensor(dev(torch.zeros(128, 128, dtype=torch.uint8)), dev(torch.zeros(2, 128, 4, dtype=torch.uint8)), 128, 256)
+    return [lambda **s: R.layer_norm_nhwc(x, stats=True, **s), lambda **s: R.layer_norm_mxfp4_nhwc(x, **s),
+            lambda **s: R.layer_norm_bwd_nhwc(x, x, None, mean, rstd, **s), lambda **s: R.mxfp4_quantize_nhwc(x, **s),
+            lambda **s: R.mxfp4_dequantize_nhwc(q, torch.float32, **s), lambda **s: R.mxfp4_linear_nhwc(x, q, **s),
+            lambda **s: R.mxfp4_linear_nhwc(q, q, **s), lambda **s: R.mxfp4_linear_bwd_nhwc(dy, x, w, **s)]
+
+
+def tensors(r):
+    return [r] if isinstance(r, torch.Tensor) else [t for v in r if not isinstance(v, int) for t in tensors(v)]
+
+
+@pytest.mark.parametrize("k", range(8))
+def test_buffers_of_another_stream_are_its_own(machine, k):
+    """A block of the current stream's pool may still be in use by work that is queued there: what a call on another
+    stream writes comes from that stream's pool, and the results are not reused before the current stream is past them."""
+    call = calls()[k]
+    out = tensors(call(stream=SIDE))
+    assert machine.calls[-1][1][-1] == SIDE
+    assert machine.made and set(machine.made.values()) == {SIDE}
+    assert {(t.data_ptr(), HOME) for t in out} <= set(Dev.recorded)
+    assert machine.current == HOME
+    machine.made.clear()
+    Dev.recorded.clear()
+    for s in (None, HOME):
+        call(stream=s)
+        assert machine.calls[-1][1][-1] == HOME and set(machine.made.values()) == {HOME} and not Dev.recorded
