@@ -241,8 +241,9 @@ def layer_norm_bwd_nhwc(dy, x, gamma, mean, rstd, dx_dtype=None, stream=None):
     """(dx, dgamma, dbeta): gradients of layer_norm_nhwc.
 
     dy, x: [..., C] of one shape, each bfloat16, float16 or float32; gamma:
-    float32 [C] or None; mean, rstd: the forward's statistics.  dx: contiguous,
-    in ``dx_dtype`` (default: x's dtype); dgamma and dbeta: float32 [C].
+    float32 [C] or None; mean, rstd: the forward's statistics, float32 in any
+    layout (copied if they are not contiguous).  dx: contiguous, in
+    ``dx_dtype`` (default: x's dtype); dgamma and dbeta: float32 [C].
     """
     if _torch is None:
         _setup()
@@ -263,8 +264,9 @@ def layer_norm_bwd_nhwc(dy, x, gamma, mean, rstd, dx_dtype=None, stream=None):
         dx_dtype = x.dtype
     dd, xd, od = _dtype(dy.dtype, "dy"), _dtype(x.dtype, "x"), _dtype(dx_dtype, "dx_dtype")
     g = _param(gamma, cols, dev, "gamma")
-    m = _param(mean if mean.dim() == 1 else mean.reshape(-1), rows, dev, "mean")
-    r = _param(rstd if rstd.dim() == 1 else rstd.reshape(-1), rows, dev, "rstd")
+    # (held until the call is made: each may be a copy)
+    mean, rstd = mean.reshape(-1).contiguous(), rstd.reshape(-1).contiguous()
+    m, r = _param(mean, rows, dev, "mean"), _param(rstd, rows, dev, "rstd")
     need = _norm_bwd_bytes(rows, cols)
     dx = _like(x, dx_dtype)
     dgamma, dbeta = _empty(cols, dtype=_f32, device=dev), _empty(cols, dtype=_f32, device=dev)

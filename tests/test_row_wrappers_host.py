@@ -104,3 +104,38 @@ def test_buffers_of_another_stream_are_its_own(machine, k):
     for s in (None, HOME):
         call(stream=s)
         assert machine.calls[-1][1][-1] == HOME and set(machine.made.values()) == {HOME} and not Dev.recorded
+
+
+def held(address):
+    """Whether a tensor that is still held covers the address."""
+    return any(isinstance(t, torch.Tensor) and t.data_ptr() <= address < t.data_ptr() + max(1, t.numel() * t.element_size())
+               for t in gc.get_objects() if isinstance(t, torch.Tensor) and t.device.type == "cpu")
+
+
+def floats(address, n):
+    return list((ctypes.c_float * n).from_address(address))
+
+
+@pytest.mark.parametrize("stream", [None, SIDE])
+@pytest.mark.parametrize("lay", [lambda t: t, lambda t: t.t().contiguous().t(), lambda t: torch.stack((t, t), -1)[..., 1],
+                                 lambda t: torch.cat((t, t), 1)[:, :t.shape[1]],
+                                 lambda t: torch.stack((t.reshape(-1), t.reshape(-1)), -1)[:, 0]],
+                         ids=["contiguous", "transposed", "every other", "narrowed", "strided vector"])
+def test_statistics_of_any_layout_are_there_when_the_kernel_reads_them(machine, lay, stream):
+    """The kernel gets the statistics themselves, or copies that are held until after the call."""
+    n, h, c = 5, 7, 16
+    mean, rstd = torch.arange(35.).view(n, h), 100 + torch.arange(35.).view(n, h)
+    x = dev(torch.ones(n, h, c))
+    seen = []
+
+    def check(name, args):
+        m, r = args[5], args[6]
+        assert held(m) and held(r), "freed statistics"
+        assert m != r and floats(m, 35) == mean.view(-1).tolist() and floats(r, 35) == rstd.view(-1).tolist()
+        others = [args[k] for k in (0, 2, 13, 14, 15, 16)]
+        assert m not in others and r not in others
+        seen.append(machine.current)
+
+    machine.check = check
+    R.layer_norm_bwd_nhwc(x, x, None, dev(lay(mean)), dev(lay(rstd)), stream=stream)
+    assert seen == [stream or HOME]
