@@ -512,8 +512,6 @@ __global__ __launch_bounds__(kLnRedThreads) void ln_bwd_reduce(const float *part
     }
 }
 
-constexpr long long kMaxRows = 0x7fffffffLL;
-
 // Rows and columns each fit an int; all element offsets are 64-bit.
 int ln_check(const void *x, long long ldx, long long rows, int cols, int dtype)
 {
@@ -521,7 +519,7 @@ int ln_check(const void *x, long long ldx, long long rows, int cols, int dtype)
         return CONVIMG_ERR_SHAPE;
     if (!dtype_ok(dtype))
         return CONVIMG_ERR_DTYPE;
-    if (rows > kMaxRows || cols > 0x7fffff00)
+    if (rows > kMaxRows || cols > kMaxCols)
         return CONVIMG_ERR_RANGE;
     if (!x && rows > 0)
         return CONVIMG_ERR_NULL;
@@ -699,6 +697,8 @@ int layer_norm_bwd_workspace(long long rows, int cols, size_t *bytes)
         return CONVIMG_ERR_NULL;
     if (rows < 0 || cols <= 0)
         return CONVIMG_ERR_SHAPE;
+    if (rows > kMaxRows || cols > kMaxCols)
+        return CONVIMG_ERR_RANGE;
     *bytes = (size_t)ln_parts(rows, cols) * 2 * (size_t)cols * 4;
     return CONVIMG_OK;
 }

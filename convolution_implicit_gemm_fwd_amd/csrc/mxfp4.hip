@@ -178,7 +178,7 @@ int mx_shape(long long rows, long long cols)
 {
     if (rows < 0 || cols <= 0)
         return CONVIMG_ERR_SHAPE;
-    if (rows > 0x7fffff00 || cols > 0x7fffff00 || mx_code_bytes(rows, (int)cols) >= 0x80000000u)
+    if (rows > kMaxRows || cols > kMaxCols || mx_code_bytes(rows, (int)cols) >= 0x80000000u)
         return CONVIMG_ERR_RANGE;
     return CONVIMG_OK;
 }

@@ -346,6 +346,10 @@ __device__ __forceinline__ unsigned mx_top(unsigned top, float v)
     return m > top ? m : top;
 }
 
+// Rows and columns at most.  Kernels count a row's columns in an int and step
+// up to 8192 past its end.
+constexpr long long kMaxRows = 0x7fffffffLL, kMaxCols = 0x7fffffffLL - 0x3fff;
+
 __host__ __device__ inline int mx_blocks(int cols) { return (cols + 31) / 32; }
 inline int mx_quads(int cols) { return (cols + 127) / 128; }
 inline size_t mx_code_bytes(long long rows, int cols) { return (size_t)rows * mx_blocks(cols) * 16; }

@@ -413,10 +413,10 @@ int conv2d_bwd_weight_workspace(int N, int H, int W, int IC, int OC, int KH, int
  * sum is taken in a fixed order.
  *
  * Errors, all before any work is queued: CONVIMG_ERR_SHAPE (rows < 0,
- * cols <= 0, ld < cols), _DTYPE, _RANGE (rows or columns of 2^31 or more,
- * packed codes of 2 GiB or more), _NULL, _ALIGN, _WORKSPACE, _ALIAS (an
- * output or the workspace overlaps any other buffer of the call).
- * CONVIMG_ERR_LAUNCH if a launch fails. */
+ * cols <= 0, ld < cols), _DTYPE, _RANGE (rows of 2^31 or more, columns
+ * above 2^31 - 2^14, packed codes of 2 GiB or more), _NULL, _ALIGN,
+ * _WORKSPACE, _ALIAS (an output or the workspace overlaps any other buffer of
+ * the call).  CONVIMG_ERR_LAUNCH if a launch fails. */
 
 /* Layer normalisation: y = (x - mean) * rstd * gamma + beta with mean and
  * rstd = 1 / sqrt(var + eps) over each row's columns (var without
