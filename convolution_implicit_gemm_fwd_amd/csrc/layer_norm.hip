@@ -678,7 +678,9 @@ int layer_norm_fwd_mxfp4(const void *x, long long ldx, const float *gamma, const
                          int cols, float eps, int x_dtype, void *codes, void *scales, float *mean, float *rstd,
                          hipStream_t stream)
 {
-    const int rc = ln_check(x, ldx, rows, cols, x_dtype);
+    int rc = ln_check(x, ldx, rows, cols, x_dtype);
+    if (rc == CONVIMG_OK)
+        rc = mx_shape(rows, cols);
     if (rc != CONVIMG_OK)
         return rc;
     if (rows == 0)

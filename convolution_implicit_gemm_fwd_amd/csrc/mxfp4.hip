@@ -173,16 +173,6 @@ void gemm_few(const MxFewArgs &g, int x_dtype, int out_dtype, hipStream_t stream
     });
 }
 
-// Rows and columns of a packed operand: its codes stay below 2^31 bytes.
-int mx_shape(long long rows, long long cols)
-{
-    if (rows < 0 || cols <= 0)
-        return CONVIMG_ERR_SHAPE;
-    if (rows > kMaxRows || cols > kMaxCols || mx_code_bytes(rows, (int)cols) >= 0x80000000u)
-        return CONVIMG_ERR_RANGE;
-    return CONVIMG_OK;
-}
-
 int launched() { return hipGetLastError() == hipSuccess ? CONVIMG_OK : CONVIMG_ERR_LAUNCH; }
 
 bool misaligned(const void *p, unsigned n) { return ((uintptr_t)p & (n - 1)) != 0; }

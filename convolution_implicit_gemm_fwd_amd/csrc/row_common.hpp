@@ -355,6 +355,16 @@ inline int mx_quads(int cols) { return (cols + 127) / 128; }
 inline size_t mx_code_bytes(long long rows, int cols) { return (size_t)rows * mx_blocks(cols) * 16; }
 inline size_t mx_scale_bytes(long long rows, int cols) { return (size_t)rows * mx_quads(cols) * 4; }
 
+// Rows and columns of a packed operand: its codes stay below 2^31 bytes.
+inline int mx_shape(long long rows, long long cols)
+{
+    if (rows < 0 || cols <= 0)
+        return CONVIMG_ERR_SHAPE;
+    if (rows > kMaxRows || cols > kMaxCols || mx_code_bytes(rows, (int)cols) >= 0x80000000u)
+        return CONVIMG_ERR_RANGE;
+    return CONVIMG_OK;
+}
+
 inline bool row_overlaps(const void *a, size_t na, const void *b, size_t nb)
 {
     if (!a || !b || !na || !nb)

@@ -36,3 +36,14 @@ def test_columns_up_to_the_counters_are_taken():
 def test_rows_past_32_bits_are_refused():
     assert abi.layer_norm_bwd_workspace(1 << 31, 1)[0] == RANGE
     assert lnb(rows=1 << 31) == RANGE
+
+
+@pytest.mark.parametrize("rows,cols", [(1 << 20, 1 << 12), (1 << 27, 1), (1, COLS), (1 << 26, 33)])
+def test_codes_of_2_gib_are_refused_by_every_call(rows, cols):
+    refused = abi.mxfp4_bytes(rows, cols)[0]
+    assert refused == (RANGE if cols != COLS else 0)
+    if refused:
+        assert lnq(rows=rows, cols=cols, ldx=cols, codes=1 << 45, scales=1 << 46) == RANGE
+        assert quant(rows=rows, cols=cols, ldx=cols) == RANGE
+        assert deq(rows=rows, cols=cols) == RANGE
+        assert lin(x_dtype=MX, x_scales=1 << 45, M=rows, K=cols, ldx=cols) == RANGE
