@@ -481,16 +481,17 @@ __global__ __launch_bounds__(row_threads(TPR)) void ln_bwd_rows(LnBwdArgs a)
 
 // dgamma and dbeta: the partial sums in a fixed order, 16 columns a workgroup
 // and 64 threads a column (512 sums of 128 columns: 3 us; a thread a column took
-// 62).
-constexpr int kLnRedCols = 16, kLnRedThreads = 1024;
+// 62).  A launch takes the columns from `first`, up to kLnRedStep of the 2
+// cols, as it holds fewer than 2^32 threads.
+constexpr int kLnRedCols = 16, kLnRedThreads = 1024, kLnRedStep = 1 << 24;
 
 __global__ __launch_bounds__(kLnRedThreads) void ln_bwd_reduce(const float *part, float *dgamma, float *dbeta,
-                                                               int cols, int parts)
+                                                               int cols, int parts, long long first)
 {
     constexpr int LANES = kLnRedThreads / kLnRedCols;
     __shared__ float lds[LANES][kLnRedCols + 1];
     const int k = threadIdx.x % kLnRedCols, p0 = threadIdx.x / kLnRedCols;
-    const long long c = (long long)blockIdx.x * kLnRedCols + k;
+    const long long c = first + (long long)blockIdx.x * kLnRedCols + k;
     float s = 0.f;
     if (c < 2LL * cols)
 #pragma unroll 4
@@ -753,8 +754,11 @@ int layer_norm_bwd(const void *dy, long long lddy, const void *x, long long ldx,
         with_dtype(x_dtype, [&](auto t) { ln_bwd_launch<decltype(d), decltype(t)>(a, stream); });
     });
     if (dgamma && parts > 1)
-        hipLaunchKernelGGL(ln_bwd_reduce, dim3((unsigned)((2LL * cols + kLnRedCols - 1) / kLnRedCols)),
-                           dim3(kLnRedThreads), 0, stream, pg, dgamma, dbeta, cols, parts);
+        for (long long c = 0, end = 2LL * cols; c < end; c += kLnRedStep) {
+            const long long n = end - c < kLnRedStep ? end - c : kLnRedStep;
+            hipLaunchKernelGGL(ln_bwd_reduce, dim3((unsigned)((n + kLnRedCols - 1) / kLnRedCols)), dim3(kLnRedThreads), 0,
+                               stream, pg, dgamma, dbeta, cols, parts, c);
+        }
     return hipGetLastError() == hipSuccess ? CONVIMG_OK : CONVIMG_ERR_LAUNCH;
 }
 
