@@ -63,9 +63,14 @@ void quantize_cols(const void *x, long long ldx, int rows, int cols, int dtype, 
 {
     const MxTileArgs a = {x, ldx, rows, cols, codes, scales, nullptr, nullptr, nullptr};
     const long long tiles = mx_tiles(rows, cols);
+    // (a launch holds fewer than 2^32 threads: 2^30 rows of one column are 2^23 tiles)
+    constexpr long long kStep = 1 << 21;
     with_dtype(dtype, [&](auto t) {
-        hipLaunchKernelGGL(mx_quantize_cols<decltype(t)>, dim3(eights(tiles)), dim3(kMxTileThreads), 0, stream, a,
-                           (unsigned)tiles);
+        for (long long first = 0; first < tiles; first += kStep) {
+            const long long end = first + kStep < tiles ? first + kStep : tiles;
+            hipLaunchKernelGGL(mx_quantize_cols<decltype(t)>, dim3(eights(end - first)), dim3(kMxTileThreads), 0, stream,
+                               a, (unsigned)first, (unsigned)end);
+        }
     });
 }
 

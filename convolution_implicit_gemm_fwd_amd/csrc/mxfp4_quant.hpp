@@ -225,12 +225,13 @@ __device__ __forceinline__ void mx_quantize_tile(const MxTileArgs &a, unsigned t
     }
 }
 
+// The tiles first .. end - 1.
 template <typename T>
-__global__ __launch_bounds__(kMxTileThreads) void mx_quantize_cols(MxTileArgs a, unsigned tiles)
+__global__ __launch_bounds__(kMxTileThreads) void mx_quantize_cols(MxTileArgs a, unsigned first, unsigned end)
 {
     __shared__ __attribute__((aligned(16))) unsigned char lds[mx_tile_lds<T>()];
-    const unsigned tile = mx_xcd_tile(blockIdx.x, gridDim.x);
-    if (tile < tiles)
+    const unsigned tile = first + mx_xcd_tile(blockIdx.x, gridDim.x);
+    if (tile < end)
         mx_quantize_tile<T, false>(a, tile, lds);
 }
 

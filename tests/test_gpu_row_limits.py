@@ -26,3 +26,16 @@ def test_layer_norm_gradient_sums_of_very_wide_rows():
     # n is off by 2 u, a product by u, and each of the sums' additions (three levels, five terms) by u
     for got, terms in ((dgamma, dy.double() * n), (dbeta, dy.double())):
         assert bool(((got - terms.sum(0)).abs() <= 8 * U * terms.abs().sum(0) + 1e-40).all())
+
+
+def test_quantisation_down_a_very_long_column():
+    """2^23 + 2 tiles of 512 threads.  The column as a row gives the same codes by another kernel."""
+    rows = (1 << 30) + 130
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    x = torch.randn(rows, 1, generator=g, device="cuda", dtype=torch.bfloat16)
+    x[-1] = 77
+    down, along = cim.mxfp4_quantize_nhwc(x, transpose=True), cim.mxfp4_quantize_nhwc(x.view(1, rows))
+    assert (down.rows, down.cols) == (along.rows, along.cols) == (1, rows)
+    assert torch.equal(down.codes, along.codes) and torch.equal(down.scales, along.scales)
+    assert down.codes[0, -16] >> 4 == 6      # the last value, second of its block: 77 / 16 rounds to 4
