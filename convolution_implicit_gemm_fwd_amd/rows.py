@@ -84,6 +84,13 @@ def _dtype(t, what):
     return c
 
 
+def _fits(rows, cols, what):
+    """Counts as the library's ints: ctypes would pass their lower 32 bits."""
+    if rows > 0x7fffffff or cols > 0x7fffffff:
+        rc = abi.CONVIMG_ERR_RANGE
+        raise RuntimeError("%s has %d rows of %d columns: %s (status %d)" % (what, rows, cols, abi.conv2d_strerror(rc), rc))
+
+
 def _rows_of(t, what):
     """(rows, columns, elements from row to row) of a tensor [..., C]."""
     if not t.is_cuda:
@@ -111,6 +118,7 @@ def _rows_of(t, what):
         ld = cols
     elif ld < cols:
         raise ValueError("the rows of %s must not overlap" % what)
+    _fits(rows, cols, what)
     return rows, cols, ld
 
 
@@ -309,6 +317,7 @@ def _check_packed(q, what):
             or codes.shape != (rows, nb * 16) or scales.shape != (-(-nb // 4), rows, 4) \
             or not codes.is_contiguous() or not scales.is_contiguous():
         raise ValueError("%s is not a packed operand of %d rows and %d columns" % (what, rows, cols))
+    _fits(rows, cols, what)
 
 
 def mxfp4_dequantize_nhwc(q, dtype, stream=None):

@@ -8,6 +8,7 @@ import types
 import pytest
 import torch
 
+from convolution_implicit_gemm_fwd_amd import abi
 from convolution_implicit_gemm_fwd_amd import rows as R
 
 HOME, SIDE = 0, 0x5000      # stream handles
@@ -139,3 +140,34 @@ def test_statistics_of_any_layout_are_there_when_the_kernel_reads_them(machine, 
     machine.check = check
     R.layer_norm_bwd_nhwc(x, x, None, dev(lay(mean)), dev(lay(rstd)), stream=stream)
     assert seen == [stream or HOME]
+
+
+def far(*shape, dtype=torch.bfloat16):
+    """A tensor of that shape without memory."""
+    return dev(torch.empty(*shape, dtype=dtype, device="meta"))
+
+
+MANY = (1 << 32) + 5      # 5 in 32 bits
+
+
+@pytest.mark.parametrize("call", [
+    lambda: R.layer_norm_nhwc(far(1, MANY)), lambda: R.layer_norm_mxfp4_nhwc(far(3, MANY)),
+    lambda: R.layer_norm_bwd_nhwc(far(1, MANY), far(1, MANY), None, far(1, dtype=torch.float32), far(1, dtype=torch.float32)),
+    lambda: R.mxfp4_quantize_nhwc(far(MANY, 32)), lambda: R.mxfp4_quantize_nhwc(far(MANY, 32), transpose=True),
+    lambda: R.mxfp4_quantize_nhwc(far(1, MANY)), lambda: R.mxfp4_quantize_nhwc(far(1 << 31, 3)),
+    lambda: R.mxfp4_dequantize_nhwc(packed(MANY, 32), torch.bfloat16),
+    lambda: R.mxfp4_dequantize_nhwc(packed(2, MANY), torch.bfloat16),
+    lambda: R.mxfp4_linear_nhwc(far(MANY, 32), packed(8, 32)), lambda: R.mxfp4_linear_nhwc(packed(MANY, 32), packed(8, 32)),
+    lambda: R.mxfp4_linear_nhwc(far(8, 32), packed(MANY, 32)),
+    lambda: R.mxfp4_linear_bwd_nhwc(far(MANY, 8), far(MANY, 32), far(8, 32)),
+    lambda: R.mxfp4_linear_bwd_nhwc(far(4, MANY), far(4, 32), far(MANY, 32))], ids=range(14))
+def test_sizes_past_the_library_s_32_bits_are_refused(machine, call):
+    """They would reach the library as their lower 32 bits."""
+    with pytest.raises(RuntimeError, match="status %d" % abi.CONVIMG_ERR_RANGE):
+        call()
+    assert not machine.calls
+
+
+def packed(rows, cols):
+    nb = -(-cols // 32)
+    return R.Mxfp4Tensor(far(rows, nb * 16, dtype=torch.uint8), far(-(-nb // 4), rows, 4, dtype=torch.uint8), rows, cols)
