@@ -2,8 +2,9 @@
 
 ``python -m convolution_implicit_gemm_fwd_amd.build`` compiles the HIP
 translation units with hipcc for gfx950 only (each with its own extra flags)
-and links them into one shared library next to this file; and the host-only
-module that calls it from torch (csrc/rows_ext.cpp) with the C++ compiler.
+and links them into one shared library next to this file; and, where torch is
+installed, the host-only module that calls it from torch (csrc/rows_ext.cpp)
+with the C++ compiler.  The library needs neither torch nor the module.
 """
 from __future__ import annotations
 
@@ -25,7 +26,7 @@ UNITS = [(os.path.join(CSRC, "conv2d_fwd.hip"), []),
          (os.path.join(CSRC, "layer_norm.hip"), []),
          (os.path.join(CSRC, "mxfp4.hip"), [])]
 SOURCES = [u[0] for u in UNITS]
-DEPENDS = SOURCES + [os.path.join(CSRC, h) for h in ("igemm_common.hpp", "igemm_regs.hpp", "igemm_pipe.hpp", "igemm_patch.hpp", "igemm_strip.hpp", "igemm_window.hpp", "igemm_resident.hpp", "igemm_image.hpp", "igemm_dgrad.hpp", "igemm_wgrad.hpp", "igemm_layout.hpp", "row_common.hpp", "mxfp4_quant.hpp", "mxfp4_gemm.hpp", "mxfp4_few.hpp")] + [os.path.join(INCLUDE, "convimg.h")]
+DEPENDS = SOURCES + [os.path.join(CSRC, h) for h in ("igemm_common.hpp", "igemm_regs.hpp", "igemm_pipe.hpp", "igemm_patch.hpp", "igemm_strip.hpp", "igemm_window.hpp", "igemm_resident.hpp", "igemm_image.hpp", "igemm_dgrad.hpp", "igemm_wgrad.hpp", "igemm_layout.hpp", "row_common.hpp", "mxfp4_quant.hpp", "mxfp4_gemm.hpp", "mxfp4_few.hpp", "rows_ext.cpp")] + [os.path.join(INCLUDE, "convimg.h")]
 
 ARCH = "gfx950"
 HIPCC_FLAGS = [
@@ -48,11 +49,15 @@ def hipcc() -> str:
 
 
 def ext_command(out: str):
-    """The command that compiles the torch module (host code only)."""
+    """The command that compiles the torch module (host code only), None
+    without torch."""
     import importlib.util
     import sysconfig
 
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    torch = spec.submodule_search_locations[0]
     cxx = os.environ.get("CXX") or shutil.which("g++") or "/opt/rocm/llvm/bin/clang++"
     return [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM",
             "-isystem", os.path.join(torch, "include"),
@@ -63,56 +68,58 @@ def ext_command(out: str):
 
 
 def build(verbose: bool = False, extra_flags=()) -> str:
-    """Compile the library (always) and return its path."""
+    """Compile the library (always) and return its path.  A failure of the
+    torch module is raised after the library is in place."""
     tag = "%d" % os.getpid()
-    objs = []
     # the host pass does not know the packed-fp32 feature and says so
     noise = "'-packed-fp32-ops' is not a recognized feature"
+    tmp, ext_tmp = LIB + ".tmp" + tag, EXT + ".tmp" + tag
+    objs = [os.path.join(PKG, os.path.basename(src) + ".%s.o" % tag) for src, _ in UNITS]
+    flags_c = [f for f in HIPCC_FLAGS if f != "-shared"]
+    units = [[hipcc(), *flags_c, *flags, *extra_flags, "-I", INCLUDE, "-c", src, "-o", obj]
+             for (src, flags), obj in zip(UNITS, objs)]
+    link = [hipcc(), "--offload-arch=" + ARCH, "-shared", "-fPIC", *objs, "-o", tmp]
+    ext = ext_command(ext_tmp)
 
-    def run(cmd):
+    def start(cmd):
         if verbose:
             print(" ".join(cmd), flush=True)
-        res = subprocess.run(cmd, capture_output=True, text=True)
-        msgs = [ln for ln in (res.stdout + res.stderr).splitlines() if noise not in ln]
-        if res.returncode != 0:
-            raise RuntimeError("hipcc failed:\n" + "\n".join(msgs))
+        return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+
+    def finish(p):
+        """What the compiler says if it fails, else None."""
+        out, _ = p.communicate()
+        msgs = "\n".join(ln for ln in out.splitlines() if noise not in ln)
+        if p.returncode != 0:
+            return msgs
         if verbose and msgs:
-            print("\n".join(msgs))
+            print(msgs)
+        return None
 
     try:
         # the translation units compile in parallel
-        procs = []
-        for src, flags in UNITS:
-            obj = os.path.join(PKG, os.path.basename(src) + ".%s.o" % tag)
-            objs.append(obj)
-            flags_c = [f for f in HIPCC_FLAGS if f != "-shared"]
-            cmd = [hipcc(), *flags_c, *flags, *extra_flags, "-I", INCLUDE, "-c", src, "-o", obj]
-            if verbose:
-                print(" ".join(cmd), flush=True)
-            procs.append(subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT,
-                                          text=True))
-        ext_tmp = EXT + ".tmp" + tag
-        objs.append(ext_tmp)
-        cmd = ext_command(ext_tmp)
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        procs.append(subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True))
-        failed = []
-        for p in procs:
-            out, _ = p.communicate()
-            msgs = [ln for ln in out.splitlines() if noise not in ln]
-            if p.returncode != 0:
-                failed.append("\n".join(msgs))
-            elif verbose and msgs:
-                print("\n".join(msgs))
+        procs = [start(cmd) for cmd in units]
+        ext_proc = ext_failed = None
+        if ext is not None:
+            try:
+                ext_proc = start(ext)
+            except OSError as e:
+                ext_failed = str(e)
+        failed = [m for m in map(finish, procs) if m is not None]
+        if ext_proc is not None:
+            ext_failed = finish(ext_proc)
+        if not failed:
+            m = finish(start(link))
+            failed = [] if m is None else [m]
         if failed:
-            raise RuntimeError("the compiler failed:\n" + "\n".join(failed))
-        tmp = LIB + ".tmp" + tag
-        run([hipcc(), "--offload-arch=" + ARCH, "-shared", "-fPIC", *objs[:len(UNITS)], "-o", tmp])
+            raise RuntimeError("hipcc failed:\n" + "\n".join(failed))
         os.replace(tmp, LIB)
-        os.replace(ext_tmp, EXT)
+        if ext_failed is not None:
+            raise RuntimeError("libconvimg.so is built; the compiler of _rows.so failed:\n" + ext_failed)
+        if ext is not None:
+            os.replace(ext_tmp, EXT)
     finally:
-        for o in objs:
+        for o in (*objs, tmp, ext_tmp):
             if os.path.exists(o):
                 os.remove(o)
     return LIB
