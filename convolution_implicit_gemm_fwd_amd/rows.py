@@ -46,7 +46,12 @@ def _setup():
     import torch
 
     _lib = abi.load()
-    from . import _rows as _fast
+    try:
+        from . import _rows as _fast
+    except ImportError as e:
+        raise abi.LibraryMissing(
+            "_rows.so, the row operators' torch module, is not built or does not load (%s); build it with "
+            "`python -m convolution_implicit_gemm_fwd_amd.build`" % e) from e
     for name in ("layer_norm_fwd", "layer_norm_fwd_mxfp4", "layer_norm_bwd", "layer_norm_bwd_workspace",
                  "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_linear_fwd", "mxfp4_linear_workspace",
                  "mxfp4_linear_bwd", "mxfp4_linear_bwd_workspace"):

@@ -171,3 +171,15 @@ def test_sizes_past_the_library_s_32_bits_are_refused(machine, call):
 def packed(rows, cols):
     nb = -(-cols // 32)
     return R.Mxfp4Tensor(far(rows, nb * 16, dtype=torch.uint8), far(-(-nb // 4), rows, 4, dtype=torch.uint8), rows, cols)
+
+
+def test_a_missing_torch_module_names_the_build(monkeypatch):
+    import sys
+
+    import convolution_implicit_gemm_fwd_amd as package
+
+    monkeypatch.setattr(R, "_torch", None)
+    monkeypatch.delattr(package, "_rows", raising=False)
+    monkeypatch.setitem(sys.modules, package.__name__ + "._rows", None)
+    with pytest.raises(abi.LibraryMissing, match="convolution_implicit_gemm_fwd_amd.build"):
+        R.layer_norm_nhwc(torch.zeros(2, 8))
