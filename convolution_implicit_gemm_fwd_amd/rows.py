@@ -173,15 +173,28 @@ def _on(stream, t, f, *args):
         r = f(*args)
     finally:
         _torch.cuda.set_stream(home)
-    for o in r if isinstance(r, tuple) else (r,):
-        if isinstance(o, _torch.Tensor):
-            o.record_stream(home)
+    _record(r, home)
     return r
+
+
+def _record(r, stream):
+    if isinstance(r, _torch.Tensor):
+        r.record_stream(stream)
+    elif isinstance(r, tuple):
+        for o in r:
+            _record(o, stream)
 
 
 def _same_device(device, t, what):
     if t.device != device:
         raise ValueError("%s must be on the device of the other tensors" % what)
+
+
+def _stats(x):
+    """(mean, rstd) for the rows of x to write, and their addresses."""
+    mean = _empty(*x.shape[:-1], dtype=_f32, device=x.device) if x.dim() > 1 else _empty((), dtype=_f32, device=x.device)
+    rstd = _torch.empty_like(mean)
+    return mean, rstd, mean.data_ptr(), rstd.data_ptr()
 
 
 def layer_norm_nhwc(x, gamma=None, beta=None, eps=1e-5, out_dtype=None, stats=False, stream=None):
@@ -208,11 +221,7 @@ def layer_norm_nhwc(x, gamma=None, beta=None, eps=1e-5, out_dtype=None, stats=Fa
     xd, yd = _dtype(x.dtype, "x"), _dtype(out_dtype, "out_dtype")
     g, b = _param(gamma, cols, dev, "gamma"), _param(beta, cols, dev, "beta")
     y = _like(x, out_dtype)
-    mean = rstd = mp = rp = None
-    if stats:
-        mean = _empty(*x.shape[:-1], dtype=_f32, device=dev) if x.dim() > 1 else _empty((), dtype=_f32, device=dev)
-        rstd = _torch.empty_like(mean)
-        mp, rp = mean.data_ptr(), rstd.data_ptr()
+    mean, rstd, mp, rp = _stats(x) if stats else (None,) * 4
     rc = _lib.layer_norm_fwd(x.data_ptr(), ld, g, b, rows, cols, eps, xd, yd, y.data_ptr(), mp, rp,
                              _stream(dev.index))
     if rc:
@@ -226,28 +235,31 @@ def _packed(device, rows, cols):
                        _empty(-(-nb // 4), rows, 4, dtype=_u8, device=device), rows, cols)
 
 
-def layer_norm_mxfp4_nhwc(x, gamma=None, beta=None, eps=1e-5, stream=None):
+def layer_norm_mxfp4_nhwc(x, gamma=None, beta=None, eps=1e-5, stream=None, stats=False):
     """layer_norm_nhwc with its result quantised to MXFP4 rows: an
-    ``Mxfp4Tensor``, the input of ``mxfp4_linear_nhwc``."""
+    ``Mxfp4Tensor``, the input of ``mxfp4_linear_nhwc``; with ``stats``
+    (that, mean, rstd), the statistics as ``layer_norm_nhwc`` gives them."""
     if _torch is None:
         _setup()
     if stream is not None:
-        return _on(stream, x, layer_norm_mxfp4_nhwc, x, gamma, beta, eps)
-    r = _fast.layer_norm_mxfp4(x, gamma, beta, eps)
-    if r is not None:
-        return _new(Mxfp4Tensor, r)
+        return _on(stream, x, layer_norm_mxfp4_nhwc, x, gamma, beta, eps, None, stats)
+    if not stats:
+        r = _fast.layer_norm_mxfp4(x, gamma, beta, eps)
+        if r is not None:
+            return _new(Mxfp4Tensor, r)
     rows, cols, ld = _rows_of(x, "x")
     dev = x.device
     if _device() != dev.index:
-        return _elsewhere(dev, layer_norm_mxfp4_nhwc, x, gamma, beta, eps)
+        return _elsewhere(dev, layer_norm_mxfp4_nhwc, x, gamma, beta, eps, None, stats)
     xd = _dtype(x.dtype, "x")
     g, b = _param(gamma, cols, dev, "gamma"), _param(beta, cols, dev, "beta")
     q = _packed(dev, rows, cols)
+    mean, rstd, mp, rp = _stats(x) if stats else (None,) * 4
     rc = _lib.layer_norm_fwd_mxfp4(x.data_ptr(), ld, g, b, rows, cols, eps, xd, q.codes.data_ptr(),
-                                   q.scales.data_ptr(), None, None, _stream(dev.index))
+                                   q.scales.data_ptr(), mp, rp, _stream(dev.index))
     if rc:
         _fail("layer_norm_fwd_mxfp4", rc)
-    return q
+    return (q, mean, rstd) if stats else q
 
 
 def layer_norm_bwd_nhwc(dy, x, gamma, mean, rstd, dx_dtype=None, stream=None):

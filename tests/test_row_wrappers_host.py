@@ -86,6 +86,17 @@ def calls():
             lambda **s: R.mxfp4_linear_nhwc(q, q, **s), lambda **s: R.mxfp4_linear_bwd_nhwc(dy, x, w, **s)]
 
 
+def test_packed_rows_come_with_statistics(machine):
+    x = dev(torch.ones(3, 5, 64))
+    q, mean, rstd = R.layer_norm_mxfp4_nhwc(x, stats=True, stream=SIDE)
+    assert isinstance(q, R.Mxfp4Tensor) and mean.shape == rstd.shape == (3, 5)
+    args = machine.calls[-1][1]
+    assert args[8:13] == (q.codes.data_ptr(), q.scales.data_ptr(), mean.data_ptr(), rstd.data_ptr(), SIDE)
+    assert {(t.data_ptr(), HOME) for t in (q.codes, q.scales, mean, rstd)} <= set(Dev.recorded)
+    q = R.layer_norm_mxfp4_nhwc(x)
+    assert isinstance(q, R.Mxfp4Tensor) and machine.calls[-1][1][10:12] == (None, None)
+
+
 def tensors(r):
     return [r] if isinstance(r, torch.Tensor) else [t for v in r if not isinstance(v, int) for t in tensors(v)]
 
