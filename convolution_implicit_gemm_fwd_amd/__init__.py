@@ -13,6 +13,12 @@ norm over the channels and its gradient (``layer_norm_nhwc``,
 convolution on them with its gradient (``mxfp4_linear_nhwc``,
 ``mxfp4_linear_bwd_nhwc``).
 
+Each call runs on ``stream`` (a stream's handle; default: torch's current
+stream).  On another stream than the current one it is made as under
+``torch.cuda.stream``: what it allocates comes from that stream's memory, and
+the caller orders that stream behind whatever made the inputs, keeps the
+inputs until it has run the call, and orders what reads the output behind it.
+
 Importing the package loads nothing; the HIP library is loaded on first use
 and its absence is an error (there is no fallback path).
 """
@@ -37,26 +43,24 @@ __all__ = ["abi", "layer_norm_nhwc", "layer_norm_bwd_nhwc", "layer_norm_mxfp4_nh
            "conv2d_fwd_num_tiles", "conv2d_fwd_status", "conv2d_fwd_test_spin_limit", "conv2d_release", "CONVIMG_BF16", "CONVIMG_FP32", "LibraryMissing"]
 
 
-def _stream_of(stream, device):
-    """(raw stream pointer, whether it is torch's current stream on device)."""
+def _on(stream, t, f, *args):
+    """The call on the stream of this handle, where that is not the current one
+    of t's device with the stream made the current one: a block of the present
+    current stream's memory may be in use by work that is still queued there.
+    The result goes back to that stream, so its memory is not used again before
+    it is past it."""
     import torch
 
-    cur = torch.cuda.current_stream(device).cuda_stream
-    if stream is None:
-        return cur, True
-    return stream, stream == cur
-
-
-def _keep_for_stream(tensors, stream, device):
-    """Buffers allocated here on torch's current stream but used by work on
-    another stream: tell the caching allocator, so that it does not hand
-    their memory out again until that stream has run the work."""
-    import torch
-
-    ext = torch.cuda.ExternalStream(stream, device=device)
-    for t in tensors:
-        if t is not None:
-            t.record_stream(ext)
+    if not t.is_cuda:
+        return f(*args)        # (refused there)
+    with torch.cuda.device(t.device):
+        home = torch.cuda.current_stream(t.device)
+        if stream == home.cuda_stream:
+            return f(*args)
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=t.device)):
+            r = f(*args)
+    r.record_stream(home)
+    return r
 
 
 def _dtype_of(a, b, what):
@@ -79,6 +83,8 @@ def conv2d_nhwc(x, w, bias=None, stride=1, pad=0, dilation=1, out=None, stream=N
     """
     import torch
 
+    if stream is not None:
+        return _on(stream, x, conv2d_nhwc, x, w, bias, stride, pad, dilation, out)
     dtype = _dtype_of(x, w, "x and w")
     if not (x.is_cuda and w.is_cuda):
         raise ValueError("x and w must be device tensors")
@@ -96,22 +102,18 @@ def conv2d_nhwc(x, w, bias=None, stride=1, pad=0, dilation=1, out=None, stream=N
     OW = conv2d_fwd_out_dim(W, KW, stride, pad, dilation)
     if OH <= 0 or OW <= 0:
         raise ValueError("no output pixel for this shape")
-    fresh = []
     if out is None:
         out = torch.empty((N, OH, OW, OC), dtype=torch.float32, device=x.device)
-        fresh.append(out)
     elif (tuple(out.shape) != (N, OH, OW, OC) or out.dtype != torch.float32
           or not out.is_contiguous() or not out.is_cuda):
         raise ValueError("out must be a contiguous float32 [N,OH,OW,OC] device tensor")
-    stream, current = _stream_of(stream, x.device)
+    stream = torch.cuda.current_stream(x.device).cuda_stream
     with torch.cuda.device(x.device):
         rc = conv2d_fwd(x.data_ptr(), w.data_ptr(), bias.data_ptr() if bias is not None else None,
                         N, H, W, IC, OC, KH, KW, stride, pad, dilation, dtype, out.data_ptr(),
                         stream)
     if rc != 0:
         raise RuntimeError("conv2d_fwd failed: %s (status %d)" % (conv2d_strerror(rc), rc))
-    if not current:
-        _keep_for_stream(fresh, stream, x.device)
     return out
 
 
@@ -128,6 +130,8 @@ def conv2d_bwd_data_nhwc(dy, w, H, W, stride=1, pad=0, dilation=1, dx=None, wt=N
     """
     import torch
 
+    if stream is not None:
+        return _on(stream, dy, conv2d_bwd_data_nhwc, dy, w, H, W, stride, pad, dilation, dx, wt)
     dtype = _dtype_of(dy, w, "dy and w")
     if not (dy.is_cuda and w.is_cuda):
         raise ValueError("dy and w must be device tensors")
@@ -140,27 +144,22 @@ def conv2d_bwd_data_nhwc(dy, w, H, W, stride=1, pad=0, dilation=1, dx=None, wt=N
     if (conv2d_fwd_out_dim(H, KH, stride, pad, dilation) != OH
             or conv2d_fwd_out_dim(W, KW, stride, pad, dilation) != OW):
         raise ValueError("dy's extent is not the forward output extent of H x W")
-    fresh = []
     if wt is None:
         wt = torch.empty(w.numel(), dtype=w.dtype, device=w.device)
-        fresh.append(wt)
     elif (wt.numel() != w.numel() or wt.dtype != w.dtype or not wt.is_contiguous()
           or not wt.is_cuda):
         raise ValueError("wt must be a contiguous device tensor of w's size and dtype")
     if dx is None:
         dx = torch.empty((N, H, W, IC), dtype=torch.float32, device=dy.device)
-        fresh.append(dx)
     elif (tuple(dx.shape) != (N, H, W, IC) or dx.dtype != torch.float32
           or not dx.is_contiguous() or not dx.is_cuda):
         raise ValueError("dx must be a contiguous float32 [N,H,W,IC] device tensor")
-    stream, current = _stream_of(stream, dy.device)
+    stream = torch.cuda.current_stream(dy.device).cuda_stream
     with torch.cuda.device(dy.device):
         rc = conv2d_bwd_data(dy.data_ptr(), w.data_ptr(), N, H, W, IC, OC, KH, KW, stride, pad,
                              dilation, dtype, wt.data_ptr(), dx.data_ptr(), stream)
     if rc != 0:
         raise RuntimeError("conv2d_bwd_data failed: %s (status %d)" % (conv2d_strerror(rc), rc))
-    if not current:
-        _keep_for_stream(fresh, stream, dy.device)
     return dx
 
 
@@ -178,6 +177,8 @@ def conv2d_bwd_weight_nhwc(x, dy, KH, KW, stride=1, pad=0, dilation=1, dw=None, 
     """
     import torch
 
+    if stream is not None:
+        return _on(stream, x, conv2d_bwd_weight_nhwc, x, dy, KH, KW, stride, pad, dilation, dw, ws)
     if x.dtype != dy.dtype or x.dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("the weight backward takes x and dy both bfloat16 or both float32")
     dtype = CONVIMG_BF16 if x.dtype == torch.bfloat16 else CONVIMG_FP32
@@ -198,25 +199,20 @@ def conv2d_bwd_weight_nhwc(x, dy, KH, KW, stride=1, pad=0, dilation=1, dw=None, 
         if rc != 0:
             raise RuntimeError("conv2d_bwd_weight_workspace failed: %s (status %d)"
                                % (conv2d_strerror(rc), rc))
-        fresh = []
         if ws is None and need > 0:
             ws = torch.empty(need, dtype=torch.uint8, device=x.device)
-            fresh.append(ws)
         if dw is None:
             dw = torch.empty((OC, KH, KW, IC), dtype=torch.float32, device=x.device)
-            fresh.append(dw)
         elif (tuple(dw.shape) != (OC, KH, KW, IC) or dw.dtype != torch.float32
               or not dw.is_contiguous() or not dw.is_cuda):
             raise ValueError("dw must be a contiguous float32 [OC,KH,KW,IC] device tensor")
-        stream, current = _stream_of(stream, x.device)
+        stream = torch.cuda.current_stream(x.device).cuda_stream
         ws_ptr = ws.data_ptr() if ws is not None else None
         ws_bytes = ws.numel() * ws.element_size() if ws is not None else 0
         rc = conv2d_bwd_weight(x.data_ptr(), dy.data_ptr(), N, H, W, IC, OC, KH, KW, stride, pad,
                                dilation, dtype, dw.data_ptr(), ws_ptr, ws_bytes, stream)
     if rc != 0:
         raise RuntimeError("conv2d_bwd_weight failed: %s (status %d)" % (conv2d_strerror(rc), rc))
-    if not current:
-        _keep_for_stream(fresh, stream, x.device)
     return dw
 
 
@@ -232,6 +228,8 @@ def conv2d_nchw(x, w, bias=None, stride=1, pad=0, dilation=1, out_dtype=None, ou
     """
     import torch
 
+    if stream is not None:
+        return _on(stream, x, conv2d_nchw, x, w, bias, stride, pad, dilation, out_dtype, out, ws)
     dtype = _dtype_of(x, w, "x and w")
     out_dtype = torch.float32 if out_dtype is None else out_dtype
     if out_dtype not in (torch.float32, torch.bfloat16):
@@ -256,23 +254,18 @@ def conv2d_nchw(x, w, bias=None, stride=1, pad=0, dilation=1, out_dtype=None, ou
         if rc != 0:
             raise RuntimeError("conv2d_fwd_nchw_workspace failed: %s (status %d)"
                                % (conv2d_strerror(rc), rc))
-        fresh = []
         if ws is None:
             ws = torch.empty(need, dtype=torch.uint8, device=x.device)
-            fresh.append(ws)
         if out is None:
             out = torch.empty((N, OC, OH, OW), dtype=out_dtype, device=x.device)
-            fresh.append(out)
         elif (tuple(out.shape) != (N, OC, OH, OW) or out.dtype != out_dtype
               or not out.is_contiguous() or not out.is_cuda):
             raise ValueError("out must be a contiguous [N,OC,OH,OW] device tensor of out_dtype")
-        stream, current = _stream_of(stream, x.device)
+        stream = torch.cuda.current_stream(x.device).cuda_stream
         od = CONVIMG_BF16 if out_dtype == torch.bfloat16 else CONVIMG_FP32
         rc = conv2d_fwd_nchw(x.data_ptr(), w.data_ptr(), bias.data_ptr() if bias is not None else None,
                              N, H, W, IC, OC, KH, KW, stride, pad, dilation, dtype, od, out.data_ptr(),
                              ws.data_ptr(), ws.numel(), stream)
     if rc != 0:
         raise RuntimeError("conv2d_fwd_nchw failed: %s (status %d)" % (conv2d_strerror(rc), rc))
-    if not current:
-        _keep_for_stream(fresh, stream, x.device)
     return out
