@@ -2072,7 +2072,7 @@ const char *conv2d_strerror(int status)
     case CONVIMG_ERR_NULL: return "null pointer argument";
     case CONVIMG_ERR_SHAPE: return "invalid shape, stride, padding or dilation (or no output pixel)";
     case CONVIMG_ERR_DTYPE: return "unsupported dtype";
-    case CONVIMG_ERR_RANGE: return "an element count reaches 2^31";
+    case CONVIMG_ERR_RANGE: return "an element count reaches 2^31, or a size of a row operator passes its limit";
     case CONVIMG_ERR_ALIAS: return "out overlaps an input";
     case CONVIMG_ERR_ALLOC: return "could not allocate split-K semaphores";
     case CONVIMG_ERR_LAUNCH: return "kernel launch failed";
