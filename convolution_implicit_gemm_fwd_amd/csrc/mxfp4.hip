@@ -98,10 +98,14 @@ auto tiles_of(int M, int N)
 //     that one stores while others load: 8192x8192x256 30.5 us against 38.3 in
 //     256 x 256, x512 38.1 against 42.1, x1024 59.9 against 55.6; 3136x2048x512
 //     (400 tiles) 8.7 against 8.3 in the longer stages.
-//   Where K is at most 2048 and the last round of 256 x 256 tiles would leave
-//     more than 15 % of all rounds idle, 128 x 128, which overlap anyway:
-//     7000x7000x1000 47.5 us against 61.0, 6000x6000x2000 62.4 against 65.6;
-//     without that rest 8192x4096x2048 48.5 against 48.0.
+//   Where K is at most 2048, the last round of 256 x 256 tiles would leave more
+//     than 15 % of all rounds idle and there are 1024 tiles of 128 x 128, those,
+//     which overlap anyway: 7000x7000x1000 47.5 us against 61.0, 6000x6000x2000
+//     62.4 against 65.6, 4100x4100 (1089 tiles) x1000 21.5 against 26.4 and x2000
+//     34.9 against 40.9; without that rest 8192x4096x2048 48.5 against 48.0.
+//     With fewer tiles the larger ones are one round, and either may win:
+//     3500x3500 (784) x1000 16.7 against 19.2 and x2000 26.1 against 26.8,
+//     3328x3328 (676) 14.3 against 14.4 and 23.7 against 22.0.
 enum Shape { k256, k128, k128Short, k128x64, k64, k64x32, k32 };
 
 template <typename C>
@@ -163,7 +167,14 @@ void gemm(MxGemmArgs g, int out_dtype, hipStream_t stream)
 }
 
 // Dense rows that the product's workgroups quantise for themselves: one
-// launch in place of two, while that costs each workgroup little.
+// launch in place of two, while that costs each workgroup little.  In one
+// launch against two (us): 4096 -> 4096 3.9 against 7.4 for one row, 5.3 against
+// 7.5 for four; 4096 -> 8000 6.2 against 9.5 and 7.6 against 9.6; 8192 -> 8192
+// 9.8 against 13.9 and, at both bounds, 13.5 against 13.9; 16384 -> 4096 11.6
+// against 19.0 for two rows.  Past the bounds, with LDS for 16 rows: 4096 -> 8000
+// 10.6 against 9.7 for five rows and 14.0 against 9.6 for eight, 4096 -> 4096
+// 5.9 against 7.7, 7.3 against 7.8 and, for 16, 10.9 against 8.0; 8192 -> 8192
+// 18.8 against 13.9 for five; 16384 -> 4096 15.6 against 18.8 for four.
 bool few_dense(int M, int K) { return M <= kMxFewM && (long long)M * K <= kMxFewSize; }
 
 void gemm_few(const MxFewArgs &g, int x_dtype, int out_dtype, hipStream_t stream)

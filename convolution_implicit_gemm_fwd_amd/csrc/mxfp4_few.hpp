@@ -14,9 +14,9 @@
 // with four neighbouring columns of one output row, and the waves' sums meet
 // in LDS in a fixed order.
 //
-// One row through 4096 x 4096: 4.4 us a call, back to back, of which an empty
-// launch takes 1.9 and the 8.9 MB 1.7 at a copy's rate; 8192 x 8192 10.0 us.
-// In two launches (quantise, 64 x 64 tiles) 9.8 us.
+// One row through 4096 x 4096: 3.9 to 4.4 us a call, back to back, of which an
+// empty launch takes 1.9 and the 8.9 MB 1.7 at a copy's rate; 8192 x 8192 9.8 us.
+// In two launches (quantise, product) 7.4 and 13.9 us.
 #pragma once
 
 #include "mxfp4_gemm.hpp"

@@ -6,13 +6,15 @@
 // a dword of four scale bytes serves 128 k.  b's rows are the instruction's
 // rows, so that a lane ends with four neighbouring columns of one output row.
 //
-// 8192^3 takes 260 us (4.2 PFLOP/s) on normal data and 190 us on zeros: the
-// clock falls with the power that the data's toggling draws.  The same stream
-// of matrix instructions alone takes 187 and 155 us; reading operands from LDS
-// adds 25 us and the copies into it 35 us (131 KB and 68 KB a K tile of 256 and
-// workgroup), so the largest wave tile that the registers hold (128 x 128)
-// bounds what is left.  Fetching the lines into L2 two K tiles ahead of the
-// copies changes nothing.
+// 8192^3 takes 260 us (4.2 PFLOP/s) on normal data and 222 us on zeros.  The
+// same stream of matrix instructions alone, operands held in registers, takes
+// 201 us (5.5 PFLOP/s) and 156 us: the clock falls with the power that the
+// data's toggling draws.  With the operands' reads from LDS it takes 195 and
+// 164 us (the same K tiles over and over), so the copies into LDS are what
+// costs 60 us more, on either data.  A K tile of 256 copies 68 KB a workgroup
+// and reads 131 KB, and the largest wave tile that the registers hold (128 x
+// 128) bounds what is left.  Fetching the lines into L2 two K tiles ahead of
+// the copies changes nothing.
 #pragma once
 
 #include "mxfp4_quant.hpp"

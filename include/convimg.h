@@ -44,7 +44,7 @@ extern "C" {
 #define CONVIMG_ERR_NULL    1  /* x, w or out is NULL, or plan is NULL */
 #define CONVIMG_ERR_SHAPE   2  /* a size <= 0, stride/dilation < 1, pad < 0, or no output pixel */
 #define CONVIMG_ERR_DTYPE   3  /* dtype is neither CONVIMG_BF16 nor CONVIMG_FP32 */
-#define CONVIMG_ERR_RANGE   4  /* an element count of x, w or out reaches 2^31 */
+#define CONVIMG_ERR_RANGE   4  /* an element count of x, w or out reaches 2^31; row operators: see there */
 #define CONVIMG_ERR_ALIAS   5  /* out overlaps x, w or bias */
 #define CONVIMG_ERR_ALLOC   6  /* the library could not allocate its semaphores */
 #define CONVIMG_ERR_LAUNCH  7  /* the HIP runtime refused the launch */
@@ -52,7 +52,7 @@ extern "C" {
 #define CONVIMG_ERR_TIMEOUT 9  /* a split-K wait gave up (reported by conv2d_fwd_status) */
 #define CONVIMG_ERR_UNSUPPORTED 10 /* no entry point returns it now: conv2d_bwd_data serves every
                                       stride, window and padding, conv2d_bwd_weight fp32 storage */
-#define CONVIMG_ERR_WORKSPACE 11   /* conv2d_bwd_weight: ws_bytes below what it needs */
+#define CONVIMG_ERR_WORKSPACE 11   /* ws_bytes below what the call's size query reports */
 #define CONVIMG_ERR_SCRATCH 12     /* conv2d_fwd_noalloc: the plan needs more semaphores than its scratch holds */
 #define CONVIMG_ERR_ALIGN 13       /* row operators: a packed operand or workspace below its alignment */
 
