@@ -12,13 +12,14 @@ MXINT8: a block of 32 consecutive columns of a row shares a unit 2^(s - 127),
 s the smallest whole number of at least 1 with max|x| <= 127 units; a value is
 stored as x / unit rounded to the nearest whole number (ties to even).  Packed:
 codes int8 [rows][Kp], Kp the columns rounded up to 32; scales
-[ceil(Kp / 128)][rows][4], one byte s a block.
+[rows][4 ceil(Kp / 128)], one byte s a block.
 
 MXFP4: a block of 32 consecutive values along the contracted axis shares a
 scale 2^(s - 127), s = clamp(floor(log2 max|x|) - 2 + 127, 0, 254); a value is
 x / scale rounded to the nearest of 0, .5, 1, 1.5, 2, 3, 4, 6 (ties to the
 even code, larger values to 6) with its sign.  Packed: codes [rows][Kp / 2],
-two a byte, the even column in the low half; scales as above.
+two a byte, the even column in the low half; scales [ceil(Kp / 128)][rows][4],
+one byte s a block.
 
 Adapters: row m of adapter g = ids[m] adds scale[g] * up[g]^T (down[g] x[m]) to
 the projection's output, a row whose id is -1 nothing; down is [G][r][K], up
@@ -115,17 +116,12 @@ def _power(s):
     return torch.where(s > 0, s << 23, torch.full_like(s, 1 << 22)).to(torch.int32).view(torch.float32)
 
 
-def _scale_layout(s):
-    """Bytes [rows, blocks] as [ceil(blocks / 4), rows, 4]."""
+def _whole_dwords(s):
+    """A byte a block, [rows, blocks], filled up with zeros to whole dwords a row."""
     n, nb = s.shape
-    quads = -(-nb // 4)
-    scales = torch.zeros(n, quads * 4, dtype=torch.uint8, device=s.device)
+    scales = torch.zeros(n, -(-nb // 4) * 4, dtype=torch.uint8, device=s.device)
     scales[:, :nb] = s.to(torch.uint8)
-    return scales.view(n, quads, 4).permute(1, 0, 2).contiguous()
-
-
-def _scale_rows(scales, blocks):
-    return scales.permute(1, 0, 2).reshape(scales.shape[1], -1)[:, :blocks].to(torch.int32)
+    return scales
 
 
 def _pack8(x):
@@ -133,14 +129,14 @@ def _pack8(x):
     b = _blocks(x)
     # the exponent field, one more where the mantissa is above 127 / 64: then 127 units of the field's own do not do
     s = ((b.abs().amax(-1).view(torch.int32) + 0x1ffff >> 23) - 6).clamp_min(1)
-    return torch.round(b * _power(254 - s).unsqueeze(-1)).to(torch.int8).view(x.shape[0], -1), _scale_layout(s)
+    return torch.round(b * _power(254 - s).unsqueeze(-1)).to(torch.int8).view(x.shape[0], -1), _whole_dwords(s)
 
 
 def _values8(codes, scales, k):
     """fp32 [rows, K]"""
     n = codes.shape[0]
     c = codes.view(n, -1, 32).float()
-    return (c * _power(_scale_rows(scales, c.shape[1])).unsqueeze(-1)).view(n, -1)[:, :k]
+    return (c * _power(scales[:, :c.shape[1]].int()).unsqueeze(-1)).view(n, -1)[:, :k]
 
 
 def _scale_bytes4(b):
@@ -170,14 +166,16 @@ def _pack4(w):
     a = r.abs()
     code = torch.where(a < 2, a * 2, torch.where(a < 4, a + 2, a / 2 + 4)).to(torch.uint8)
     code = (code | (torch.signbit(r).to(torch.uint8) << 3)).view(b.shape[0], -1, 2)
-    return code[:, :, 0] | (code[:, :, 1] << 4), _scale_layout(s)
+    scales = _whole_dwords(s).view(b.shape[0], -1, 4).permute(1, 0, 2).contiguous()
+    return code[:, :, 0] | (code[:, :, 1] << 4), scales
 
 
 def _values4(codes, scales, k):
     n = codes.shape[0]
     v = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], device=codes.device)
     q = torch.stack((codes & 15, codes >> 4), -1).to(torch.int32).reshape(n, -1, 32)
-    return (torch.cat((v, -v))[q] * _power(_scale_rows(scales, q.shape[1])).unsqueeze(-1)).reshape(n, -1)[:, :k]
+    s = scales.permute(1, 0, 2).reshape(n, -1)[:, :q.shape[1]].int()
+    return (torch.cat((v, -v))[q] * _power(s).unsqueeze(-1)).reshape(n, -1)[:, :k]
 
 
 # ---- inputs ---------------------------------------------------------------
@@ -420,14 +418,8 @@ def _exact_fake8(x):
     return ((low + up) * unit).reshape(x.shape[0], -1)[:, :x.shape[1]]
 
 
-def _exact_columns(scales, cols):
-    """Byte of each column, [rows, cols]."""
-    c = torch.arange(cols, device=scales.device)
-    return scales.long()[c // 128, :, (c // 32) % 4].t()
-
-
 def _exact_values8(codes, scales, k):
-    return codes[:, :k].double() * _exact_power(_exact_columns(scales, k) - 127)
+    return codes[:, :k].double() * _exact_power(scales.long().repeat_interleave(32, 1)[:, :k] - 127)
 
 
 def _exact_fake4(x):
@@ -448,7 +440,8 @@ def _exact_values4(codes, scales, k):
     q = q[:, :k]
     e, m = (q % 8) // 2, (q % 2).double()
     mag = torch.where(e == 0, m / 2, (1 + m / 2) * _exact_power(e - 1))
-    return torch.where(q >= 8, -mag, mag) * _exact_power(_exact_columns(scales, k) - 127)
+    c = torch.arange(k, device=codes.device)
+    return torch.where(q >= 8, -mag, mag) * _exact_power(scales.long()[c // 128, :, (c // 32) % 4].t() - 127)
 
 
 def _exact_adapters(x, first, second, scale, ids):
