@@ -11,7 +11,9 @@ tensors with an fp32 or bf16 output.  The row operators (``rows``): layer
 norm over the channels and its gradient (``layer_norm_nhwc``,
 ``layer_norm_bwd_nhwc``), MXFP4 rows (``mxfp4_quantize_nhwc``) and the 1x1
 convolution on them with its gradient (``mxfp4_linear_nhwc``,
-``mxfp4_linear_bwd_nhwc``).
+``mxfp4_linear_bwd_nhwc``), activations kept in 8 bits for the backward pass
+(``mxint8_quantize_nhwc``, ``layer_norm_mxint8_nhwc``) and low-rank adapters of
+many requests beside that layer (``mxfp4_linear_adapters_nhwc``).
 
 Each call runs on ``stream`` (a stream's handle; default: torch's current
 stream).  On another stream than the current one it is made as under
@@ -31,11 +33,16 @@ from .abi import (CONVIMG_BF16, CONVIMG_FP32, LibraryMissing, conv2d_bwd_data,
                   conv2d_fwd_nchw, conv2d_fwd_nchw_workspace, conv2d_fwd_num_tiles, conv2d_fwd_out_dim,
                   conv2d_fwd_plan, conv2d_fwd_status, conv2d_fwd_test_spin_limit, conv2d_release,
                   conv2d_strerror)
-from .rows import (Mxfp4Tensor, layer_norm_bwd_nhwc, layer_norm_mxfp4_nhwc, layer_norm_nhwc,
-                   mxfp4_dequantize_nhwc, mxfp4_linear_bwd_nhwc, mxfp4_linear_nhwc, mxfp4_quantize_nhwc)
+from .rows import (Adapters, Mxfp4Tensor, Mxint8Tensor, layer_norm_bwd_mxint8_nhwc, layer_norm_bwd_nhwc,
+                   layer_norm_mxfp4_nhwc, layer_norm_mxint8_nhwc, layer_norm_nhwc, mxfp4_dequantize_nhwc,
+                   mxfp4_linear_adapters_bwd_nhwc, mxfp4_linear_adapters_nhwc, mxfp4_linear_bwd_nhwc,
+                   mxfp4_linear_nhwc, mxfp4_quantize_nhwc, mxint8_dequantize_nhwc, mxint8_quantize_nhwc)
 
 __all__ = ["abi", "layer_norm_nhwc", "layer_norm_bwd_nhwc", "layer_norm_mxfp4_nhwc", "Mxfp4Tensor",
-           "mxfp4_quantize_nhwc", "mxfp4_dequantize_nhwc", "mxfp4_linear_nhwc", "mxfp4_linear_bwd_nhwc", "conv2d_nhwc", "conv2d_bwd_data_nhwc", "conv2d_bwd_weight_nhwc",
+           "mxfp4_quantize_nhwc", "mxfp4_dequantize_nhwc", "mxfp4_linear_nhwc", "mxfp4_linear_bwd_nhwc",
+           "Mxint8Tensor", "mxint8_quantize_nhwc", "mxint8_dequantize_nhwc", "layer_norm_mxint8_nhwc",
+           "layer_norm_bwd_mxint8_nhwc", "Adapters", "mxfp4_linear_adapters_nhwc",
+           "mxfp4_linear_adapters_bwd_nhwc", "conv2d_nhwc", "conv2d_bwd_data_nhwc", "conv2d_bwd_weight_nhwc",
            "conv2d_bwd_data", "conv2d_bwd_data_weights", "conv2d_bwd_weight",
            "conv2d_bwd_weight_workspace", "conv2d_fwd", "conv2d_fwd_autotune",
            "conv2d_fwd_autotune_clear", "conv2d_fwd_nchw", "conv2d_fwd_nchw_workspace", "conv2d_nchw",

@@ -15,6 +15,7 @@ CONVIMG_BF16 = 0
 CONVIMG_FP32 = 1
 CONVIMG_FP16 = 2       # row operators only
 CONVIMG_MXFP4 = 3      # row operators only
+CONVIMG_MXINT8 = 4     # row operators only
 
 CONVIMG_OK = 0
 CONVIMG_ERR_NULL = 1
@@ -52,7 +53,11 @@ EXPORTS = ("conv2d_fwd", "conv2d_fwd_out_dim", "conv2d_fwd_plan", "conv2d_strerr
            "conv2d_fwd_nchw", "conv2d_fwd_nchw_workspace", "conv2d_fwd_test_spin_limit",
            "conv2d_fwd_noalloc", "layer_norm_fwd", "layer_norm_fwd_mxfp4", "layer_norm_bwd",
            "layer_norm_bwd_workspace", "mxfp4_bytes", "mxfp4_quantize", "mxfp4_dequantize",
-           "mxfp4_linear_fwd", "mxfp4_linear_workspace", "mxfp4_linear_bwd", "mxfp4_linear_bwd_workspace")
+           "mxfp4_linear_fwd", "mxfp4_linear_workspace", "mxfp4_linear_bwd", "mxfp4_linear_bwd_workspace",
+           "mxint8_bytes", "mxint8_quantize", "mxint8_dequantize", "layer_norm_fwd_mxint8",
+           "layer_norm_bwd_mxint8", "mxfp4_linear_bwd_mxint8", "mxfp4_linear_adapters_fwd",
+           "mxfp4_linear_adapters_workspace", "mxfp4_linear_adapters_bwd",
+           "mxfp4_linear_adapters_bwd_workspace")
 
 
 class convimg_plan(ctypes.Structure):
@@ -137,7 +142,19 @@ def load(path: str = LIB_PATH):
             ("mxfp4_linear_fwd", [vp, ll, vp, i, vp, vp, vp, i, i, i, i, vp, vp, sz, vp]),
             ("mxfp4_linear_workspace", [i, i, i, i, szp]),
             ("mxfp4_linear_bwd", [vp, ll, i, vp, ll, vp, ll, i, i, i, i, i, vp, vp, vp, vp, sz, vp]),
-            ("mxfp4_linear_bwd_workspace", [i, i, i, szp])):
+            ("mxfp4_linear_bwd_workspace", [i, i, i, szp]),
+            ("mxint8_bytes", [ll, i, szp, szp]),
+            ("mxint8_quantize", [vp, ll, ll, i, i, vp, vp, vp]),
+            ("mxint8_dequantize", [vp, vp, ll, i, i, vp, vp]),
+            ("layer_norm_fwd_mxint8", [vp, ll, vp, vp, ll, i, f, i, i, vp, vp, vp, vp, vp]),
+            ("layer_norm_bwd_mxint8", [vp, ll, vp, vp, vp, vp, ll, i, i, i, vp, vp, vp, vp, sz, vp]),
+            ("mxfp4_linear_bwd_mxint8", [vp, ll, i, vp, vp, vp, ll, i, i, i, i, i, vp, vp, vp, vp, sz, vp]),
+            ("mxfp4_linear_adapters_fwd", [vp, ll, i, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, vp, vp, vp, vp,
+                                           vp, sz, vp]),
+            ("mxfp4_linear_adapters_workspace", [i, i, i, i, i, szp]),
+            ("mxfp4_linear_adapters_bwd", [vp, ll, i, vp, ll, vp, i, vp, vp, vp, vp, vp, vp, i, i, i, vp, i, i, i, i,
+                                           vp, vp, vp, vp, sz, vp]),
+            ("mxfp4_linear_adapters_bwd_workspace", [i, i, i, i, i, szp])):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = i
     _lib = lib
@@ -323,4 +340,71 @@ def mxfp4_linear_bwd_workspace(M, N, K):
     """Returns (status, workspace bytes of mxfp4_linear_bwd)."""
     b = ctypes.c_size_t(0)
     rc = load().mxfp4_linear_bwd_workspace(M, N, K, ctypes.byref(b))
+    return rc, b.value
+
+
+def mxint8_bytes(rows, cols):
+    """Returns (status, bytes of the codes, bytes of the scales) of 8-bit rows."""
+    c, s = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    rc = load().mxint8_bytes(rows, cols, ctypes.byref(c), ctypes.byref(s))
+    return rc, c.value, s.value
+
+
+def mxint8_quantize(x, ldx, rows, cols, dtype, codes, scales, stream):
+    """Raw C call, returns a status."""
+    return load().mxint8_quantize(x, ldx, rows, cols, dtype, codes, scales, stream)
+
+
+def mxint8_dequantize(codes, scales, rows, cols, dtype, out, stream):
+    """Raw C call, returns a status."""
+    return load().mxint8_dequantize(codes, scales, rows, cols, dtype, out, stream)
+
+
+def layer_norm_fwd_mxint8(x, ldx, gamma, beta, rows, cols, eps, x_dtype, y_dtype, y, codes, scales, rstd, stream):
+    """Raw C call, returns a status."""
+    return load().layer_norm_fwd_mxint8(x, ldx, gamma, beta, rows, cols, eps, x_dtype, y_dtype, y, codes, scales,
+                                        rstd, stream)
+
+
+def layer_norm_bwd_mxint8(dy, lddy, codes, scales, gamma, rstd, rows, cols, dy_dtype, dx_dtype, dx, dgamma, dbeta,
+                          ws, ws_bytes, stream):
+    """Raw C call, returns a status."""
+    return load().layer_norm_bwd_mxint8(dy, lddy, codes, scales, gamma, rstd, rows, cols, dy_dtype, dx_dtype, dx,
+                                        dgamma, dbeta, ws, ws_bytes, stream)
+
+
+def mxfp4_linear_bwd_mxint8(dy, lddy, dy_dtype, x_codes, x_scales, w, ldw, w_dtype, M, N, K, dx_dtype, dx, dw, db,
+                            ws, ws_bytes, stream):
+    """Raw C call, returns a status."""
+    return load().mxfp4_linear_bwd_mxint8(dy, lddy, dy_dtype, x_codes, x_scales, w, ldw, w_dtype, M, N, K, dx_dtype,
+                                          dx, dw, db, ws, ws_bytes, stream)
+
+
+def mxfp4_linear_adapters_fwd(x, ldx, x_dtype, w_codes, w_scales, bias, down, up, scale, ids, adapters, rank, a_dtype,
+                              M, N, K, out_dtype, out, h, x_codes, x_scales, ws, ws_bytes, stream):
+    """Raw C call, returns a status."""
+    return load().mxfp4_linear_adapters_fwd(x, ldx, x_dtype, w_codes, w_scales, bias, down, up, scale, ids, adapters,
+                                            rank, a_dtype, M, N, K, out_dtype, out, h, x_codes, x_scales, ws, ws_bytes,
+                                            stream)
+
+
+def mxfp4_linear_adapters_workspace(M, N, K, rank, x_dtype):
+    """Returns (status, workspace bytes of mxfp4_linear_adapters_fwd)."""
+    b = ctypes.c_size_t(0)
+    rc = load().mxfp4_linear_adapters_workspace(M, N, K, rank, x_dtype, ctypes.byref(b))
+    return rc, b.value
+
+
+def mxfp4_linear_adapters_bwd(dy, lddy, dy_dtype, x, ldx, x_scales, x_dtype, wt_codes, wt_scales, down, up, scale, ids,
+                              adapters, rank, a_dtype, h, M, N, K, dx_dtype, dx, ddown, dup, ws, ws_bytes, stream):
+    """Raw C call, returns a status."""
+    return load().mxfp4_linear_adapters_bwd(dy, lddy, dy_dtype, x, ldx, x_scales, x_dtype, wt_codes, wt_scales, down,
+                                            up, scale, ids, adapters, rank, a_dtype, h, M, N, K, dx_dtype, dx, ddown,
+                                            dup, ws, ws_bytes, stream)
+
+
+def mxfp4_linear_adapters_bwd_workspace(M, N, K, adapters, rank):
+    """Returns (status, workspace bytes of mxfp4_linear_adapters_bwd)."""
+    b = ctypes.c_size_t(0)
+    rc = load().mxfp4_linear_adapters_bwd_workspace(M, N, K, adapters, rank, ctypes.byref(b))
     return rc, b.value

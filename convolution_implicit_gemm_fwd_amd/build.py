@@ -24,9 +24,14 @@ EXT = os.path.join(PKG, "_rows.so")
 UNITS = [(os.path.join(CSRC, "conv2d_fwd.hip"), []),
          (os.path.join(CSRC, "conv2d_wgrad.hip"), ["-mllvm", "-amdgpu-mfma-vgpr-form"]),
          (os.path.join(CSRC, "layer_norm.hip"), []),
-         (os.path.join(CSRC, "mxfp4.hip"), [])]
+         (os.path.join(CSRC, "layer_norm_kept.hip"), []),
+         (os.path.join(CSRC, "mxfp4.hip"), []),
+         (os.path.join(CSRC, "mxint8.hip"), []),
+         (os.path.join(CSRC, "adapters.hip"), []),
+         (os.path.join(CSRC, "adapter_shrink.hip"), []),
+         (os.path.join(CSRC, "adapter_grads.hip"), [])]
 SOURCES = [u[0] for u in UNITS]
-DEPENDS = SOURCES + [os.path.join(CSRC, h) for h in ("igemm_common.hpp", "igemm_regs.hpp", "igemm_pipe.hpp", "igemm_patch.hpp", "igemm_strip.hpp", "igemm_window.hpp", "igemm_resident.hpp", "igemm_image.hpp", "igemm_dgrad.hpp", "igemm_wgrad.hpp", "igemm_layout.hpp", "row_common.hpp", "mxfp4_quant.hpp", "mxfp4_gemm.hpp", "mxfp4_few.hpp", "rows_ext.cpp")] + [os.path.join(INCLUDE, "convimg.h")]
+DEPENDS = SOURCES + [os.path.join(CSRC, h) for h in ("igemm_common.hpp", "igemm_regs.hpp", "igemm_pipe.hpp", "igemm_patch.hpp", "igemm_strip.hpp", "igemm_window.hpp", "igemm_resident.hpp", "igemm_image.hpp", "igemm_dgrad.hpp", "igemm_wgrad.hpp", "igemm_layout.hpp", "row_common.hpp", "layer_norm.hpp", "mxint8.hpp", "mxfp4_quant.hpp", "mxfp4_gemm.hpp", "mxfp4_few.hpp", "mxfp4_plan.hpp", "adapter_expand.hpp", "adapter.hpp", "rows_ext.cpp")] + [os.path.join(INCLUDE, "convimg.h")]
 
 ARCH = "gfx950"
 HIPCC_FLAGS = [

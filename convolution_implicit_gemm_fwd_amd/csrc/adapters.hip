@@ -1,0 +1,219 @@
+// adapters.hip -- low-rank adapters of many requests beside the linear layer
+// on 4-bit rows: entry points, and the products with the adapters' second half
+// (adapter_expand.hpp) inside.
+//
+//   h[m]   = down_g x[m],  g = ids[m]              a pass over x that quantises it, too
+//   out[m] = Q(x[m]) W^T + bias + scale_g h[m] up_g     the product
+//
+// Backward, with t[m] = up_g dy[m], the same two steps with down and up
+// exchanged, and the adapters' gradients from t and x, h and dy.
+#include "adapter.hpp"
+
+namespace convimg {
+
+void gemm_adapters(MxGemmArgs g, const MxAdapterArgs &ad, int out_dtype, hipStream_t stream)
+{
+    with_dtype(out_dtype, [&](auto o) {
+        with_shape(shape_of(tiles_of(g.M, g.N), g.kb), [&](auto shape) {
+            typedef decltype(shape) S;
+            const unsigned grid = gemm_grid(g, S::BM, S::BN);
+            hipLaunchKernelGGL((mx_gemm_tile_adapters<S, decltype(o)>), dim3(grid), dim3(S::threads), 0, stream, g, ad);
+        });
+    });
+}
+
+void few_adapters(const MxFewArgs &g, const MxAdapterArgs &ad, int x_dtype, int out_dtype, hipStream_t stream)
+{
+    const int pairs = (g.kb + 7) / 8, waves = pairs < kMxFewWaves ? pairs : kMxFewWaves;
+    with_dtype(x_dtype, [&](auto x) {
+        with_dtype(out_dtype, [&](auto o) {
+            hipLaunchKernelGGL((mx_gemm_few<decltype(x), decltype(o), MxAdapterArgs>), dim3((g.N + 15) / 16),
+                               dim3(waves * 64), 0, stream, g, ad);
+        });
+    });
+}
+
+constexpr int kMaxRank = 4096;
+
+int adapters_shape(int M, int N, int K, int rank)
+{
+    int rc = mx_shape(M, K);
+    if (rc == CONVIMG_OK)
+        rc = N <= 0 ? CONVIMG_ERR_SHAPE : mx_shape(N, K);
+    if (rc == CONVIMG_OK)
+        rc = rank <= 0 ? CONVIMG_ERR_SHAPE : rank > kMaxRank ? CONVIMG_ERR_RANGE : CONVIMG_OK;
+    return rc;
+}
+
+// Workspace of the forward call: x's packed rows, then h's parts.
+size_t fwd_codes(int M, int K) { return few_dense(M, K) ? 0 : packed_bytes(M, K); }
+size_t fwd_h(int M, int K, int rank) { return (size_t)adapter_splits(M, K, false) * M * rank * 4; }
+
+struct AdBwdLayout {
+    size_t dy, t, part_down, part_up, count, total;
+    int split_down, split_up;
+};
+
+AdBwdLayout ad_bwd_layout(int M, int N, int K, int G, int rank)
+{
+    AdBwdLayout l;
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        const size_t here = at;
+        at += align256(n);
+        return here;
+    };
+    l.split_down = adapter_grad_splits(M, K, G, rank);
+    l.split_up = adapter_grad_splits(M, N, G, rank);
+    l.dy = take(packed_bytes(M, N));
+    l.t = take((size_t)M * rank * 4);
+    l.part_down = take(l.split_down > 1 ? (size_t)l.split_down * G * rank * K * 4 : 0);
+    l.part_up = take(l.split_up > 1 ? (size_t)l.split_up * G * rank * N * 4 : 0);
+    l.count = take((size_t)(l.split_down + l.split_up) * G * 4);
+    l.total = at;
+    return l;
+}
+
+int ad_bwd_shape(int M, int N, int K, int adapters, int rank)
+{
+    int rc = adapters_shape(M, K, N, rank);      // dy's rows and wt's
+    if (rc == CONVIMG_OK)
+        rc = mx_shape(M, K);
+    return rc != CONVIMG_OK ? rc : adapters <= 0 ? CONVIMG_ERR_SHAPE : CONVIMG_OK;
+}
+
+}  // namespace convimg
+
+using namespace convimg;
+
+extern "C" {
+
+int mxfp4_linear_adapters_workspace(int M, int N, int K, int rank, int x_dtype, size_t *bytes)
+{
+    if (!bytes)
+        return CONVIMG_ERR_NULL;
+    const int rc = adapters_shape(M, N, K, rank);
+    if (rc != CONVIMG_OK)
+        return rc;
+    if (!dtype_ok(x_dtype))
+        return CONVIMG_ERR_DTYPE;
+    *bytes = fwd_codes(M, K) + fwd_h(M, K, rank);
+    return CONVIMG_OK;
+}
+
+int mxfp4_linear_adapters_fwd(const void *x, long long ldx, int x_dtype, const void *w_codes, const void *w_scales,
+                              const float *bias, const void *down, const void *up, const float *scale, const int *ids,
+                              int adapters, int rank, int a_dtype, int M, int N, int K, int out_dtype, void *out,
+                              float *h, void *x_codes, void *x_scales, void *ws, size_t ws_bytes, hipStream_t stream)
+{
+    size_t need = 0;
+    const int rc = mxfp4_linear_adapters_workspace(M, N, K, rank, x_dtype, &need);
+    if (rc != CONVIMG_OK)
+        return rc;
+    if (!dtype_ok(out_dtype) || !dtype_ok(a_dtype))
+        return CONVIMG_ERR_DTYPE;
+    if (ldx < K || adapters <= 0)
+        return CONVIMG_ERR_SHAPE;
+    if (M == 0)
+        return CONVIMG_OK;
+    if (!x || !w_codes || !w_scales || !down || !up || !scale || !ids || !out || !ws || (!x_codes) != (!x_scales))
+        return CONVIMG_ERR_NULL;
+    if (misaligned(w_codes, 16) || misaligned(w_scales, 4) || misaligned(ws, 16) || misaligned(x_codes, 16)
+        || misaligned(x_scales, 4))
+        return CONVIMG_ERR_ALIGN;
+    if (ws_bytes < need)
+        return CONVIMG_ERR_WORKSPACE;
+    const size_t na = (size_t)adapters * rank * dtype_bytes(a_dtype);
+    const void *in[8] = {x, w_codes, w_scales, bias, down, up, scale, ids}, *outs[5] = {out, h, x_codes, x_scales, ws};
+    const size_t nin[8] = {span_bytes(M, ldx, K, x_dtype), mx_code_bytes(N, K), mx_scale_bytes(N, K), (size_t)N * 4, na * K,
+                           na * N, (size_t)adapters * 4, (size_t)M * 4},
+                 nout[5] = {span_bytes(M, N, N, out_dtype), (size_t)M * rank * 4, mxi_code_bytes(M, K),
+                            mxi_scale_bytes(M, K), need};
+    if (any_overlap(outs, nout, 5, in, nin, 8))
+        return CONVIMG_ERR_ALIAS;
+    // (what is kept has to be whole, not in parts)
+    const bool keep = h || x_codes;
+    const int splits = adapter_splits(M, K, keep);
+    unsigned char *codes = fwd_codes(M, K) ? (unsigned char *)ws : nullptr,
+                  *scales = codes ? codes + align256(mx_code_bytes(M, K)) : nullptr;
+    float *hh = h ? h : (float *)((unsigned char *)ws + fwd_codes(M, K));
+    const AdShrinkArgs s = {x,      down, ids, hh, codes, scales, (unsigned char *)x_codes, (unsigned char *)x_scales,
+                            ldx,    M,    K,   adapters, rank};
+    adapter_shrink(s, x_dtype, a_dtype, splits, stream);
+    const MxAdapterArgs ad = {hh, up, scale, ids, adapters, rank, splits, a_dtype};
+    const MxOperand b = {(const unsigned char *)w_codes, (const unsigned char *)w_scales};
+    if (!codes)
+        few_adapters({x, b.codes, b.scales, bias, out, ldx, M, N, K, mx_blocks(K)}, ad, x_dtype, out_dtype, stream);
+    else
+        gemm_adapters(gemm_args({codes, scales}, b, bias, M, N, K, out), ad, out_dtype, stream);
+    return launched();
+}
+
+int mxfp4_linear_adapters_bwd_workspace(int M, int N, int K, int adapters, int rank, size_t *bytes)
+{
+    if (!bytes)
+        return CONVIMG_ERR_NULL;
+    const int rc = ad_bwd_shape(M, N, K, adapters, rank);
+    if (rc != CONVIMG_OK)
+        return rc;
+    *bytes = ad_bwd_layout(M, N, K, adapters, rank).total;
+    return CONVIMG_OK;
+}
+
+int mxfp4_linear_adapters_bwd(const void *dy, long long lddy, int dy_dtype, const void *x, long long ldx,
+                              const void *x_scales, int x_dtype, const void *wt_codes, const void *wt_scales,
+                              const void *down, const void *up, const float *scale, const int *ids, int adapters,
+                              int rank, int a_dtype, const float *h, int M, int N, int K, int dx_dtype, void *dx,
+                              float *ddown, float *dup, void *ws, size_t ws_bytes, hipStream_t stream)
+{
+    const int rc = ad_bwd_shape(M, N, K, adapters, rank);
+    if (rc != CONVIMG_OK)
+        return rc;
+    const bool kept = x_dtype == CONVIMG_MXINT8;
+    if (!dtype_ok(dy_dtype) || !(kept || dtype_ok(x_dtype)) || !dtype_ok(a_dtype) || !dtype_ok(dx_dtype))
+        return CONVIMG_ERR_DTYPE;
+    if (lddy < N || (!kept && ldx < K))
+        return CONVIMG_ERR_SHAPE;
+    if (!ddown || !dup || !ws || (wt_codes && !wt_scales)
+        || (M > 0 && (!dy || !x || (kept && !x_scales) || !down || !up || !scale || !ids || !h || (!dx) != (!wt_codes))))
+        return CONVIMG_ERR_NULL;
+    if (misaligned(ws, 16) || misaligned(wt_codes, 16) || misaligned(wt_scales, 4)
+        || (kept && (misaligned(x, 16) || misaligned(x_scales, 4))))
+        return CONVIMG_ERR_ALIGN;
+    const AdBwdLayout l = ad_bwd_layout(M, N, K, adapters, rank);
+    if (ws_bytes < l.total)
+        return CONVIMG_ERR_WORKSPACE;
+    const size_t na = (size_t)adapters * rank, ab = dtype_bytes(a_dtype);
+    const void *in[10] = {dy, x, kept ? x_scales : nullptr, wt_codes, wt_scales, down, up, scale, ids, h},
+               *outs[4] = {dx, ddown, dup, ws};
+    const size_t nin[10] = {span_bytes(M, lddy, N, dy_dtype), kept ? mxi_code_bytes(M, K) : span_bytes(M, ldx, K, x_dtype),
+                            mxi_scale_bytes(M, K), mx_code_bytes(K, N), mx_scale_bytes(K, N), na * K * ab, na * N * ab,
+                            (size_t)adapters * 4, (size_t)M * 4, (size_t)M * rank * 4},
+                 nout[4] = {span_bytes(M, K, K, dx_dtype), na * K * 4, na * N * 4, l.total};
+    if (any_overlap(outs, nout, 4, in, nin, 10))
+        return CONVIMG_ERR_ALIAS;
+    if (M == 0) {
+        fill_zero(ddown, (long long)(na * K), stream);
+        fill_zero(dup, (long long)(na * N), stream);
+        return launched();
+    }
+    unsigned char *base = (unsigned char *)ws, *codes = base + l.dy, *scales = codes + align256(mx_code_bytes(M, N));
+    float *t = (float *)(base + l.t);
+    int *count = (int *)(base + l.count);
+    const AdShrinkArgs s = {dy, up, ids, t, dx ? codes : nullptr, scales, nullptr, nullptr, lddy, M, N, adapters, rank};
+    adapter_shrink(s, dy_dtype, a_dtype, 1, stream);
+    if (dx) {
+        const MxAdapterArgs ad = {t, down, scale, ids, adapters, rank, 1, a_dtype};
+        gemm_adapters(gemm_args({codes, scales}, {(const unsigned char *)wt_codes, (const unsigned char *)wt_scales},
+                                nullptr, M, K, N, dx),
+                      ad, dx_dtype, stream);
+    }
+    adapter_grad({h, dy, nullptr, ids, scale, dup, (float *)(base + l.part_up), count, lddy, M, N, adapters, rank}, dy_dtype,
+                 l.split_up, stream);
+    adapter_grad({t, x, (const unsigned char *)x_scales, ids, scale, ddown, (float *)(base + l.part_down),
+                  count + (long long)l.split_up * adapters, ldx, M, K, adapters, rank},
+                 x_dtype, l.split_down, stream);
+    return launched();
+}
+
+}  // extern "C"

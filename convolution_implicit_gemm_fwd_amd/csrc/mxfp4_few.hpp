@@ -39,9 +39,11 @@ struct MxFewArgs {
     int M, N, K, kb;
 };
 
-template <typename X, typename O>
-__global__ __launch_bounds__(kMxFewWaves * 64) void mx_gemm_few(MxFewArgs g)
+// AD: MxAdapterArgs adds each row's low-rank adapter, MxNoAdapters nothing.
+template <typename X, typename O, typename AD = MxNoAdapters>
+__global__ __launch_bounds__(kMxFewWaves * 64) void mx_gemm_few(MxFewArgs g, AD ad)
 {
+    constexpr bool ADAPT = !__is_same(AD, MxNoAdapters);
     __shared__ __attribute__((aligned(16))) unsigned char rows[kMxFewRows];
     __shared__ __attribute__((aligned(16))) unsigned char ring[kMxFewWaves][kMxFewRing][kMxFewStage];
     constexpr int PER = 3;                      // copies a stage
@@ -100,9 +102,47 @@ __global__ __launch_bounds__(kMxFewWaves * 64) void mx_gemm_few(MxFewArgs g)
     for (int i = 0; i < AHEAD; ++i)
         if (i < g.M * per)
             load_row(i, raw[i]);
+    // Adapters: thread 16 i + n takes the ranks i, i + 4 waves, .. of column n.
+    // h comes in before the weights, up behind their first stages.
+    [[maybe_unused]] float low[kMxFewM] = {}, h0[kMxFewM] = {};
+    if constexpr (ADAPT)
+#pragma unroll
+        for (int m = 0; m < kMxFewM; ++m)
+            if (m < g.M && (int)(threadIdx.x >> 4) < ad.r)
+                for (int k = 0; k < ad.splits; ++k)
+                    h0[m] += ad.h[((long long)k * g.M + m) * ad.r + (threadIdx.x >> 4)];
 #pragma unroll
     for (int u = 0; u < kMxFewRing; ++u)
         fetch(u * waves + wave, u);
+    if constexpr (ADAPT) {
+        const int n = n0 + (threadIdx.x & 15), first = threadIdx.x >> 4, step = blockDim.x >> 4;
+        auto add = [&](auto type) {
+            typedef decltype(type) T;
+#pragma unroll
+            for (int m = 0; m < kMxFewM; ++m) {
+                const int id = m < g.M ? ad.ids[m] : -1;
+                if (id < 0 || id >= ad.G || n >= g.N)
+                    continue;
+                const typename T::raw *up = (const typename T::raw *)ad.up + (long long)id * ad.r * g.N + n;
+                for (int i = first; i < ad.r; i += step) {
+                    float h = h0[m];
+                    if (i != first) {
+                        h = 0.f;
+                        for (int k = 0; k < ad.splits; ++k)
+                            h += ad.h[((long long)k * g.M + m) * ad.r + i];
+                    }
+                    low[m] = __builtin_fmaf(h, load1<T>(up + (long long)i * g.N), low[m]);
+                }
+                low[m] *= ad.scale[id];
+            }
+        };
+        if (ad.dtype == CONVIMG_BF16)
+            add(Bf16{});
+        else if (ad.dtype == CONVIMG_FP16)
+            add(Fp16{});
+        else
+            add(Fp32{});
+    }
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i)
         if (i < g.M * per)
@@ -151,6 +191,14 @@ __global__ __launch_bounds__(kMxFewWaves * 64) void mx_gemm_few(MxFewArgs g)
     // the waves' sums, in order; a wave's lie in its own ring
     if (r16 < g.M)
         *(f32x4_t *)(ring[wave][0] + (r16 * 16 + b4 * 4) * 4) = acc;
+    if constexpr (ADAPT)
+#pragma unroll
+        for (int m = 0; m < kMxFewM; ++m)
+            if (m < g.M) {
+                const float s = stride_sum<16>(low[m]);
+                if (lane < 16)
+                    *(float *)(ring[wave][0] + kMxFewM * 64 + (m * 16 + lane) * 4) = s;
+            }
     mx_wait_lds();
     mx_barrier();
     for (int e = threadIdx.x; e < g.M * 16; e += blockDim.x) {
@@ -159,6 +207,9 @@ __global__ __launch_bounds__(kMxFewWaves * 64) void mx_gemm_few(MxFewArgs g)
             float s = g.bias ? g.bias[n] : 0.f;
             for (int k = 0; k < waves; ++k)
                 s += *(const float *)(ring[k][0] + e * 4);
+            if constexpr (ADAPT)
+                for (int k = 0; k < waves; ++k)
+                    s += *(const float *)(ring[k][0] + kMxFewM * 64 + e * 4);
             store1<O>((typename O::raw *)g.out + (long long)(e >> 4) * g.N + n, s);
         }
     }

@@ -17,13 +17,13 @@
 // the copies changes nothing.
 #pragma once
 
+#include "adapter_expand.hpp"
 #include "mxfp4_quant.hpp"
 
 namespace convimg {
 
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
-typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
 constexpr unsigned kMxOutOfRange = 0x80000000u;   // buffer offset past every packed operand
 constexpr int kMxRsrcWord3 = 0x00020000;          // raw buffer, 32-bit data format
@@ -110,8 +110,11 @@ constexpr int mx_gemm_lds()
 // groups of such waves each takes one run of the K tiles, in a ring of its
 // own, and their sums meet in LDS at the end: where there are few output
 // tiles this keeps more copies in flight a CU.
-template <typename S, typename O>
-__device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsigned char *smem)
+//
+// AD: MxAdapterArgs adds each row's low-rank adapter to the sums, MxNoAdapters
+// nothing.
+template <typename S, typename O, typename AD = MxNoAdapters>
+__device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsigned char *smem, const AD &ad = {})
 {
     constexpr int BM = S::BM, BN = S::BN, BK = S::BK, WM = S::WM, NW = S::WM * S::WN, STAGES = S::STAGES, KG = S::KG;
     constexpr int TM = BM / S::WM, TN = BN / S::WN;         // a wave's tile
@@ -240,6 +243,10 @@ __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsign
 #pragma unroll
         for (int c = 0; c < (t < STAGES - 1 ? PER : E0); ++c)
             issue1(t0 + t, c);
+    // (adapters while the copies are under way)
+    if constexpr (!__is_same(AD, MxNoAdapters))
+        if (group == 0)
+            adapter_expand<FM, FN>(ad, g.M, g.N, m0 + wm * TM, n0 + wn * TN, acc);
 
     // Step h of a K tile takes two blocks of each row.  Of eight, lanes 0 .. 31
     // take block h and the others block 4 + h, so that each half needs one
@@ -420,6 +427,15 @@ __global__ __launch_bounds__(S::threads) void mx_gemm_tile(MxGemmArgs g)
     const unsigned id = mx_xcd_tile(blockIdx.x, gridDim.x);
     if (id < (unsigned)g.tm * g.tn)
         mx_gemm_body<S, O>(g, id, smem);
+}
+
+template <typename S, typename O>
+__global__ __launch_bounds__(S::threads) void mx_gemm_tile_adapters(MxGemmArgs g, MxAdapterArgs ad)
+{
+    __shared__ __attribute__((aligned(16))) unsigned char smem[mx_gemm_lds<S, sizeof(typename O::raw)>()];
+    const unsigned id = mx_xcd_tile(blockIdx.x, gridDim.x);
+    if (id < (unsigned)g.tm * g.tn)
+        mx_gemm_body<S, O>(g, id, smem, ad);
 }
 
 // Column sums from partial sums [parts][cols], 64 columns a workgroup.

@@ -10,7 +10,7 @@
 // columns 36 us (170 MB, 4.7 TB/s; a copy of 256 MiB reaches 5.2).
 #pragma once
 
-#include "row_common.hpp"
+#include "mxint8.hpp"
 
 namespace convimg {
 
@@ -79,8 +79,10 @@ __global__ __launch_bounds__(kMxThreads) void mx_quantize_rows(MxQuantArgs a)
 // A matrix that is quantised in tiles: down its columns into ccodes
 // [cols][rows / 32 blocks], along its rows into rcodes, and summed down its
 // columns, one partial sum a row of tiles.
+// An operand kept in 8 bits is given by its codes and xs, its scale bytes.
 struct MxTileArgs {
     const void *x;
+    const unsigned char *xs;
     long long ldx;
     int rows, cols;
     unsigned char *ccodes, *cscales, *rcodes, *rscales;
@@ -119,9 +121,26 @@ __device__ __forceinline__ unsigned mx_encode32(const float (&v)[32], u32v4_t &q
     return byte;
 }
 
+// Eight values of a row kept in 8 bits as bf16, which holds them exactly.
+__device__ __forceinline__ Raw8<Bf16> load_kept8(const MxTileArgs &a, int row, int col)
+{
+    Raw8<Bf16> r = {};
+    if (row < a.rows && col < a.cols) {
+        const int kp = (a.cols + 31) & ~31;
+        float v[8];
+        mxi_decode8(*(const uint2 *)((const unsigned char *)a.x + (long long)row * kp + col),
+                    mxi_unit(a.xs, row, a.cols, col), v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            r.w[0][e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+    }
+    return r;
+}
+
 // One tile, by the whole workgroup; lds: mx_tile_lds<T>() bytes, 16-byte
-// aligned.  ROWS: along the rows and the column sums too.
-template <typename T, bool ROWS>
+// aligned.  ROWS: along the rows and the column sums too.  KEPT: of an operand
+// in 8 bits, which is bf16 from there on.
+template <typename T, bool ROWS, bool KEPT = false>
 __device__ __forceinline__ void mx_quantize_tile(const MxTileArgs &a, unsigned tile, unsigned char *lds)
 {
     constexpr int PITCH = mx_tile_pitch<T>(), ES = sizeof(typename T::raw);
@@ -143,7 +162,12 @@ __device__ __forceinline__ void mx_quantize_tile(const MxTileArgs &a, unsigned t
     const bool whole = r0 + kMxTile <= a.rows && c0 + kMxTile <= a.cols;
     const int lr = t >> 4, lc = (t & 15) * 8;
     Raw8<T> raw[PASSES];
-    if (whole) {
+    if constexpr (KEPT) {
+        static_assert(!ROWS && T::code == CONVIMG_BF16, "bf16 values, down the columns");
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p)
+            raw[p] = load_kept8(a, r0 + lr + p * LR, c0 + lc);
+    } else if (whole) {
         const typename T::raw *x = (const typename T::raw *)a.x + (long long)(r0 + lr) * a.ldx + c0 + lc;
 #pragma unroll
         for (int p = 0; p < PASSES; ++p)
@@ -238,7 +262,8 @@ __global__ __launch_bounds__(kMxTileThreads) void mx_quantize_cols(MxTileArgs a,
 // The operands of the backward pass in one launch: dy both ways with its
 // column sums, w and x down their columns (8192x4096x4096 bf16: 46 us for 232
 // MB, 5.0 TB/s).
-template <typename DY, typename X>
+// KEPT: x is kept in 8 bits; X is then w's type alone.
+template <typename DY, typename X, bool KEPT>
 __global__ __launch_bounds__(kMxTileThreads) void mx_quantize_bwd(MxTileArgs dy, MxTileArgs w, MxTileArgs x,
                                                               unsigned dy_tiles, unsigned w_tiles, unsigned x_tiles)
 {
@@ -256,8 +281,14 @@ __global__ __launch_bounds__(kMxTileThreads) void mx_quantize_bwd(MxTileArgs dy,
     const unsigned b = blockIdx.x - dy_blocks;
     const bool is_w = b < w_blocks;
     const unsigned tile = is_w ? mx_xcd_tile(b, w_blocks) : mx_xcd_tile(b - w_blocks, (x_tiles + 7) & ~7u);
-    if (tile < (is_w ? w_tiles : x_tiles))
+    if constexpr (KEPT) {
+        if (is_w && tile < w_tiles)
+            mx_quantize_tile<X, false>(w, tile, lds);
+        else if (!is_w && tile < x_tiles)
+            mx_quantize_tile<Bf16, false, true>(x, tile, lds);
+    } else if (tile < (is_w ? w_tiles : x_tiles)) {
         mx_quantize_tile<X, false>(is_w ? w : x, tile, lds);
+    }
 }
 
 // MXFP4 rows to values: a thread takes 8 columns.

@@ -365,12 +365,37 @@ inline int mx_shape(long long rows, long long cols)
     return CONVIMG_OK;
 }
 
+// Threads a row (log2): enough for its columns, eight a thread, up to a
+// workgroup of 256; at least the four lanes of a block.
+inline int row_lg(int cols)
+{
+    int lg = 2;
+    while (lg < 8 && (8 << lg) < cols)
+        ++lg;
+    return lg;
+}
+
 inline bool row_overlaps(const void *a, size_t na, const void *b, size_t nb)
 {
     if (!a || !b || !na || !nb)
         return false;
     const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
     return x < y + nb && y < x + na;
+}
+
+// Whether one of the outputs overlaps an input or another output.
+inline bool any_overlap(const void *const *out, const size_t *nout, int outs, const void *const *in, const size_t *nin,
+                        int ins)
+{
+    for (int i = 0; i < outs; ++i) {
+        for (int j = 0; j < ins; ++j)
+            if (row_overlaps(out[i], nout[i], in[j], nin[j]))
+                return true;
+        for (int j = 0; j < i; ++j)
+            if (row_overlaps(out[i], nout[i], out[j], nout[j]))
+                return true;
+    }
+    return false;
 }
 
 // Bytes from the first to the last element of `rows` rows of `cols` that

@@ -34,6 +34,15 @@ decltype(&mxfp4_linear_fwd) p_mxfp4_linear_fwd;
 decltype(&mxfp4_linear_workspace) p_mxfp4_linear_workspace;
 decltype(&mxfp4_linear_bwd) p_mxfp4_linear_bwd;
 decltype(&mxfp4_linear_bwd_workspace) p_mxfp4_linear_bwd_workspace;
+decltype(&mxint8_quantize) p_mxint8_quantize;
+decltype(&mxint8_dequantize) p_mxint8_dequantize;
+decltype(&layer_norm_fwd_mxint8) p_layer_norm_fwd_mxint8;
+decltype(&layer_norm_bwd_mxint8) p_layer_norm_bwd_mxint8;
+decltype(&mxfp4_linear_bwd_mxint8) p_mxfp4_linear_bwd_mxint8;
+decltype(&mxfp4_linear_adapters_fwd) p_mxfp4_linear_adapters_fwd;
+decltype(&mxfp4_linear_adapters_workspace) p_mxfp4_linear_adapters_workspace;
+decltype(&mxfp4_linear_adapters_bwd) p_mxfp4_linear_adapters_bwd;
+decltype(&mxfp4_linear_adapters_bwd_workspace) p_mxfp4_linear_adapters_bwd_workspace;
 
 int type_code(at::ScalarType t)
 {
@@ -201,6 +210,91 @@ struct Given {
             && codes->is_contiguous() && scales->is_contiguous();
     }
 };
+
+// Rows kept in 8 bits, to write.
+struct Kept8 {
+    at::Tensor codes, scales;
+    int64_t rows, cols;
+
+    Kept8(int64_t r, int64_t c, const at::Tensor &like) : rows(r), cols(c)
+    {
+        codes = fresh({r, (c + 31) / 32 * 32}, at::kChar, like);
+        scales = fresh({r, (c + 127) / 128 * 4}, at::kByte, like);
+    }
+    // As (codes, scales, rows, columns); NULL if Python fails.
+    PyObject *object() const
+    {
+        return Py_BuildValue("(NNLL)", THPVariable_Wrap(codes), THPVariable_Wrap(scales), (long long)rows, (long long)cols);
+    }
+};
+
+// Such rows, to read: (codes, scales, rows, columns).
+struct Given8 {
+    const at::Tensor *codes = nullptr, *scales = nullptr;
+    int64_t rows = 0;
+    int cols = 0;
+
+    bool of(PyObject *o)
+    {
+        if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 4)
+            return false;
+        const long r = PyLong_AsLong(PyTuple_GET_ITEM(o, 2)), c = PyLong_AsLong(PyTuple_GET_ITEM(o, 3));
+        if (PyErr_Occurred()) {
+            PyErr_Clear();
+            return false;
+        }
+        if (r <= 0 || c <= 0 || r > INT32_MAX || c > INT32_MAX || !tensor_of(PyTuple_GET_ITEM(o, 0), codes)
+            || !tensor_of(PyTuple_GET_ITEM(o, 1), scales))
+            return false;
+        rows = r;
+        cols = (int)c;
+        return codes->scalar_type() == at::kChar && scales->scalar_type() == at::kByte
+            && codes->sizes() == at::IntArrayRef({r, (c + 31) / 32 * 32})
+            && scales->sizes() == at::IntArrayRef({r, (c + 127) / 128 * 4}) && codes->is_contiguous()
+            && scales->is_contiguous();
+    }
+};
+
+// The adapters of a layer K -> N: (down, up, scale).
+struct Low {
+    const at::Tensor *down = nullptr, *up = nullptr;
+    float *scale = nullptr;
+    int number = 0, rank = 0, type = -1;
+
+    bool of(PyObject *o, int64_t N, int64_t K)
+    {
+        if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 3 || !tensor_of(PyTuple_GET_ITEM(o, 0), down)
+            || !tensor_of(PyTuple_GET_ITEM(o, 1), up) || down->dim() != 3 || up->dim() != 3)
+            return false;
+        const int64_t g = down->size(0), r = down->size(1);
+        if (g <= 0 || r <= 0 || g > INT32_MAX || r > INT32_MAX || down->size(2) != K
+            || up->sizes() != at::IntArrayRef({g, r, N}) || !down->is_contiguous() || !up->is_contiguous()
+            || down->scalar_type() != up->scalar_type() || !vector_of(PyTuple_GET_ITEM(o, 2), g, false, scale))
+            return false;
+        number = (int)g;
+        rank = (int)r;
+        type = type_code(down->scalar_type());
+        return type >= 0;
+    }
+};
+
+// int32 of the given shape, one a row.
+bool ids_of(PyObject *o, at::IntArrayRef shape, const int *&p)
+{
+    const at::Tensor *t;
+    if (!tensor_of(o, t) || t->scalar_type() != at::kInt || t->sizes() != shape || !t->is_contiguous())
+        return false;
+    p = static_cast<const int *>(t->data_ptr());
+    return true;
+}
+
+// (a, the kept rows, b) or None if the call was refused.
+PyObject *result_kept(int rc, const at::Tensor &a, const Kept8 &q, const at::Tensor &b)
+{
+    if (rc != CONVIMG_OK)
+        Py_RETURN_NONE;
+    return Py_BuildValue("(NNN)", THPVariable_Wrap(a), q.object(), THPVariable_Wrap(b));
+}
 
 // Runs f; a C++ exception (an allocation that fails) becomes torch's Python
 // exception for it.
@@ -380,11 +474,39 @@ PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t count)
     });
 }
 
+// (dy, x, w, dx_dtype); x as rows kept in 8 bits
+PyObject *linear_bwd_kept(PyObject *const *a)
+{
+    Rows dy, w;
+    Given8 x;
+    at::ScalarType t;
+    if (!dy.of(a[0]) || !x.of(a[1]) || !w.of(a[2]) || w.t->dim() != 2 || w.rows != dy.cols || w.cols != x.cols
+        || x.rows != dy.rows || !type_of(a[3], w.t->scalar_type(), t))
+        Py_RETURN_NONE;
+    const int M = (int)dy.rows, N = dy.cols, K = x.cols;
+    size_t need = 0;
+    if (p_mxfp4_linear_bwd_workspace(M, N, K, &need) != CONVIMG_OK)
+        Py_RETURN_NONE;
+    c10::SmallVector<int64_t, 8> sizes(dy.t->sizes().begin(), dy.t->sizes().end() - 1);
+    sizes.push_back(K);
+    const at::Tensor dx = fresh(sizes, t, *dy.t), dw = fresh({N, K}, at::kFloat, dx), db = fresh({N}, at::kFloat, dx),
+                     ws = fresh({(int64_t)need}, at::kByte, dx);
+    const hipStream_t s = stream_of(dx);
+    return result(unlocked([&] {
+                      return p_mxfp4_linear_bwd_mxint8(dy.p, dy.ld, dy.type, x.codes->data_ptr(), x.scales->data_ptr(),
+                                                       w.p, w.ld, w.type, M, N, K, type_code(t), dx.data_ptr(),
+                                                       dw.data_ptr<float>(), db.data_ptr<float>(), ws.data_ptr(), need, s);
+                  }),
+                  dx, dw, db);
+}
+
 // (dy, x, w, dx_dtype)
 PyObject *linear_bwd(PyObject *, PyObject *const *a, Py_ssize_t count)
 {
     ARGS(4)
     return guarded([&]() -> PyObject * {
+        if (PyTuple_Check(a[1]))
+            return linear_bwd_kept(a);
         Rows dy, x, w;
         at::ScalarType t;
         if (!dy.of(a[0]) || !x.of(a[1]) || !w.of(a[2]) || w.t->dim() != 2 || w.rows != dy.cols || w.cols != x.cols
@@ -405,6 +527,184 @@ PyObject *linear_bwd(PyObject *, PyObject *const *a, Py_ssize_t count)
                                                     db.data_ptr<float>(), ws.data_ptr(), need, s);
                       }),
                       dx, dw, db);
+    });
+}
+
+// (x): rows kept in 8 bits
+PyObject *quantize8(PyObject *, PyObject *const *a, Py_ssize_t count)
+{
+    ARGS(1)
+    return guarded([&]() -> PyObject * {
+        Rows x;
+        if (!x.of(a[0]))
+            Py_RETURN_NONE;
+        const Kept8 q(x.rows, x.cols, *x.t);
+        const hipStream_t s = stream_of(*x.t);
+        const int rc = unlocked([&] {
+            return p_mxint8_quantize(x.p, x.ld, x.rows, x.cols, x.type, q.codes.data_ptr(), q.scales.data_ptr(), s);
+        });
+        if (rc != CONVIMG_OK)
+            Py_RETURN_NONE;
+        return q.object();
+    });
+}
+
+// (q, dtype)
+PyObject *dequantize8(PyObject *, PyObject *const *a, Py_ssize_t count)
+{
+    ARGS(2)
+    return guarded([&]() -> PyObject * {
+        Given8 q;
+        at::ScalarType t;
+        if (!q.of(a[0]) || a[1] == Py_None || !type_of(a[1], at::kFloat, t))
+            Py_RETURN_NONE;
+        const at::Tensor out = fresh({q.rows, q.cols}, t, *q.codes);
+        const hipStream_t s = stream_of(out);
+        return result(unlocked([&] {
+                          return p_mxint8_dequantize(q.codes->data_ptr(), q.scales->data_ptr(), q.rows, q.cols,
+                                                     type_code(t), out.data_ptr(), s);
+                      }),
+                      out);
+    });
+}
+
+// (x, gamma, beta, eps, out_dtype): y, the kept rows, rstd
+PyObject *layer_norm_kept(PyObject *, PyObject *const *a, Py_ssize_t count)
+{
+    ARGS(5)
+    return guarded([&]() -> PyObject * {
+        Rows x;
+        float *g, *b;
+        at::ScalarType t;
+        if (!x.of(a[0]) || !vector_of(a[1], x.cols, true, g) || !vector_of(a[2], x.cols, true, b)
+            || !PyFloat_Check(a[3]) || !type_of(a[4], x.t->scalar_type(), t))
+            Py_RETURN_NONE;
+        const float eps = (float)PyFloat_AS_DOUBLE(a[3]);
+        const auto sizes = x.t->sizes();
+        const at::Tensor y = fresh(sizes, t, *x.t), rstd = fresh(sizes.slice(0, sizes.size() - 1), at::kFloat, *x.t);
+        const Kept8 q(x.rows, x.cols, *x.t);
+        const hipStream_t s = stream_of(*x.t);
+        const int rc = unlocked([&] {
+            return p_layer_norm_fwd_mxint8(x.p, x.ld, g, b, x.rows, x.cols, eps, x.type, type_code(t), y.data_ptr(),
+                                           q.codes.data_ptr(), q.scales.data_ptr(), rstd.data_ptr<float>(), s);
+        });
+        return result_kept(rc, y, q, rstd);
+    });
+}
+
+// (dy, kept, gamma, rstd, dx_dtype)
+PyObject *layer_norm_kept_bwd(PyObject *, PyObject *const *a, Py_ssize_t count)
+{
+    ARGS(5)
+    return guarded([&]() -> PyObject * {
+        Rows dy;
+        Given8 q;
+        float *g;
+        const at::Tensor *rstd;
+        at::ScalarType t;
+        if (!dy.of(a[0]) || !q.of(a[1]) || q.rows != dy.rows || q.cols != dy.cols || !vector_of(a[2], dy.cols, true, g)
+            || !tensor_of(a[3], rstd) || rstd->scalar_type() != at::kFloat || rstd->numel() != dy.rows
+            || !rstd->is_contiguous() || !type_of(a[4], dy.t->scalar_type(), t))
+            Py_RETURN_NONE;
+        size_t need = 0;
+        if (p_layer_norm_bwd_workspace(dy.rows, dy.cols, &need) != CONVIMG_OK)
+            Py_RETURN_NONE;
+        const at::Tensor dx = fresh(dy.t->sizes(), t, *dy.t), dgamma = fresh({dy.cols}, at::kFloat, dx),
+                         dbeta = fresh({dy.cols}, at::kFloat, dx), ws = fresh({(int64_t)need}, at::kByte, dx);
+        const hipStream_t s = stream_of(dx);
+        return result(unlocked([&] {
+                          return p_layer_norm_bwd_mxint8(dy.p, dy.ld, q.codes->data_ptr(), q.scales->data_ptr(), g,
+                                                         rstd->data_ptr<float>(), dy.rows, dy.cols, dy.type, type_code(t),
+                                                         dx.data_ptr(), dgamma.data_ptr<float>(),
+                                                         dbeta.data_ptr<float>(), ws.data_ptr(), need, s);
+                      }),
+                      dx, dgamma, dbeta);
+    });
+}
+
+// (x, w, bias, adapters, ids, out_dtype, save)
+PyObject *adapters(PyObject *, PyObject *const *a, Py_ssize_t count)
+{
+    ARGS(7)
+    return guarded([&]() -> PyObject * {
+        Given w;
+        Rows x;
+        Low low;
+        float *b;
+        const int *ids;
+        at::ScalarType t;
+        if (!x.of(a[0]) || !w.of(a[1]) || x.cols != w.cols || !vector_of(a[2], w.rows, true, b)
+            || !low.of(a[3], w.rows, w.cols) || !ids_of(a[4], x.t->sizes().slice(0, x.t->dim() - 1), ids)
+            || !type_of(a[5], x.t->scalar_type(), t) || !PyBool_Check(a[6]))
+            Py_RETURN_NONE;
+        const int M = (int)x.rows, N = w.rows, K = w.cols;
+        size_t need = 0;
+        if (p_mxfp4_linear_adapters_workspace(M, N, K, low.rank, x.type, &need) != CONVIMG_OK)
+            Py_RETURN_NONE;
+        c10::SmallVector<int64_t, 8> sizes(x.t->sizes().begin(), x.t->sizes().end());
+        sizes.back() = N;
+        const at::Tensor out = fresh(sizes, t, *x.t), ws = fresh({(int64_t)need}, at::kByte, *x.t);
+        const hipStream_t s = stream_of(out);
+        auto call = [&](float *h, void *codes, void *scales) {
+            return unlocked([&] {
+                return p_mxfp4_linear_adapters_fwd(x.p, x.ld, x.type, w.codes->data_ptr(), w.scales->data_ptr(), b,
+                                                   low.down->data_ptr(), low.up->data_ptr(), low.scale, ids, low.number,
+                                                   low.rank, low.type, M, N, K, type_code(t), out.data_ptr(), h, codes,
+                                                   scales, ws.data_ptr(), need, s);
+            });
+        };
+        if (a[6] != Py_True)
+            return result(call(nullptr, nullptr, nullptr), out);
+        const Kept8 q(M, K, out);
+        sizes.back() = low.rank;
+        const at::Tensor h = fresh(sizes, at::kFloat, out);
+        return result_kept(call(h.data_ptr<float>(), q.codes.data_ptr(), q.scales.data_ptr()), out, q, h);
+    });
+}
+
+// (dy, x, wt, adapters, ids, h, dx_dtype), with dx
+PyObject *adapters_bwd(PyObject *, PyObject *const *a, Py_ssize_t count)
+{
+    ARGS(7)
+    return guarded([&]() -> PyObject * {
+        Given wt;
+        Rows dy, x;
+        Given8 q;
+        Low low;
+        const int *ids;
+        const at::Tensor *h;
+        at::ScalarType t;
+        const bool kept = PyTuple_Check(a[1]);
+        if (!dy.of(a[0]) || !(kept ? q.of(a[1]) : x.of(a[1])) || !wt.of(a[2]) || wt.cols != dy.cols)
+            Py_RETURN_NONE;
+        const int M = (int)dy.rows, N = dy.cols, K = kept ? q.cols : x.cols;
+        const auto lead = dy.t->sizes().slice(0, dy.t->dim() - 1);
+        if ((kept ? q.rows != M : x.t->sizes().slice(0, x.t->dim() - 1) != lead) || wt.rows != K
+            || !low.of(a[3], N, K) || !ids_of(a[4], lead, ids) || !tensor_of(a[5], h) || h->scalar_type() != at::kFloat
+            || !h->is_contiguous() || !type_of(a[6], dy.t->scalar_type(), t))
+            Py_RETURN_NONE;
+        c10::SmallVector<int64_t, 8> sizes(dy.t->sizes().begin(), dy.t->sizes().end());
+        sizes.back() = low.rank;
+        if (h->sizes() != at::IntArrayRef(sizes))
+            Py_RETURN_NONE;
+        size_t need = 0;
+        if (p_mxfp4_linear_adapters_bwd_workspace(M, N, K, low.number, low.rank, &need) != CONVIMG_OK)
+            Py_RETURN_NONE;
+        sizes.back() = K;
+        const at::Tensor dx = fresh(sizes, t, *dy.t), ddown = fresh({low.number, low.rank, K}, at::kFloat, dx),
+                         dup = fresh({low.number, low.rank, N}, at::kFloat, dx),
+                         ws = fresh({(int64_t)need}, at::kByte, dx);
+        const hipStream_t s = stream_of(dx);
+        return result(unlocked([&] {
+                          return p_mxfp4_linear_adapters_bwd(
+                              dy.p, dy.ld, dy.type, kept ? q.codes->data_ptr() : x.p, kept ? K : x.ld,
+                              kept ? q.scales->data_ptr() : nullptr, kept ? CONVIMG_MXINT8 : x.type,
+                              wt.codes->data_ptr(), wt.scales->data_ptr(), low.down->data_ptr(), low.up->data_ptr(),
+                              low.scale, ids, low.number, low.rank, low.type, h->data_ptr<float>(), M, N, K,
+                              type_code(t), dx.data_ptr(), ddown.data_ptr<float>(), dup.data_ptr<float>(),
+                              ws.data_ptr(), need, s);
+                      }),
+                      dx, ddown, dup);
     });
 }
 
@@ -431,6 +731,15 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t count)
     BIND(mxfp4_linear_workspace)
     BIND(mxfp4_linear_bwd)
     BIND(mxfp4_linear_bwd_workspace)
+    BIND(mxint8_quantize)
+    BIND(mxint8_dequantize)
+    BIND(layer_norm_fwd_mxint8)
+    BIND(layer_norm_bwd_mxint8)
+    BIND(mxfp4_linear_bwd_mxint8)
+    BIND(mxfp4_linear_adapters_fwd)
+    BIND(mxfp4_linear_adapters_workspace)
+    BIND(mxfp4_linear_adapters_bwd)
+    BIND(mxfp4_linear_adapters_bwd_workspace)
     PyErr_SetString(PyExc_KeyError, name);
     return nullptr;
 }
@@ -449,6 +758,12 @@ PyMethodDef methods[] = {method("bind", bind),
                          method("dequantize", dequantize),
                          method("linear", linear),
                          method("linear_bwd", linear_bwd),
+                         method("quantize8", quantize8),
+                         method("dequantize8", dequantize8),
+                         method("layer_norm_kept", layer_norm_kept),
+                         method("layer_norm_kept_bwd", layer_norm_kept_bwd),
+                         method("adapters", adapters),
+                         method("adapters_bwd", adapters_bwd),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_rows", "The row operators' calls in their common case.", -1, methods,

@@ -37,6 +37,7 @@ extern "C" {
 /* Further types, taken by the row operators (layer norm, MXFP4) only. */
 #define CONVIMG_FP16 2   /* IEEE half */
 #define CONVIMG_MXFP4 3  /* packed 4-bit rows with a scale per 32 values (see mxfp4_quantize) */
+#define CONVIMG_MXINT8 4 /* 8-bit rows with a unit per 32 values (see mxint8_quantize) */
 
 /* Status codes.  0 is success; every error is returned before any work is
  * queued, and then `out` is untouched, except CONVIMG_ERR_LAUNCH. */
@@ -399,7 +400,8 @@ int conv2d_bwd_weight_workspace(int N, int H, int W, int IC, int OC, int KH, int
 
 /* ---- Row operators ------------------------------------------------------
  *
- * Layer normalisation over channels and a linear layer on 4-bit rows, for
+ * Layer normalisation over channels, a linear layer on 4-bit rows, low-rank
+ * adapters beside it and activations kept in 8 bits, for
  * channels-last data: a row is one pixel of an NHWC map or one token, its
  * `cols` columns are the channels.  A dense operand is `rows` rows whose
  * first elements are ld >= cols elements apart (a view into a wider buffer
@@ -451,6 +453,44 @@ int layer_norm_bwd(const void *dy, long long lddy, const void *x, long long ldx,
                    int dx_dtype, void *dx, float *dgamma, float *dbeta, void *ws, size_t ws_bytes,
                    hipStream_t stream);
 int layer_norm_bwd_workspace(long long rows, int cols, size_t *bytes);
+
+/* Activations kept in 8 bits for the backward pass (MXINT8 rows).  A block
+ * is 32 consecutive values of a row (the last one filled with zeros).  Its unit
+ * is u = 2^(s - 127), s the smallest whole number of at least 1 for which 127 u
+ * reaches the block's largest magnitude; a value is stored as value / u rounded
+ * to the nearest whole number, ties to even, so it is off by at most u / 2 and
+ * none saturates.  The values code * u are exact in bf16.  A block that holds
+ * an infinity or a NaN gets the byte 255 and stands for NaN throughout.  Layout,
+ * with kp = cols rounded up to 32:
+ *
+ *   codes   [rows][kp] signed bytes; 16-byte aligned
+ *   scales  [rows][4 * ceil(kp / 128)] bytes s, 0 for blocks past the last;
+ *           4-byte aligned
+ *
+ * mxint8_bytes reports the two sizes.  (Packed codes may exceed 2 GiB here.) */
+int mxint8_bytes(long long rows, int cols, size_t *codes, size_t *scales);
+int mxint8_quantize(const void *x, long long ldx, long long rows, int cols, int dtype, void *codes, void *scales,
+                    hipStream_t stream);
+
+/* out [rows][cols] = the values that 8-bit rows stand for. */
+int mxint8_dequantize(const void *codes, const void *scales, long long rows, int cols, int dtype, void *out,
+                      hipStream_t stream);
+
+/* layer_norm_fwd that also keeps n = (x - mean) * rstd in 8 bits, in place of
+ * x and the mean, for layer_norm_bwd_mxint8.  y is computed from n before that
+ * rounding.
+ *
+ *   codes, scales  device, MXINT8 rows of n
+ *   rstd           device, fp32 [rows] */
+int layer_norm_fwd_mxint8(const void *x, long long ldx, const float *gamma, const float *beta, long long rows,
+                          int cols, float eps, int x_dtype, int y_dtype, void *y, void *codes, void *scales,
+                          float *rstd, hipStream_t stream);
+
+/* layer_norm_bwd from what layer_norm_fwd_mxint8 kept: its formulas with the
+ * values of the 8-bit rows as n.  ws: layer_norm_bwd_workspace bytes. */
+int layer_norm_bwd_mxint8(const void *dy, long long lddy, const void *codes, const void *scales, const float *gamma,
+                          const float *rstd, long long rows, int cols, int dy_dtype, int dx_dtype, void *dx,
+                          float *dgamma, float *dbeta, void *ws, size_t ws_bytes, hipStream_t stream);
 
 /* MXFP4 rows.  A block is 32 consecutive values of a row (the last one
  * filled with zeros).  With t its largest magnitude its scale byte is
@@ -516,6 +556,68 @@ int mxfp4_linear_bwd(const void *dy, long long lddy, int dy_dtype, const void *x
                      long long ldw, int dtype, int M, int N, int K, int dx_dtype, void *dx, float *dw, float *db,
                      void *ws, size_t ws_bytes, hipStream_t stream);
 int mxfp4_linear_bwd_workspace(int M, int N, int K, size_t *bytes);
+
+/* mxfp4_linear_bwd with x kept in 8 bits (MXINT8 rows, M of K columns): x's
+ * part of dw is quantised from the values that they stand for.  w in w_dtype;
+ * ws: mxfp4_linear_bwd_workspace bytes. */
+int mxfp4_linear_bwd_mxint8(const void *dy, long long lddy, int dy_dtype, const void *x_codes, const void *x_scales,
+                            const void *w, long long ldw, int w_dtype, int M, int N, int K, int dx_dtype, void *dx,
+                            float *dw, float *db, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* Low-rank adapters of many requests beside the linear layer.  Row m belongs
+ * to adapter g = ids[m]; any number outside 0 .. adapters-1 means none, and the
+ * rows of an adapter may lie anywhere.  With
+ *
+ *   h[m] = down_g x[m]      (rank values, fp32; 0 for a row without adapter)
+ *   out[m][n] = sum_k Q(x)[m][k] * w[n][k] + bias[n] + scale_g * sum_i h[m][i] * up_g[i][n]
+ *
+ * where the adapter's part is taken from x itself, not from Q(x), and added
+ * before the one rounding to out_dtype.  A row depends on its own adapter only:
+ * an infinity or a NaN in another one or in another row does not reach it.
+ *
+ *   x, w_codes, w_scales, bias, out   as for mxfp4_linear_fwd, x dense
+ *   down      device, [adapters][rank][K] in a_dtype
+ *   up        device, [adapters][rank][N] in a_dtype
+ *   scale     device, fp32 [adapters]
+ *   ids       device, int [M]
+ *   h         device, fp32 [M][rank], kept for the backward call, or NULL
+ *   x_codes, x_scales   device, MXINT8 rows of x, kept for the backward
+ *             call, written in the pass that reads x; NULL together for none
+ *   ws        at least mxfp4_linear_adapters_workspace bytes
+ *
+ * rank (1 .. 4096) and a_dtype are those of all adapters; one of a lower rank
+ * is filled up with zeros.  down and up of any size (64-bit offsets). */
+int mxfp4_linear_adapters_fwd(const void *x, long long ldx, int x_dtype, const void *w_codes, const void *w_scales,
+                              const float *bias, const void *down, const void *up, const float *scale, const int *ids,
+                              int adapters, int rank, int a_dtype, int M, int N, int K, int out_dtype, void *out,
+                              float *h, void *x_codes, void *x_scales, void *ws, size_t ws_bytes, hipStream_t stream);
+int mxfp4_linear_adapters_workspace(int M, int N, int K, int rank, int x_dtype, size_t *bytes);
+
+/* Gradients of mxfp4_linear_adapters_fwd with the shared weights and the bias
+ * frozen.  With t[m] = up_g dy[m]:
+ *
+ *   dx[m][k]       = sum_n Q(dy)[m][n] * wt[k][n] + scale_g * sum_i t[m][i] * down_g[i][k]
+ *   ddown[g][i][k] = scale_g * sum over the rows m of g of t[m][i] * x[m][k]
+ *   dup[g][i][n]   = scale_g * sum over the rows m of g of h[m][i] * dy[m][n]
+ *
+ * (0 for an adapter without rows).
+ *
+ *   dy        device, [M][N] in dy_dtype, rows lddy apart
+ *   x         the forward input: dense [M][K] in x_dtype, rows ldx apart, or
+ *             (CONVIMG_MXINT8) its kept codes, with x_scales
+ *   wt_codes, wt_scales   the transpose of the shared weights quantised along
+ *             n: packed MXFP4, K rows of N columns (mxfp4_quantize of w [N][K]
+ *             with transpose).  NULL together with dx to skip dx
+ *   h         device, fp32 [M][rank]: what the forward call wrote
+ *   dx        device, [M][K] in dx_dtype
+ *   ddown, dup  device, fp32, [adapters][rank][K] and [adapters][rank][N]
+ *   ws        at least mxfp4_linear_adapters_bwd_workspace bytes */
+int mxfp4_linear_adapters_bwd(const void *dy, long long lddy, int dy_dtype, const void *x, long long ldx,
+                              const void *x_scales, int x_dtype, const void *wt_codes, const void *wt_scales,
+                              const void *down, const void *up, const float *scale, const int *ids, int adapters,
+                              int rank, int a_dtype, const float *h, int M, int N, int K, int dx_dtype, void *dx,
+                              float *ddown, float *dup, void *ws, size_t ws_bytes, hipStream_t stream);
+int mxfp4_linear_adapters_bwd_workspace(int M, int N, int K, int adapters, int rank, size_t *bytes);
 
 /* Free every library-owned buffer (synchronising each device that has
  * one).  Later calls allocate again as needed.  Library plumbing with no
