@@ -151,7 +151,7 @@ def load(path: str = LIB_PATH):
             ("mxfp4_linear_bwd_mxint8", [vp, ll, i, vp, vp, vp, ll, i, i, i, i, i, vp, vp, vp, vp, sz, vp]),
             ("mxfp4_linear_adapters_fwd", [vp, ll, i, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, vp, vp, vp, vp,
                                            vp, sz, vp]),
-            ("mxfp4_linear_adapters_workspace", [i, i, i, i, i, szp]),
+            ("mxfp4_linear_adapters_workspace", [i, i, i, i, i, i, szp]),
             ("mxfp4_linear_adapters_bwd", [vp, ll, i, vp, ll, vp, i, vp, vp, vp, vp, vp, vp, i, i, i, vp, i, i, i, i,
                                            vp, vp, vp, vp, sz, vp]),
             ("mxfp4_linear_adapters_bwd_workspace", [i, i, i, i, i, szp])):
@@ -388,10 +388,10 @@ def mxfp4_linear_adapters_fwd(x, ldx, x_dtype, w_codes, w_scales, bias, down, up
                                             stream)
 
 
-def mxfp4_linear_adapters_workspace(M, N, K, rank, x_dtype):
+def mxfp4_linear_adapters_workspace(M, N, K, adapters, rank, x_dtype):
     """Returns (status, workspace bytes of mxfp4_linear_adapters_fwd)."""
     b = ctypes.c_size_t(0)
-    rc = load().mxfp4_linear_adapters_workspace(M, N, K, rank, x_dtype, ctypes.byref(b))
+    rc = load().mxfp4_linear_adapters_workspace(M, N, K, adapters, rank, x_dtype, ctypes.byref(b))
     return rc, b.value
 
 

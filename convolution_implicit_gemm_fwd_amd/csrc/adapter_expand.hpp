@@ -85,101 +85,191 @@ struct MxNoAdapters {};
 
 struct MxAdapterArgs {
     const float *h;        // [splits][M][r], to be summed over the splits
-    const void *up;        // [G][r][N] in `dtype`
+    const void *up;        // [G][r][N]
     const float *scale;    // [G]
-    const int *ids;        // [M]
+    const int *ids;        // [rows]
+    const int *order;      // [M]: the row at each place of h and of the product, or NULL for their own order
     int G, r, splits, dtype;
+
+    __device__ __forceinline__ int row(int m) const { return order ? order[m] : m; }
 };
 
-// h of a row from rank i0 on, eight values times s, zeros past the rank.
-__device__ __forceinline__ void adapter_h8(const MxAdapterArgs &a, int M, int m, int i0, float s, float (&v)[8])
+// The same with up's type known when compiled.
+template <typename T>
+struct MxAdapters : MxAdapterArgs {
+    typedef T type;
+};
+
+// Eight ranks of a row from i0 on, the parts' sums, zeros past the rank.
+// (Loads are unconditional, at clamped places: a branch around each would make
+// the wave wait for them one by one.)
+__device__ __forceinline__ void adapter_h8(const MxAdapterArgs &a, int M, int m, int i0, float (&v)[8])
 {
+    const float *p = a.h + (long long)m * a.r;
 #pragma unroll
     for (int e = 0; e < 8; ++e)
         v[e] = 0.f;
-    for (int k = 0; k < a.splits; ++k) {
-        const float *p = a.h + ((long long)k * M + m) * a.r;
+    for (int k = 0; k < a.splits; ++k, p += (long long)M * a.r) {
+        float u[8];
+        if (a.r >= 8) {
+            unpack8<Fp32>(load_raw8<Fp32, false>(p, i0, a.r), u);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                u[e] = p[min(i0 + e, a.r - 1)];
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            if (i0 + e < a.r)
-                v[e] += p[i0 + e];
+            v[e] += u[e];
     }
+    if (a.r >= 8) {
+        Raw8<Fp32> w;
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        v[e] *= s;
+        for (int e = 0; e < 8; ++e)
+            w.w[e / 4][e % 4] = __float_as_uint(v[e]);
+        unpack8<Fp32>(tail8<Fp32, false>(w, i0, a.r), v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = i0 + e < a.r ? v[e] : 0.f;
+    }
 }
 
-// The sums of FM x FN blocks of 32 x 32 from row m0 and column n0 on; a lane
-// holds row lane % 32 of a block and 16 of its columns (the instruction's rows).
+// Adds to the sums of FM x FN blocks of 32 x 32 from row m0 and column n0 on; a
+// lane holds row lane % 32 of a block and 16 of its columns (the instruction's
+// rows).
 //
-// The wave goes through the adapters that its rows have, in the order of their
-// first rows, so the tile costs one round of small loads and 3 FN FM matrix
-// instructions a 16 ranks and adapter.  A row takes only its own adapter's
-// product (selected after the product: a zero times another adapter's infinity
-// would not do).
-template <int FM, int FN>
-__device__ __forceinline__ void adapter_expand(const MxAdapterArgs &a, int M, int N, int m0, int n0,
+// For 16 ranks at a time the wave goes through the adapters that its rows have,
+// in the order of their first rows, P of them in flight at once; of KG groups
+// of waves that share the tile each takes every KG-th.  A row has zeros for h
+// in another adapter's product.  Zero times an infinity would not do: such
+// values of up are left out (0) here, and the answer says that there are some,
+// for adapter_infinite.  (Selecting by row after the product instead takes the
+// sums from the matrix unit's registers: the largest tile then spills.)
+template <typename T, int FM, int FN, int KG>
+__device__ __forceinline__ bool adapter_expand(const MxAdapterArgs &a, int M, int N, int m0, int n0, int group,
                                                f32x16_t (&acc)[FM][FN])
 {
+    constexpr int P = FM * FN <= 1 ? 8 : FM * FN <= 2 ? 4 : FM * FN <= 4 ? 2 : 1;
     const int lane = threadIdx.x & 63, half = lane >> 5, l32 = lane & 31;
     int id[FM];
-    unsigned left[FM];
+    float s[FM];
+    unsigned any[FM];
+    bool infinite = false;
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+        id[i] = a.ids[a.row(min(m0 + i * 32 + l32, M - 1))];
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-        const int m = m0 + i * 32 + l32;
-        id[i] = m < M ? a.ids[m] : -1;
-        left[i] = (unsigned)__ballot(id[i] >= 0 && id[i] < a.G);
+        id[i] = m0 + i * 32 + l32 < M && id[i] < a.G ? id[i] : -1;
+        s[i] = a.scale[max(id[i], 0)];
+        any[i] = (unsigned)__ballot(id[i] >= 0);
     }
-    for (;;) {
-        int g = -1;
+    // (one pass through each loop at least, without a branch around: the sums stay where they are)
+    int r0 = 0, turn = group;
+    do {
+        const int i0 = r0 + half * 8;
+        u32v4_t h[FM][3];
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+            float v[8];
+            adapter_h8(a, M, min(m0 + i * 32 + l32, M - 1), i0, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] *= s[i];
+            split8(v, h[i]);
+        }
+        unsigned left[FM], rest;
 #pragma unroll
         for (int i = 0; i < FM; ++i)
-            if (g < 0 && left[i])
-                g = __builtin_amdgcn_readlane(id[i], __builtin_ctz(left[i]));
-        if (g < 0)
-            return;
+            left[i] = any[i];
+        int number = 0;      // of the adapter among the tile's
+        do {
+            int g[P];
+            typename T::raw w[P][FN][8];
 #pragma unroll
-        for (int i = 0; i < FM; ++i)
-            left[i] &= ~(unsigned)__ballot(id[i] == g);
-        const float s = a.scale[g];
-        for (int r0 = 0; r0 < a.r; r0 += 16) {
-            const int i0 = r0 + half * 8;
-            u32v4_t h[FM][3];
+            for (int p = 0; p < P; ++p) {
+                for (;;) {
+                    g[p] = -2;
 #pragma unroll
-            for (int i = 0; i < FM; ++i) {
-                float v[8] = {};
-                if (id[i] == g)
-                    adapter_h8(a, M, m0 + i * 32 + l32, i0, s, v);
-                split8(v, h[i]);
-            }
-            auto columns = [&](auto type) {
-                typedef decltype(type) T;
-                const typename T::raw *up = (const typename T::raw *)a.up + ((long long)g * a.r + i0) * N;
+                    for (int i = 0; i < FM; ++i)
+                        if (g[p] < 0 && left[i])
+                            g[p] = __builtin_amdgcn_readlane(id[i], __builtin_ctz(left[i]));
 #pragma unroll
-                for (int j = 0; j < FN; ++j) {
-                    const int n = n0 + j * 32 + l32;
-                    float u[8];
+                    for (int i = 0; i < FM; ++i)
+                        left[i] &= ~(unsigned)__ballot(id[i] == g[p]);
+                    if (KG == 1 || g[p] < 0 || (number++ + turn) % KG == 0)
+                        break;
+                }
+                const typename T::raw *up = (const typename T::raw *)a.up + (long long)max(g[p], 0) * a.r * N;
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        u[e] = n < N && i0 + e < a.r ? load1<T>(up + (long long)e * N + n) : 0.f;
+                        w[p][j][e] = up[(long long)min(i0 + e, a.r - 1) * N + min(n0 + j * 32 + l32, N - 1)];
+            }
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                u32v4_t hm[FM][3];
+#pragma unroll
+                for (int i = 0; i < FM; ++i)
+#pragma unroll
+                    for (int k = 0; k < 3; ++k)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            hm[i][k][e] = id[i] == g[p] ? h[i][k][e] : 0u;
+#pragma unroll
+                for (int j = 0; j < FN; ++j) {
+                    float u[8];
+                    bool odd = false;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        u[e] = i0 + e < a.r ? load1<T>(&w[p][j][e]) : 0.f;
+                        const bool fine = __builtin_fabsf(u[e]) < __builtin_inff();
+                        odd |= !fine;
+                        u[e] = fine ? u[e] : 0.f;
+                    }
+                    infinite |= __any(odd);
                     u32v4_t b[split_terms<T>()];
                     split8(u, b);
 #pragma unroll
-                    for (int i = 0; i < FM; ++i) {
-                        const f32x16_t t = mfma_terms32(b, h[i], acc[i][j]);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            acc[i][j][e] = id[i] == g ? t[e] : acc[i][j][e];
-                    }
+                    for (int i = 0; i < FM; ++i)
+                        acc[i][j] = mfma_terms32(b, hm[i], acc[i][j]);
                 }
-            };
-            if (a.dtype == CONVIMG_BF16)
-                columns(Bf16{});
-            else if (a.dtype == CONVIMG_FP16)
-                columns(Fp16{});
-            else
-                columns(Fp32{});
+            }
+            rest = 0;
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+                rest |= left[i];
+        } while (rest);
+        r0 += 16;
+        ++turn;
+    } while (r0 < a.r);
+    return infinite;
+}
+
+// The outputs that an infinity or a NaN in up reaches, over what was stored for
+// them: TM x TN of them from row m0 and column n0 on, by one wave.
+template <typename T, typename O>
+__device__ __forceinline__ void adapter_infinite(const MxAdapterArgs &a, int M, int N, int m0, int n0, int TM, int TN,
+                                                 void *out)
+{
+    for (int k = threadIdx.x & 63; k < TM * TN; k += 64) {
+        const int m = m0 + k / TN, n = n0 + k % TN, row = a.row(min(m, M - 1)), id = m < M && n < N ? a.ids[row] : -1;
+        if (id < 0 || id >= a.G)
+            continue;
+        float s = 0.f;
+        for (int i = 0; i < a.r; ++i) {
+            const float u = load1<T>((const typename T::raw *)a.up + ((long long)id * a.r + i) * N + n);
+            if (!(__builtin_fabsf(u) < __builtin_inff())) {
+                float h = 0.f;
+                for (int p = 0; p < a.splits; ++p)
+                    h += a.h[((long long)p * M + m) * a.r + i];
+                s += h * a.scale[id] * u;
+            }
         }
+        if (!(__builtin_fabsf(s) < __builtin_inff()))
+            store1<O>((typename O::raw *)out + (long long)row * N + n, s);
     }
 }
 

@@ -63,75 +63,58 @@ constexpr int grad_terms()
         return split_terms<V>();
 }
 
-// A workgroup takes 128 columns, 16 RT ranks of one adapter and one part of
-// the rows.  Each of its four waves walks the part's ids and lists the
-// adapter's rows, of which it takes every fourth run of 32: lane l loads eight
-// columns (l % 16) of eight rows (l / 16) and turns them over in registers to
-// the matrix instruction's operand, eight consecutive rows of one column.
-// Rows of other adapters are not loaded.
-constexpr int kAdGradCols = 128, kAdGradWaves = 4, kAdGradRows = 2048;      // rows listed at once
+// A workgroup takes 128 columns, 16 RT ranks and one chunk of the sorted rows,
+// adapter by adapter; of an adapter's rows each of the four waves takes every
+// fourth run of 32: lane l loads eight columns (l % 16) of eight rows (l / 16)
+// and turns them over in registers to the matrix instruction's operand, eight
+// consecutive rows of one column.
+//
+// An adapter whose rows lie in one chunk is finished there; one that goes on
+// leaves its sum in the chunk's first slot if it begins with the chunk, else in
+// the second.
+constexpr int kAdGradCols = 128, kAdGradWaves = 4;
 
 template <typename V, int RT>
-__global__ __launch_bounds__(kAdGradWaves * 64) void ad_grad(AdGradArgs a, int splits, int tiles, int chunks,
-                                                             long long first, long long end)
+__global__ __launch_bounds__(kAdGradWaves * 64) void ad_grad(AdGradArgs a, int tiles, int ranks)
 {
-    __shared__ __attribute__((aligned(16))) int list[kAdGradWaves][kAdGradRows / kAdGradWaves + 32];
     __shared__ f32x4_t sums[kAdGradWaves - 1][8][64];
     constexpr int NV = grad_terms<V>();
-    long long b = first + blockIdx.x;
-    if (b >= end)
-        return;
+    unsigned b = blockIdx.x;
     const int tile = (int)(b % tiles);
     b /= tiles;
-    const int chunk = (int)(b % chunks);
-    b /= chunks;
-    const int g = (int)(b % a.G), split = (int)(b / a.G);
+    const int i0 = (int)(b % ranks) * 16 * RT, chunk = (int)(b / ranks);
     const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int c = tile * kAdGradCols + r16 * 8, i0 = chunk * 16 * RT;
-    const int per = (int)((a.M + (long long)splits - 1) / splits), lo = min((long long)a.M, (long long)split * per),
-              hi = min((long long)a.M, (long long)lo + per);
-    int *mine = list[wave];
-    f32x4_t acc[RT][8] = {};
-    int total = 0;
+    const int c = tile * kAdGradCols + r16 * 8;
+    const int lo = chunk * a.per, hi = min(a.start[a.G], lo + a.per);
 
-    for (int s0 = lo; s0 < hi; s0 += kAdGradRows) {
-        const int s1 = min(hi, s0 + kAdGradRows);
-        int n = 0;      // the adapter's rows so far
-        for (int m = s0; m < s1; m += 64) {
-            const bool is = m + lane < s1 && a.ids[m + lane] == g;
-            const unsigned long long all = __ballot(is);
-            if (is) {
-                const int p = n + __builtin_amdgcn_mbcnt_hi((unsigned)(all >> 32), __builtin_amdgcn_mbcnt_lo((unsigned)all, 0));
-                if (((p >> 5) & (kAdGradWaves - 1)) == wave)
-                    mine[(p >> 7) * 32 + (p & 31)] = m + lane;
-            }
-            n += __builtin_popcountll(all);
-        }
-        total += n;
-        mx_wait_lds();      // (the list is the wave's own)
-        __builtin_amdgcn_wave_barrier();
-        for (int run = wave; run * 32 < n; run += kAdGradWaves) {
-            const int slot = (run >> 2) * 32 + q * 8, have = n - run * 32 - q * 8;      // of the lane's eight
-            int row[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                row[e] = e < have ? mine[slot + e] : -1;
-            Grad8<V> v[8];
+    for (int s0 = lo, s1; s0 < hi; s0 = s1) {
+        const int g = a.ids[a.order[s0]], g0 = a.start[g], g1 = a.start[g + 1];
+        s1 = min(hi, g1);
+        f32x4_t acc[RT][8] = {};
+        for (int p0 = s0 + wave * 32; p0 < s1; p0 += kAdGradWaves * 32) {
+            int at[8], row[8];      // the lane's eight places and rows
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                v[e] = {};
-                if (row[e] >= 0)
-                    v[e].load(a, row[e], c);
+                at[e] = min(p0 + q * 8 + e, s1 - 1);
+                row[e] = a.order[at[e]];
             }
+            const int have = s1 - p0 - q * 8;
+            Grad8<V> v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e].load(a, row[e], c);
             u32v4_t uf[RT][3];
 #pragma unroll
             for (int t = 0; t < RT; ++t) {
-                const int i = i0 + t * 16 + r16;
+                const int i = min(i0 + t * 16 + r16, a.r - 1);
                 float u[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    u[e] = row[e] >= 0 && i < a.r ? a.u[(long long)row[e] * a.r + i] : 0.f;
+                    u[e] = a.u[(long long)(a.u_sorted ? at[e] : row[e]) * a.r + i];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    u[e] = e < have ? u[e] : 0.f;
                 split8(u, uf[t]);
             }
 #pragma unroll
@@ -139,7 +122,7 @@ __global__ __launch_bounds__(kAdGradWaves * 64) void ad_grad(AdGradArgs a, int s
                 float w[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    w[e] = v[e].get(j);
+                    w[e] = e < have ? v[e].get(j) : 0.f;
                 u32v4_t vf[NV];
                 split8(w, vf);
 #pragma unroll
@@ -147,82 +130,82 @@ __global__ __launch_bounds__(kAdGradWaves * 64) void ad_grad(AdGradArgs a, int s
                     acc[t][j] = mfma_terms16(uf[t], vf, acc[t][j]);
             }
         }
-        __builtin_amdgcn_wave_barrier();
-    }
-
-    // the waves' sums in order; a lane holds ranks 4 q .. 4 q + 3 of its eight columns
-    if (splits > 1) {
-        if (tile == 0 && chunk == 0 && threadIdx.x == 0)
-            a.count[(long long)split * a.G + g] = total;
-        if (total == 0)
-            return;
-    }
-    const float s = a.scale[g];
-    float *out = (splits > 1 ? a.part + (long long)split * a.G * a.r * a.C : a.out) + (long long)g * a.r * a.C;
+        // the waves' sums in order; a lane holds ranks 4 q .. 4 q + 3 of its eight columns
+        const bool whole = s0 == g0 && s1 == g1, several = s1 - s0 > 32;
+        const float s = a.scale[g];
+        float *out = whole ? a.out + (long long)g * a.r * a.C
+                           : a.part + ((long long)chunk * 2 + (s0 == lo ? 0 : 1)) * a.r * a.C;
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-        __syncthreads();
-        if (wave > 0)
+        for (int t = 0; t < RT; ++t) {
+            if (several) {
+                __syncthreads();
+                if (wave > 0)
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                sums[wave - 1][j][lane] = acc[t][j];
-        __syncthreads();
-        if (wave > 0)
-            continue;
+                    for (int j = 0; j < 8; ++j)
+                        sums[wave - 1][j][lane] = acc[t][j];
+                __syncthreads();
+            }
+            if (wave > 0)
+                continue;
+            if (several)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+                for (int j = 0; j < 8; ++j)
 #pragma unroll
-            for (int w = 0; w < kAdGradWaves - 1; ++w)
-                acc[t][j] += sums[w][j][lane];
+                    for (int w = 0; w < kAdGradWaves - 1; ++w)
+                        acc[t][j] += sums[w][j][lane];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int i = i0 + t * 16 + q * 4 + e;
-            float o[8];
+            for (int e = 0; e < 4; ++e) {
+                const int i = i0 + t * 16 + q * 4 + e;
+                float o[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                o[j] = total > 0 ? acc[t][j][e] * s : 0.f;
-            if (i < a.r && c < a.C)
-                store8<Fp32>(out + (long long)i * a.C, c, a.C, o);
+                for (int j = 0; j < 8; ++j)
+                    o[j] = acc[t][j][e] * s;
+                if (i < a.r && c < a.C)
+                    store8<Fp32>(out + (long long)i * a.C, c, a.C, o);
+            }
         }
     }
 }
 
-// The parts' sums in order, without the parts in which the adapter has no rows.
-__global__ __launch_bounds__(256) void ad_grad_sum(AdGradArgs a, int splits)
+// The sums of the adapters whose rows lie in several chunks, in order, and
+// zeros for those without rows.
+__global__ __launch_bounds__(256) void ad_grad_sum(AdGradArgs a)
 {
-    const long long per = (long long)a.r * a.C, all = per * a.G;
-    for (long long p = (long long)blockIdx.x * 256 + threadIdx.x; p < all; p += (long long)gridDim.x * 256) {
-        const int g = (int)(p / per);
-        float s = 0.f;
-        for (int k = 0; k < splits; ++k)
-            if (a.count[(long long)k * a.G + g] > 0)
-                s += a.part[k * all + p];
-        a.out[p] = s;
+    const long long per = (long long)a.r * a.C;
+    for (int g = blockIdx.y; g < a.G; g += gridDim.y) {
+        const int g0 = a.start[g], g1 = a.start[g + 1];
+        const int first = g0 / a.per, last = (g1 - 1) / a.per;
+        if (g0 < g1 && first == last)
+            continue;
+        for (long long p = (long long)blockIdx.x * 256 + threadIdx.x; p < per; p += (long long)gridDim.x * 256) {
+            float s = 0.f;
+            if (g0 < g1) {
+                s = a.part[(first * 2LL + (g0 == first * a.per ? 0 : 1)) * per + p];
+                for (int k = first + 1; k <= last; ++k)
+                    s += a.part[k * 2LL * per + p];
+            }
+            a.out[g * per + p] = s;
+        }
     }
 }
 
 int grad_ranks(int r) { return r <= 16 ? 1 : r <= 32 ? 2 : 4; }
 
-int adapter_grad_splits(int M, int C, int G, int r)
+// Sorted rows a chunk: as many chunks as give about 1024 workgroups, runs of 32.
+int adapter_grad_per(int M, int C, int r)
 {
-    const long long rt = 16 * grad_ranks(r), blocks = (C + kAdGradCols - 1LL) / kAdGradCols * G * ((r + rt - 1) / rt);
-    const long long want = (2047 + blocks) / blocks, most = (M + 511LL) / 512;
-    const long long n = want < most ? want : most;
-    return n < 1 ? 1 : n > 64 ? 64 : (int)n;
+    const long long rt = 16 * grad_ranks(r), tiles = (C + kAdGradCols - 1LL) / kAdGradCols * ((r + rt - 1) / rt);
+    const long long chunks = tiles < 1024 ? 1024 / tiles : 1, per = (M + chunks - 1) / chunks;
+    return (int)((per + 31) / 32 * 32 < 32 ? 32 : (per + 31) / 32 * 32);
 }
 
-void adapter_grad(const AdGradArgs &a, int v_dtype, int splits, hipStream_t stream)
+void adapter_grad(const AdGradArgs &a, int v_dtype, hipStream_t stream)
 {
     auto launch = [&](auto v, auto rt) {
         constexpr int RT = decltype(rt)::value;
-        const int tiles = (int)((a.C + kAdGradCols - 1LL) / kAdGradCols), chunks = (a.r + 16 * RT - 1) / (16 * RT);
-        const long long blocks = (long long)tiles * chunks * a.G * splits;
-        constexpr long long kStep = 1 << 22;      // (a launch holds fewer than 2^32 threads)
-        for (long long first = 0; first < blocks; first += kStep) {
-            const long long n = blocks - first < kStep ? blocks - first : kStep;
-            hipLaunchKernelGGL((ad_grad<decltype(v), RT>), dim3((unsigned)n), dim3(kAdGradWaves * 64), 0, stream, a, splits,
-                               tiles, chunks, first, blocks);
-        }
+        const unsigned tiles = (unsigned)((a.C + kAdGradCols - 1LL) / kAdGradCols), ranks = (a.r + 16 * RT - 1) / (16 * RT);
+        hipLaunchKernelGGL((ad_grad<decltype(v), RT>), dim3(tiles * ranks * a.chunks), dim3(kAdGradWaves * 64), 0, stream, a,
+                           (int)tiles, (int)ranks);
     };
     auto ranks = [&](auto v) {
         switch (grad_ranks(a.r)) {
@@ -235,10 +218,9 @@ void adapter_grad(const AdGradArgs &a, int v_dtype, int splits, hipStream_t stre
         ranks(Kept{});
     else
         with_dtype(v_dtype, ranks);
-    if (splits > 1) {
-        const long long n = ((long long)a.G * a.r * a.C + 255) / 256;
-        hipLaunchKernelGGL(ad_grad_sum, dim3((unsigned)(n < (1 << 20) ? n : (1 << 20))), dim3(256), 0, stream, a, splits);
-    }
+    const long long n = ((long long)a.r * a.C + 255) / 256;
+    hipLaunchKernelGGL(ad_grad_sum, dim3((unsigned)(n < 256 ? n : 256), (unsigned)(a.G < 4096 ? a.G : 4096)), dim3(256), 0,
+                       stream, a);
 }
 
 }  // namespace convimg

@@ -1,0 +1,16 @@
+// adapter_products_fp16.hip -- adapter_products.hpp for adapters in fp16.
+#include "adapter_products.hpp"
+
+namespace convimg {
+
+void gemm_adapters_fp16(const MxGemmArgs &g, const MxAdapterArgs &ad, int out_dtype, hipStream_t stream)
+{
+    gemm_adapters_of<Fp16>(g, ad, out_dtype, stream);
+}
+
+void few_adapters_fp16(const MxFewArgs &g, const MxAdapterArgs &ad, int x_dtype, int out_dtype, hipStream_t stream)
+{
+    few_adapters_of<Fp16>(g, ad, x_dtype, out_dtype, stream);
+}
+
+}  // namespace convimg

@@ -11,48 +11,68 @@
 
 namespace convimg {
 
-void gemm_adapters(MxGemmArgs g, const MxAdapterArgs &ad, int out_dtype, hipStream_t stream)
+// adapter_products_*.hip
+void gemm_adapters_bf16(const MxGemmArgs &g, const MxAdapterArgs &ad, int out_dtype, hipStream_t stream);
+void few_adapters_bf16(const MxFewArgs &g, const MxAdapterArgs &ad, int x_dtype, int out_dtype, hipStream_t stream);
+void gemm_adapters_fp16(const MxGemmArgs &g, const MxAdapterArgs &ad, int out_dtype, hipStream_t stream);
+void few_adapters_fp16(const MxFewArgs &g, const MxAdapterArgs &ad, int x_dtype, int out_dtype, hipStream_t stream);
+void gemm_adapters_fp32(const MxGemmArgs &g, const MxAdapterArgs &ad, int out_dtype, hipStream_t stream);
+void few_adapters_fp32(const MxFewArgs &g, const MxAdapterArgs &ad, int x_dtype, int out_dtype, hipStream_t stream);
+
+void gemm_adapters(const MxGemmArgs &g, const MxAdapterArgs &ad, int out_dtype, hipStream_t stream)
 {
-    with_dtype(out_dtype, [&](auto o) {
-        with_shape(shape_of(tiles_of(g.M, g.N), g.kb), [&](auto shape) {
-            typedef decltype(shape) S;
-            const unsigned grid = gemm_grid(g, S::BM, S::BN);
-            hipLaunchKernelGGL((mx_gemm_tile_adapters<S, decltype(o)>), dim3(grid), dim3(S::threads), 0, stream, g, ad);
-        });
-    });
+    auto f = ad.dtype == CONVIMG_BF16 ? gemm_adapters_bf16 : ad.dtype == CONVIMG_FP16 ? gemm_adapters_fp16 : gemm_adapters_fp32;
+    f(g, ad, out_dtype, stream);
 }
 
 void few_adapters(const MxFewArgs &g, const MxAdapterArgs &ad, int x_dtype, int out_dtype, hipStream_t stream)
 {
-    const int pairs = (g.kb + 7) / 8, waves = pairs < kMxFewWaves ? pairs : kMxFewWaves;
-    with_dtype(x_dtype, [&](auto x) {
-        with_dtype(out_dtype, [&](auto o) {
-            hipLaunchKernelGGL((mx_gemm_few<decltype(x), decltype(o), MxAdapterArgs>), dim3((g.N + 15) / 16),
-                               dim3(waves * 64), 0, stream, g, ad);
-        });
-    });
+    auto f = ad.dtype == CONVIMG_BF16 ? few_adapters_bf16 : ad.dtype == CONVIMG_FP16 ? few_adapters_fp16 : few_adapters_fp32;
+    f(g, ad, x_dtype, out_dtype, stream);
 }
 
 constexpr int kMaxRank = 4096;
 
-int adapters_shape(int M, int N, int K, int rank)
+// Columns of an adapter at most: 16 rows of it stay below 2^31 bytes.
+constexpr int kMaxAdapterCols = (1 << 25) - 1;
+
+int adapters_shape(int M, int N, int K, int adapters, int rank)
 {
     int rc = mx_shape(M, K);
     if (rc == CONVIMG_OK)
         rc = N <= 0 ? CONVIMG_ERR_SHAPE : mx_shape(N, K);
     if (rc == CONVIMG_OK)
-        rc = rank <= 0 ? CONVIMG_ERR_SHAPE : rank > kMaxRank ? CONVIMG_ERR_RANGE : CONVIMG_OK;
+        rc = rank <= 0 || adapters <= 0 ? CONVIMG_ERR_SHAPE
+             : rank > kMaxRank || N > kMaxAdapterCols || K > kMaxAdapterCols ? CONVIMG_ERR_RANGE
+                                                                            : CONVIMG_OK;
     return rc;
 }
 
-// Workspace of the forward call: x's packed rows, then h's parts.
-size_t fwd_codes(int M, int K) { return few_dense(M, K) ? 0 : packed_bytes(M, K); }
-size_t fwd_h(int M, int K, int rank) { return (size_t)adapter_splits(M, K, false) * M * rank * 4; }
+// Workspace of the forward call: x's packed rows, h's parts and the sorted
+// order; for a call that keeps something and one that does not.
+struct AdFwdLayout {
+    size_t h, order, total;
+    AdPlan plan;
+};
+
+AdFwdLayout ad_fwd_layout(int M, int K, int G, int rank, bool keep)
+{
+    AdFwdLayout l;
+    l.plan = adapter_plan(M, K, G, keep);
+    if (few_dense(M, K))      // (its product takes the rows as they come)
+        l.plan.sorted = false;
+    l.h = few_dense(M, K) ? 0 : packed_bytes(M, K);
+    l.order = l.h + align256((size_t)l.plan.splits * M * rank * 4);
+    l.total = l.order + (l.plan.sorted ? (size_t)M * 8 : 0);
+    return l;
+}
 
 struct AdBwdLayout {
-    size_t dy, t, part_down, part_up, count, total;
-    int split_down, split_up;
+    size_t dy, t, part_down, part_up, order, start, total;
+    int per_down, per_up;
 };
+
+int ad_chunks(int M, int per) { return (int)((M + (long long)per - 1) / per); }
 
 AdBwdLayout ad_bwd_layout(int M, int N, int K, int G, int rank)
 {
@@ -63,23 +83,22 @@ AdBwdLayout ad_bwd_layout(int M, int N, int K, int G, int rank)
         at += align256(n);
         return here;
     };
-    l.split_down = adapter_grad_splits(M, K, G, rank);
-    l.split_up = adapter_grad_splits(M, N, G, rank);
+    l.per_down = adapter_grad_per(M, K, rank);
+    l.per_up = adapter_grad_per(M, N, rank);
     l.dy = take(packed_bytes(M, N));
     l.t = take((size_t)M * rank * 4);
-    l.part_down = take(l.split_down > 1 ? (size_t)l.split_down * G * rank * K * 4 : 0);
-    l.part_up = take(l.split_up > 1 ? (size_t)l.split_up * G * rank * N * 4 : 0);
-    l.count = take((size_t)(l.split_down + l.split_up) * G * 4);
+    l.part_down = take((size_t)ad_chunks(M, l.per_down) * 2 * rank * K * 4);
+    l.part_up = take((size_t)ad_chunks(M, l.per_up) * 2 * rank * N * 4);
+    l.order = take((size_t)M * 8);
+    l.start = take(((size_t)G + 1) * 4);
     l.total = at;
     return l;
 }
 
 int ad_bwd_shape(int M, int N, int K, int adapters, int rank)
 {
-    int rc = adapters_shape(M, K, N, rank);      // dy's rows and wt's
-    if (rc == CONVIMG_OK)
-        rc = mx_shape(M, K);
-    return rc != CONVIMG_OK ? rc : adapters <= 0 ? CONVIMG_ERR_SHAPE : CONVIMG_OK;
+    const int rc = adapters_shape(M, K, N, adapters, rank);      // dy's rows and wt's
+    return rc != CONVIMG_OK ? rc : mx_shape(M, K);
 }
 
 }  // namespace convimg
@@ -88,16 +107,17 @@ using namespace convimg;
 
 extern "C" {
 
-int mxfp4_linear_adapters_workspace(int M, int N, int K, int rank, int x_dtype, size_t *bytes)
+int mxfp4_linear_adapters_workspace(int M, int N, int K, int adapters, int rank, int x_dtype, size_t *bytes)
 {
     if (!bytes)
         return CONVIMG_ERR_NULL;
-    const int rc = adapters_shape(M, N, K, rank);
+    const int rc = adapters_shape(M, N, K, adapters, rank);
     if (rc != CONVIMG_OK)
         return rc;
     if (!dtype_ok(x_dtype))
         return CONVIMG_ERR_DTYPE;
-    *bytes = fwd_codes(M, K) + fwd_h(M, K, rank);
+    const size_t a = ad_fwd_layout(M, K, adapters, rank, false).total, b = ad_fwd_layout(M, K, adapters, rank, true).total;
+    *bytes = a > b ? a : b;
     return CONVIMG_OK;
 }
 
@@ -107,12 +127,12 @@ int mxfp4_linear_adapters_fwd(const void *x, long long ldx, int x_dtype, const v
                               float *h, void *x_codes, void *x_scales, void *ws, size_t ws_bytes, hipStream_t stream)
 {
     size_t need = 0;
-    const int rc = mxfp4_linear_adapters_workspace(M, N, K, rank, x_dtype, &need);
+    const int rc = mxfp4_linear_adapters_workspace(M, N, K, adapters, rank, x_dtype, &need);
     if (rc != CONVIMG_OK)
         return rc;
     if (!dtype_ok(out_dtype) || !dtype_ok(a_dtype))
         return CONVIMG_ERR_DTYPE;
-    if (ldx < K || adapters <= 0)
+    if (ldx < K)
         return CONVIMG_ERR_SHAPE;
     if (M == 0)
         return CONVIMG_OK;
@@ -132,15 +152,18 @@ int mxfp4_linear_adapters_fwd(const void *x, long long ldx, int x_dtype, const v
     if (any_overlap(outs, nout, 5, in, nin, 8))
         return CONVIMG_ERR_ALIAS;
     // (what is kept has to be whole, not in parts)
-    const bool keep = h || x_codes;
-    const int splits = adapter_splits(M, K, keep);
-    unsigned char *codes = fwd_codes(M, K) ? (unsigned char *)ws : nullptr,
+    const AdFwdLayout l = ad_fwd_layout(M, K, adapters, rank, h || x_codes);
+    unsigned char *base = (unsigned char *)ws, *codes = l.h ? base : nullptr,
                   *scales = codes ? codes + align256(mx_code_bytes(M, K)) : nullptr;
-    float *hh = h ? h : (float *)((unsigned char *)ws + fwd_codes(M, K));
-    const AdShrinkArgs s = {x,      down, ids, hh, codes, scales, (unsigned char *)x_codes, (unsigned char *)x_scales,
-                            ldx,    M,    K,   adapters, rank};
-    adapter_shrink(s, x_dtype, a_dtype, splits, stream);
-    const MxAdapterArgs ad = {hh, up, scale, ids, adapters, rank, splits, a_dtype};
+    int *order = l.plan.sorted ? (int *)(base + l.order) : nullptr;
+    // (h in the rows' own order needs no copy of its own)
+    float *hh = h && !order ? h : (float *)(base + l.h);
+    if (order)
+        adapter_sort(ids, M, adapters, order, nullptr, stream);
+    const AdShrinkArgs s = {x,      down, ids, order, hh, order ? h : nullptr, codes, scales, (unsigned char *)x_codes,
+                            (unsigned char *)x_scales, ldx, M, K, adapters, rank};
+    adapter_shrink(s, l.plan, x_dtype, a_dtype, stream);
+    const MxAdapterArgs ad = {hh, up, scale, ids, order, adapters, rank, l.plan.splits, a_dtype};
     const MxOperand b = {(const unsigned char *)w_codes, (const unsigned char *)w_scales};
     if (!codes)
         few_adapters({x, b.codes, b.scales, bias, out, ldx, M, N, K, mx_blocks(K)}, ad, x_dtype, out_dtype, stream);
@@ -199,20 +222,23 @@ int mxfp4_linear_adapters_bwd(const void *dy, long long lddy, int dy_dtype, cons
     }
     unsigned char *base = (unsigned char *)ws, *codes = base + l.dy, *scales = codes + align256(mx_code_bytes(M, N));
     float *t = (float *)(base + l.t);
-    int *count = (int *)(base + l.count);
-    const AdShrinkArgs s = {dy, up, ids, t, dx ? codes : nullptr, scales, nullptr, nullptr, lddy, M, N, adapters, rank};
-    adapter_shrink(s, dy_dtype, a_dtype, 1, stream);
+    int *order = (int *)(base + l.order), *start = (int *)(base + l.start);
+    adapter_sort(ids, M, adapters, order, start, stream);
+    const AdShrinkArgs s = {dy, up, ids, order, t, nullptr, dx ? codes : nullptr, scales, nullptr, nullptr, lddy, M, N,
+                            adapters, rank};
+    adapter_shrink(s, {false, true, 1}, dy_dtype, a_dtype, stream);
     if (dx) {
-        const MxAdapterArgs ad = {t, down, scale, ids, adapters, rank, 1, a_dtype};
+        const MxAdapterArgs ad = {t, down, scale, ids, order, adapters, rank, 1, a_dtype};
         gemm_adapters(gemm_args({codes, scales}, {(const unsigned char *)wt_codes, (const unsigned char *)wt_scales},
                                 nullptr, M, K, N, dx),
                       ad, dx_dtype, stream);
     }
-    adapter_grad({h, dy, nullptr, ids, scale, dup, (float *)(base + l.part_up), count, lddy, M, N, adapters, rank}, dy_dtype,
-                 l.split_up, stream);
-    adapter_grad({t, x, (const unsigned char *)x_scales, ids, scale, ddown, (float *)(base + l.part_down),
-                  count + (long long)l.split_up * adapters, ldx, M, K, adapters, rank},
-                 x_dtype, l.split_down, stream);
+    adapter_grad({h, dy, nullptr, ids, order, start, scale, dup, (float *)(base + l.part_up), lddy, M, N, adapters, rank, 0,
+                  l.per_up, ad_chunks(M, l.per_up)},
+                 dy_dtype, stream);
+    adapter_grad({t, x, (const unsigned char *)x_scales, ids, order, start, scale, ddown, (float *)(base + l.part_down),
+                  ldx, M, K, adapters, rank, 1, l.per_down, ad_chunks(M, l.per_down)},
+                 x_dtype, stream);
     return launched();
 }
 

@@ -39,7 +39,7 @@ struct MxFewArgs {
     int M, N, K, kb;
 };
 
-// AD: MxAdapterArgs adds each row's low-rank adapter, MxNoAdapters nothing.
+// AD: MxAdapters adds each row's low-rank adapter, MxNoAdapters nothing.
 template <typename X, typename O, typename AD = MxNoAdapters>
 __global__ __launch_bounds__(kMxFewWaves * 64) void mx_gemm_few(MxFewArgs g, AD ad)
 {
@@ -116,32 +116,24 @@ __global__ __launch_bounds__(kMxFewWaves * 64) void mx_gemm_few(MxFewArgs g, AD 
         fetch(u * waves + wave, u);
     if constexpr (ADAPT) {
         const int n = n0 + (threadIdx.x & 15), first = threadIdx.x >> 4, step = blockDim.x >> 4;
-        auto add = [&](auto type) {
-            typedef decltype(type) T;
+        typedef typename AD::type T;
 #pragma unroll
-            for (int m = 0; m < kMxFewM; ++m) {
-                const int id = m < g.M ? ad.ids[m] : -1;
-                if (id < 0 || id >= ad.G || n >= g.N)
-                    continue;
-                const typename T::raw *up = (const typename T::raw *)ad.up + (long long)id * ad.r * g.N + n;
-                for (int i = first; i < ad.r; i += step) {
-                    float h = h0[m];
-                    if (i != first) {
-                        h = 0.f;
-                        for (int k = 0; k < ad.splits; ++k)
-                            h += ad.h[((long long)k * g.M + m) * ad.r + i];
-                    }
-                    low[m] = __builtin_fmaf(h, load1<T>(up + (long long)i * g.N), low[m]);
+        for (int m = 0; m < kMxFewM; ++m) {
+            const int id = m < g.M ? ad.ids[m] : -1;
+            if (id < 0 || id >= ad.G || n >= g.N)
+                continue;
+            const typename T::raw *up = (const typename T::raw *)ad.up + (long long)id * ad.r * g.N + n;
+            for (int i = first; i < ad.r; i += step) {
+                float h = h0[m];
+                if (i != first) {
+                    h = 0.f;
+                    for (int k = 0; k < ad.splits; ++k)
+                        h += ad.h[((long long)k * g.M + m) * ad.r + i];
                 }
-                low[m] *= ad.scale[id];
+                low[m] = __builtin_fmaf(h, load1<T>(up + (long long)i * g.N), low[m]);
             }
-        };
-        if (ad.dtype == CONVIMG_BF16)
-            add(Bf16{});
-        else if (ad.dtype == CONVIMG_FP16)
-            add(Fp16{});
-        else
-            add(Fp32{});
+            low[m] *= ad.scale[id];
+        }
     }
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i)

@@ -111,7 +111,7 @@ constexpr int mx_gemm_lds()
 // own, and their sums meet in LDS at the end: where there are few output
 // tiles this keeps more copies in flight a CU.
 //
-// AD: MxAdapterArgs adds each row's low-rank adapter to the sums, MxNoAdapters
+// AD: MxAdapters adds each row's low-rank adapter to the sums, MxNoAdapters
 // nothing.
 template <typename S, typename O, typename AD = MxNoAdapters>
 __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsigned char *smem, const AD &ad = {})
@@ -243,10 +243,6 @@ __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsign
 #pragma unroll
         for (int c = 0; c < (t < STAGES - 1 ? PER : E0); ++c)
             issue1(t0 + t, c);
-    // (adapters while the copies are under way)
-    if constexpr (!__is_same(AD, MxNoAdapters))
-        if (group == 0)
-            adapter_expand<FM, FN>(ad, g.M, g.N, m0 + wm * TM, n0 + wn * TN, acc);
 
     // Step h of a K tile takes two blocks of each row.  Of eight, lanes 0 .. 31
     // take block h and the others block 4 + h, so that each half needs one
@@ -328,6 +324,12 @@ __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsign
         __atomic_signal_fence(__ATOMIC_SEQ_CST);
     } while (++t < t0 + nk);
 
+    // Adapters, here and not while the first copies are under way: the loop's
+    // registers are free again, of which the largest tile has none to spare.
+    [[maybe_unused]] bool infinite = false;
+    if constexpr (!__is_same(AD, MxNoAdapters))
+        infinite = adapter_expand<typename AD::type, FM, FN, KG>(ad, g.M, g.N, m0 + wm * TM, n0 + wn * TN, group, acc);
+
     // Rows of the output through LDS, as many blocks of 32 a wave as it holds,
     // so that stores are 16 bytes a lane along the row.
     mx_wait_vm<0>();
@@ -370,6 +372,12 @@ __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsign
     static_assert(FM % G == 0 || G == 1, "whole groups");
 #pragma unroll
     for (int i0 = 0; i0 < FM; i0 += G) {
+        // (adapters: row l32 of each block at its own place of the output)
+        [[maybe_unused]] int place[G];
+        if constexpr (!__is_same(AD, MxNoAdapters))
+#pragma unroll
+            for (int i = 0; i < G; ++i)
+                place[i] = ad.row(min(m0 + wm * TM + (i0 + i) * 32 + l32, g.M - 1));
 #pragma unroll
         for (int i = 0; i < G; ++i) {
             unsigned char *mine = lds + (i * NW + wave) * 32 * PITCH;
@@ -394,7 +402,15 @@ __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsign
         for (int i = 0; i < G; ++i) {
             const unsigned char *mine = lds + (i * NW + wave) * 32 * PITCH;
             const int m = m0 + wm * TM + (i0 + i) * 32, rows = min(g.M - m, 32);
-            typename O::raw *o = (typename O::raw *)g.out + (long long)m * g.N + n;
+            typename O::raw *to[32 / RP];
+#pragma unroll
+            for (int p = 0; p < 32 / RP; ++p) {
+                const int r = p * RP + lane / CHUNKS;
+                long long row = m + r;
+                if constexpr (!__is_same(AD, MxNoAdapters))
+                    row = __shfl(place[i], r);
+                to[p] = (typename O::raw *)g.out + row * g.N + n;
+            }
             if (n + EPC <= g.N) {
 #pragma unroll
                 for (int p = 0; p < 32 / RP; ++p) {
@@ -402,15 +418,19 @@ __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsign
                     const u32v4_t v = *(const u32v4_t *)(mine + r * PITCH + k * 16);
                     if (r < rows) {
                         if constexpr (OS == 4)
-                            *(u32v4_a4_t *)(o + (long long)r * g.N) = v;
+                            *(u32v4_a4_t *)to[p] = v;
                         else
-                            *(u32v4_a2_t *)(o + (long long)r * g.N) = v;
+                            *(u32v4_a2_t *)to[p] = v;
                     }
                 }
             } else if (n < g.N) {
-                for (int r = lane / CHUNKS; r < rows; r += RP)
-                    for (int e = 0; n + e < g.N; ++e)
-                        o[(long long)r * g.N + e] = ((const typename O::raw *)(mine + r * PITCH + k * 16))[e];
+#pragma unroll
+                for (int p = 0; p < 32 / RP; ++p) {
+                    const int r = p * RP + lane / CHUNKS;
+                    if (r < rows)
+                        for (int e = 0; n + e < g.N; ++e)
+                            to[p][e] = ((const typename O::raw *)(mine + r * PITCH + k * 16))[e];
+                }
             }
         }
         if (i0 + G < FM) {
@@ -418,6 +438,11 @@ __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsign
             __builtin_amdgcn_wave_barrier();
         }
     }
+    if constexpr (!__is_same(AD, MxNoAdapters))
+        if (infinite) {
+            mx_wait_vm<0>();
+            adapter_infinite<typename AD::type, O>(ad, g.M, g.N, m0 + wm * TM, n0 + wn * TN, TM, TN, g.out);
+        }
 }
 
 template <typename S, typename O>
@@ -429,8 +454,8 @@ __global__ __launch_bounds__(S::threads) void mx_gemm_tile(MxGemmArgs g)
         mx_gemm_body<S, O>(g, id, smem);
 }
 
-template <typename S, typename O>
-__global__ __launch_bounds__(S::threads) void mx_gemm_tile_adapters(MxGemmArgs g, MxAdapterArgs ad)
+template <typename S, typename O, typename T>
+__global__ __launch_bounds__(S::threads) void mx_gemm_tile_adapters(MxGemmArgs g, MxAdapters<T> ad)
 {
     __shared__ __attribute__((aligned(16))) unsigned char smem[mx_gemm_lds<S, sizeof(typename O::raw)>()];
     const unsigned id = mx_xcd_tile(blockIdx.x, gridDim.x);

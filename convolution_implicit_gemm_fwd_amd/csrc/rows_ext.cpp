@@ -639,7 +639,7 @@ PyObject *adapters(PyObject *, PyObject *const *a, Py_ssize_t count)
             Py_RETURN_NONE;
         const int M = (int)x.rows, N = w.rows, K = w.cols;
         size_t need = 0;
-        if (p_mxfp4_linear_adapters_workspace(M, N, K, low.rank, x.type, &need) != CONVIMG_OK)
+        if (p_mxfp4_linear_adapters_workspace(M, N, K, low.number, low.rank, x.type, &need) != CONVIMG_OK)
             Py_RETURN_NONE;
         c10::SmallVector<int64_t, 8> sizes(x.t->sizes().begin(), x.t->sizes().end());
         sizes.back() = N;

@@ -679,7 +679,7 @@ def mxfp4_linear_adapters_nhwc(x, w, bias, adapters, ids, out_dtype=None, save=F
         out_dtype = x.dtype
     xd, od = _dtype(x.dtype, "x"), _dtype(out_dtype, "out_dtype")
     b = _param(bias, N, dev, "bias")
-    need = _adapters_bytes(M, N, K, rank, xd)
+    need = _adapters_bytes(M, N, K, G, rank, xd)
     out = _empty(*x.shape[:-1], N, dtype=out_dtype, device=dev)
     kept = _kept(dev, M, K) if save else None
     h = _empty(*x.shape[:-1], rank, dtype=_f32, device=dev) if save else None

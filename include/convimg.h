@@ -591,7 +591,7 @@ int mxfp4_linear_adapters_fwd(const void *x, long long ldx, int x_dtype, const v
                               const float *bias, const void *down, const void *up, const float *scale, const int *ids,
                               int adapters, int rank, int a_dtype, int M, int N, int K, int out_dtype, void *out,
                               float *h, void *x_codes, void *x_scales, void *ws, size_t ws_bytes, hipStream_t stream);
-int mxfp4_linear_adapters_workspace(int M, int N, int K, int rank, int x_dtype, size_t *bytes);
+int mxfp4_linear_adapters_workspace(int M, int N, int K, int adapters, int rank, int x_dtype, size_t *bytes);
 
 /* Gradients of mxfp4_linear_adapters_fwd with the shared weights and the bias
  * frozen.  With t[m] = up_g dy[m]:
