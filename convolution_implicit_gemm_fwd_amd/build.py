@@ -29,12 +29,14 @@ UNITS = [(os.path.join(CSRC, "conv2d_fwd.hip"), []),
          (os.path.join(CSRC, "mxint8.hip"), []),
          (os.path.join(CSRC, "adapters.hip"), []),
          (os.path.join(CSRC, "adapter_shrink.hip"), []),
-         (os.path.join(CSRC, "adapter_grads.hip"), []),
+         (os.path.join(CSRC, "adapter_grads_bf16.hip"), []),
+         (os.path.join(CSRC, "adapter_grads_fp16.hip"), []),
+         (os.path.join(CSRC, "adapter_grads_fp32.hip"), []),
          (os.path.join(CSRC, "adapter_products_bf16.hip"), []),
          (os.path.join(CSRC, "adapter_products_fp16.hip"), []),
          (os.path.join(CSRC, "adapter_products_fp32.hip"), [])]
 SOURCES = [u[0] for u in UNITS]
-DEPENDS = SOURCES + [os.path.join(CSRC, h) for h in ("igemm_common.hpp", "igemm_regs.hpp", "igemm_pipe.hpp", "igemm_patch.hpp", "igemm_strip.hpp", "igemm_window.hpp", "igemm_resident.hpp", "igemm_image.hpp", "igemm_dgrad.hpp", "igemm_wgrad.hpp", "igemm_layout.hpp", "row_common.hpp", "layer_norm.hpp", "mxint8.hpp", "mxfp4_quant.hpp", "mxfp4_gemm.hpp", "mxfp4_few.hpp", "mxfp4_plan.hpp", "adapter_expand.hpp", "adapter.hpp", "adapter_products.hpp", "rows_ext.cpp")] + [os.path.join(INCLUDE, "convimg.h")]
+DEPENDS = SOURCES + [os.path.join(CSRC, h) for h in ("igemm_common.hpp", "igemm_regs.hpp", "igemm_pipe.hpp", "igemm_patch.hpp", "igemm_strip.hpp", "igemm_window.hpp", "igemm_resident.hpp", "igemm_image.hpp", "igemm_dgrad.hpp", "igemm_wgrad.hpp", "igemm_layout.hpp", "row_common.hpp", "layer_norm.hpp", "mxint8.hpp", "mxfp4_quant.hpp", "mxfp4_gemm.hpp", "mxfp4_few.hpp", "mxfp4_plan.hpp", "adapter_expand.hpp", "adapter.hpp", "adapter_products.hpp", "adapter_grads.hpp", "rows_ext.cpp")] + [os.path.join(INCLUDE, "convimg.h")]
 
 ARCH = "gfx950"
 HIPCC_FLAGS = [

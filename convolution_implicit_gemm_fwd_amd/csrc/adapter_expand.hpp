@@ -83,13 +83,21 @@ __device__ __forceinline__ f32x16_t mfma_terms32(const u32v4_t (&a)[NA], const u
 
 struct MxNoAdapters {};
 
+// Ranks in whole steps of the matrix instruction.
+__host__ __device__ inline int adapter_ranks(int r) { return (r + 15) & ~15; }
+
+// h of a place as the products take it: scaled, for each 16 ranks three terms
+// of 16, zeros past the rank.
+constexpr int kAdTermBytes = 96;
+
 struct MxAdapterArgs {
-    const float *h;        // [splits][M][r], to be summed over the splits
-    const void *up;        // [G][r][N]
-    const float *scale;    // [G]
-    const int *ids;        // [rows]
-    const int *order;      // [M]: the row at each place of h and of the product, or NULL for their own order
-    int G, r, splits, dtype;
+    const unsigned char *terms;      // [M][ranks / 16][3][16] bf16, 16-byte aligned
+    const float *h;                  // [M][adapter_ranks(r)], not scaled
+    const void *up;                  // [G][r][N]
+    const float *scale;              // [G]
+    const int *key;                  // [M]: the adapter at each place of h and of the product
+    const int *order;                // [M]: the output's row at each place, or NULL for their own order
+    int G, r, dtype;
 
     __device__ __forceinline__ int row(int m) const { return order ? order[m] : m; }
 };
@@ -100,151 +108,156 @@ struct MxAdapters : MxAdapterArgs {
     typedef T type;
 };
 
-// Eight ranks of a row from i0 on, the parts' sums, zeros past the rank.
-// (Loads are unconditional, at clamped places: a branch around each would make
-// the wave wait for them one by one.)
-__device__ __forceinline__ void adapter_h8(const MxAdapterArgs &a, int M, int m, int i0, float (&v)[8])
+// Eight loaded values of up as terms; infinities and NaN, of which the answer
+// tells, are left out.
+template <typename T>
+__device__ __forceinline__ bool adapter_up8(const typename T::raw (&w)[8], u32v4_t (&t)[split_terms<T>()])
 {
-    const float *p = a.h + (long long)m * a.r;
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        v[e] = 0.f;
-    for (int k = 0; k < a.splits; ++k, p += (long long)M * a.r) {
+    if constexpr (T::code == CONVIMG_FP32) {
         float u[8];
-        if (a.r >= 8) {
-            unpack8<Fp32>(load_raw8<Fp32, false>(p, i0, a.r), u);
-        } else {
+        unsigned top = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            top = mx_top(top, u[e] = w[e]);
+        const bool odd = __any(top >= 0x7f800000u);
+        if (odd)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                u[e] = p[min(i0 + e, a.r - 1)];
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            v[e] += u[e];
-    }
-    if (a.r >= 8) {
-        Raw8<Fp32> w;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            w.w[e / 4][e % 4] = __float_as_uint(v[e]);
-        unpack8<Fp32>(tail8<Fp32, false>(w, i0, a.r), v);
+                u[e] = __builtin_fabsf(u[e]) < __builtin_inff() ? u[e] : 0.f;
+        split8(u, t);
+        return odd;
     } else {
+        typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+        constexpr unsigned short INF = T::code == CONVIMG_BF16 ? 0x7f80 : 0x7c00;
+        u16x2 top = {};
+        Raw8<T> r;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            v[e] = i0 + e < a.r ? v[e] : 0.f;
+        for (int e = 0; e < 4; ++e) {
+            r.w[0][e] = w[2 * e] | (unsigned)w[2 * e + 1] << 16;
+            top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, r.w[0][e] & 0x7fff7fffu));
+        }
+        const bool odd = __any(max(top[0], top[1]) >= INF);
+        if (odd)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const unsigned v = r.w[0][e];
+                r.w[0][e] = ((v & 0x7fffu) < INF ? v & 0xffffu : 0u) | ((v >> 16 & 0x7fffu) < INF ? v & 0xffff0000u : 0u);
+            }
+        split_raw8<T>(r, t);
+        return odd;
     }
 }
 
-// Adds to the sums of FM x FN blocks of 32 x 32 from row m0 and column n0 on; a
-// lane holds row lane % 32 of a block and 16 of its columns (the instruction's
+// Adds to the sums of FM x FN blocks of 32 x 32 from place m0 and column n0 on; a
+// lane holds place lane % 32 of a block and 16 of its columns (the instruction's
 // rows).
 //
-// For 16 ranks at a time the wave goes through the adapters that its rows have,
-// in the order of their first rows, P of them in flight at once; of KG groups
-// of waves that share the tile each takes every KG-th.  A row has zeros for h
-// in another adapter's product.  Zero times an infinity would not do: such
-// values of up are left out (0) here, and the answer says that there are some,
-// for adapter_infinite.  (Selecting by row after the product instead takes the
-// sums from the matrix unit's registers: the largest tile then spills.)
+// The wave goes through the adapters that its places have, in their order, 16
+// ranks at a time, P such steps in flight at once (loads are unconditional, at
+// clamped places: a branch around each would make the wave wait for them one
+// by one); of KG groups of waves that share the tile each takes every KG-th
+// step.  A place has zeros for h in another adapter's product.  Zero times an
+// infinity would not do: such values of up are left out (0) here, and the answer
+// says that there are some, for adapter_infinite.  (Selecting by place after the
+// product instead takes the sums from the matrix unit's registers: the largest
+// tile then spills.)
 template <typename T, int FM, int FN, int KG>
 __device__ __forceinline__ bool adapter_expand(const MxAdapterArgs &a, int M, int N, int m0, int n0, int group,
                                                f32x16_t (&acc)[FM][FN])
 {
-    constexpr int P = FM * FN <= 1 ? 8 : FM * FN <= 2 ? 4 : FM * FN <= 4 ? 2 : 1;
+    constexpr int P = FM * FN <= 1 ? 8 : FM * FN <= 2 ? 4 : 2, NT = split_terms<T>();
     const int lane = threadIdx.x & 63, half = lane >> 5, l32 = lane & 31;
+    const int steps = adapter_ranks(a.r) / 16;
     int id[FM];
-    float s[FM];
-    unsigned any[FM];
+    unsigned any[FM], left[FM];
     bool infinite = false;
 #pragma unroll
     for (int i = 0; i < FM; ++i)
-        id[i] = a.ids[a.row(min(m0 + i * 32 + l32, M - 1))];
+        id[i] = a.key[min(m0 + i * 32 + l32, M - 1)];
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
         id[i] = m0 + i * 32 + l32 < M && id[i] < a.G ? id[i] : -1;
-        s[i] = a.scale[max(id[i], 0)];
-        any[i] = (unsigned)__ballot(id[i] >= 0);
+        left[i] = any[i] = (unsigned)__ballot(id[i] >= 0);
     }
-    // (one pass through each loop at least, without a branch around: the sums stay where they are)
-    int r0 = 0, turn = group;
-    do {
-        const int i0 = r0 + half * 8;
-        u32v4_t h[FM][3];
-#pragma unroll
-        for (int i = 0; i < FM; ++i) {
-            float v[8];
-            adapter_h8(a, M, min(m0 + i * 32 + l32, M - 1), i0, v);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                v[e] *= s[i];
-            split8(v, h[i]);
-        }
-        unsigned left[FM], rest;
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
-            left[i] = any[i];
-        int number = 0;      // of the adapter among the tile's
-        do {
-            int g[P];
-            typename T::raw w[P][FN][8];
-#pragma unroll
-            for (int p = 0; p < P; ++p) {
-                for (;;) {
-                    g[p] = -2;
-#pragma unroll
-                    for (int i = 0; i < FM; ++i)
-                        if (g[p] < 0 && left[i])
-                            g[p] = __builtin_amdgcn_readlane(id[i], __builtin_ctz(left[i]));
-#pragma unroll
-                    for (int i = 0; i < FM; ++i)
-                        left[i] &= ~(unsigned)__ballot(id[i] == g[p]);
-                    if (KG == 1 || g[p] < 0 || (number++ + turn) % KG == 0)
-                        break;
-                }
-                const typename T::raw *up = (const typename T::raw *)a.up + (long long)max(g[p], 0) * a.r * N;
-#pragma unroll
-                for (int j = 0; j < FN; ++j)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        w[p][j][e] = up[(long long)min(i0 + e, a.r - 1) * N + min(n0 + j * 32 + l32, N - 1)];
-            }
-#pragma unroll
-            for (int p = 0; p < P; ++p) {
-                u32v4_t hm[FM][3];
-#pragma unroll
-                for (int i = 0; i < FM; ++i)
-#pragma unroll
-                    for (int k = 0; k < 3; ++k)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            hm[i][k][e] = id[i] == g[p] ? h[i][k][e] : 0u;
-#pragma unroll
-                for (int j = 0; j < FN; ++j) {
-                    float u[8];
-                    bool odd = false;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        u[e] = i0 + e < a.r ? load1<T>(&w[p][j][e]) : 0.f;
-                        const bool fine = __builtin_fabsf(u[e]) < __builtin_inff();
-                        odd |= !fine;
-                        u[e] = fine ? u[e] : 0.f;
-                    }
-                    infinite |= __any(odd);
-                    u32v4_t b[split_terms<T>()];
-                    split8(u, b);
-#pragma unroll
-                    for (int i = 0; i < FM; ++i)
-                        acc[i][j] = mfma_terms32(b, hm[i], acc[i][j]);
-                }
-            }
-            rest = 0;
+    int step = 0, number = 0;
+    // the next adapter, -2 for none, and (in step) its 16 ranks
+    auto next = [&]() {
+        for (;;) {
+            int g = -2;
 #pragma unroll
             for (int i = 0; i < FM; ++i)
-                rest |= left[i];
-        } while (rest);
-        r0 += 16;
-        ++turn;
-    } while (r0 < a.r);
+                if (g < 0 && left[i])
+                    g = __builtin_amdgcn_readlane(id[i], __builtin_ctz(left[i]));
+            if (g < 0) {
+                unsigned some = 0;
+#pragma unroll
+                for (int i = 0; i < FM; ++i)
+                    some |= left[i] = any[i];
+                if (!some || step + 1 >= steps) {
+#pragma unroll
+                    for (int i = 0; i < FM; ++i)
+                        left[i] = any[i] = 0;
+                    return g;
+                }
+                ++step;
+                continue;
+            }
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+                left[i] &= ~(unsigned)__ballot(id[i] == g);
+            if (KG == 1 || number++ % KG == group)
+                return g;
+        }
+    };
+    int g0 = next();
+    if (g0 < 0)
+        return false;
+    do {
+        int g[P];
+        u32v4_t h[P][FM][3];
+        typename T::raw w[P][FN][8];
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            g[p] = p == 0 ? g0 : next();
+            if (g[p] < 0)
+                continue;
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+                const u32v4_t *from = (const u32v4_t *)(a.terms + ((long long)min(m0 + i * 32 + l32, M - 1) * steps + step)
+                                                                     * kAdTermBytes) + half;
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+                    h[p][i][k] = from[2 * k];
+            }
+            const typename T::raw *up = (const typename T::raw *)a.up + (long long)g[p] * a.r * N;
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    w[p][j][e] = up[(long long)min(step * 16 + half * 8 + e, a.r - 1) * N + min(n0 + j * 32 + l32, N - 1)];
+        }
+        g0 = g[P - 1] < 0 ? -2 : next();
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            if (g[p] < 0)
+                continue;
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        h[p][i][k][e] = id[i] == g[p] ? h[p][i][k][e] : 0u;
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                u32v4_t b[NT];
+                infinite |= adapter_up8<T>(w[p][j], b);
+#pragma unroll
+                for (int i = 0; i < FM; ++i)
+                    acc[i][j] = mfma_terms32(b, h[p][i], acc[i][j]);
+            }
+        }
+    } while (g0 >= 0);
     return infinite;
 }
 
@@ -255,17 +268,14 @@ __device__ __forceinline__ void adapter_infinite(const MxAdapterArgs &a, int M, 
                                                  void *out)
 {
     for (int k = threadIdx.x & 63; k < TM * TN; k += 64) {
-        const int m = m0 + k / TN, n = n0 + k % TN, row = a.row(min(m, M - 1)), id = m < M && n < N ? a.ids[row] : -1;
+        const int m = m0 + k / TN, n = n0 + k % TN, row = a.row(min(m, M - 1)), id = m < M && n < N ? a.key[m] : -1;
         if (id < 0 || id >= a.G)
             continue;
         float s = 0.f;
         for (int i = 0; i < a.r; ++i) {
             const float u = load1<T>((const typename T::raw *)a.up + ((long long)id * a.r + i) * N + n);
             if (!(__builtin_fabsf(u) < __builtin_inff())) {
-                float h = 0.f;
-                for (int p = 0; p < a.splits; ++p)
-                    h += a.h[((long long)p * M + m) * a.r + i];
-                s += h * a.scale[id] * u;
+                s += a.h[(long long)m * adapter_ranks(a.r) + i] * a.scale[id] * u;
             }
         }
         if (!(__builtin_fabsf(s) < __builtin_inff()))

@@ -1,9 +1,11 @@
-// adapter_grads.hip -- gradients of the adapters: for each adapter g
+// adapter_grads.hpp -- gradients of the adapters: for each adapter g
 //
 //   out[i][c] = scale_g * sum over the rows m with ids[m] = g of u[m][i] * v[m][c]
 //
 // (u = t, v = x for down; u = h, v = dy for up).  The contracted axis is the
 // rows, of which an adapter has any number at any places.
+#pragma once
+
 #include "adapter.hpp"
 
 namespace convimg {
@@ -75,21 +77,19 @@ constexpr int grad_terms()
 constexpr int kAdGradCols = 128, kAdGradWaves = 4;
 
 template <typename V, int RT>
-__global__ __launch_bounds__(kAdGradWaves * 64) void ad_grad(AdGradArgs a, int tiles, int ranks)
+__device__ __forceinline__ void ad_grad_body(const AdGradArgs &a, unsigned b, f32x4_t (*sums)[8][64])
 {
-    __shared__ f32x4_t sums[kAdGradWaves - 1][8][64];
     constexpr int NV = grad_terms<V>();
-    unsigned b = blockIdx.x;
-    const int tile = (int)(b % tiles);
-    b /= tiles;
-    const int i0 = (int)(b % ranks) * 16 * RT, chunk = (int)(b / ranks);
+    const int tile = (int)(b % (unsigned)a.tiles);
+    b /= (unsigned)a.tiles;
+    const int i0 = (int)(b % (unsigned)a.ranks) * 16 * RT, chunk = (int)(b / (unsigned)a.ranks);
     const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = tile * kAdGradCols + r16 * 8;
     const int lo = chunk * a.per, hi = min(a.start[a.G], lo + a.per);
 
     for (int s0 = lo, s1; s0 < hi; s0 = s1) {
-        const int g = a.ids[a.order[s0]], g0 = a.start[g], g1 = a.start[g + 1];
+        const int g = a.key[s0], g0 = a.start[g], g1 = a.start[g + 1];
         s1 = min(hi, g1);
         f32x4_t acc[RT][8] = {};
         for (int p0 = s0 + wave * 32; p0 < s1; p0 += kAdGradWaves * 32) {
@@ -111,7 +111,7 @@ __global__ __launch_bounds__(kAdGradWaves * 64) void ad_grad(AdGradArgs a, int t
                 float u[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    u[e] = a.u[(long long)(a.u_sorted ? at[e] : row[e]) * a.r + i];
+                    u[e] = a.u[(long long)(a.u_sorted ? at[e] : row[e]) * a.u_ld + i];
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     u[e] = e < have ? u[e] : 0.f;
@@ -167,10 +167,22 @@ __global__ __launch_bounds__(kAdGradWaves * 64) void ad_grad(AdGradArgs a, int t
     }
 }
 
+// Both operands' gradients in one launch, up's first.
+template <typename DY, typename X, int RT>
+__global__ __launch_bounds__(kAdGradWaves * 64) void ad_grad(AdGradArgs up, AdGradArgs down, unsigned up_blocks)
+{
+    __shared__ f32x4_t sums[kAdGradWaves - 1][8][64];
+    if (blockIdx.x < up_blocks)
+        ad_grad_body<DY, RT>(up, blockIdx.x, sums);
+    else
+        ad_grad_body<X, RT>(down, blockIdx.x - up_blocks, sums);
+}
+
 // The sums of the adapters whose rows lie in several chunks, in order, and
 // zeros for those without rows.
-__global__ __launch_bounds__(256) void ad_grad_sum(AdGradArgs a)
+static __global__ __launch_bounds__(256) void ad_grad_sum(AdGradArgs up, AdGradArgs down)
 {
+    const AdGradArgs &a = blockIdx.z == 0 ? up : down;
     const long long per = (long long)a.r * a.C;
     for (int g = blockIdx.y; g < a.G; g += gridDim.y) {
         const int g0 = a.start[g], g1 = a.start[g + 1];
@@ -181,6 +193,7 @@ __global__ __launch_bounds__(256) void ad_grad_sum(AdGradArgs a)
             float s = 0.f;
             if (g0 < g1) {
                 s = a.part[(first * 2LL + (g0 == first * a.per ? 0 : 1)) * per + p];
+#pragma unroll 8
                 for (int k = first + 1; k <= last; ++k)
                     s += a.part[k * 2LL * per + p];
             }
@@ -189,38 +202,31 @@ __global__ __launch_bounds__(256) void ad_grad_sum(AdGradArgs a)
     }
 }
 
-int grad_ranks(int r) { return r <= 16 ? 1 : r <= 32 ? 2 : 4; }
+inline int grad_ranks(int r) { return r <= 16 ? 1 : r <= 32 ? 2 : 4; }
 
-// Sorted rows a chunk: as many chunks as give about 1024 workgroups, runs of 32.
-int adapter_grad_per(int M, int C, int r)
+// The launches for one type of dy.
+template <typename DY>
+void adapter_grads_of(const AdGradArgs &up, const AdGradArgs &down, int x_dtype, hipStream_t stream)
 {
-    const long long rt = 16 * grad_ranks(r), tiles = (C + kAdGradCols - 1LL) / kAdGradCols * ((r + rt - 1) / rt);
-    const long long chunks = tiles < 1024 ? 1024 / tiles : 1, per = (M + chunks - 1) / chunks;
-    return (int)((per + 31) / 32 * 32 < 32 ? 32 : (per + 31) / 32 * 32);
-}
-
-void adapter_grad(const AdGradArgs &a, int v_dtype, hipStream_t stream)
-{
-    auto launch = [&](auto v, auto rt) {
-        constexpr int RT = decltype(rt)::value;
-        const unsigned tiles = (unsigned)((a.C + kAdGradCols - 1LL) / kAdGradCols), ranks = (a.r + 16 * RT - 1) / (16 * RT);
-        hipLaunchKernelGGL((ad_grad<decltype(v), RT>), dim3(tiles * ranks * a.chunks), dim3(kAdGradWaves * 64), 0, stream, a,
-                           (int)tiles, (int)ranks);
+    const unsigned n_up = (unsigned)up.tiles * up.ranks * up.chunks, n_down = (unsigned)down.tiles * down.ranks * down.chunks;
+    auto launch = [&](auto x, auto rt) {
+        hipLaunchKernelGGL((ad_grad<DY, decltype(x), decltype(rt)::value>), dim3(n_up + n_down), dim3(kAdGradWaves * 64), 0,
+                           stream, up, down, n_up);
     };
-    auto ranks = [&](auto v) {
-        switch (grad_ranks(a.r)) {
-        case 1: launch(v, std::integral_constant<int, 1>{}); break;
-        case 2: launch(v, std::integral_constant<int, 2>{}); break;
-        default: launch(v, std::integral_constant<int, 4>{}); break;
+    auto ranks = [&](auto x) {
+        switch (grad_ranks(up.r)) {
+        case 1: launch(x, std::integral_constant<int, 1>{}); break;
+        case 2: launch(x, std::integral_constant<int, 2>{}); break;
+        default: launch(x, std::integral_constant<int, 4>{}); break;
         }
     };
-    if (v_dtype == CONVIMG_MXINT8)
+    if (x_dtype == CONVIMG_MXINT8)
         ranks(Kept{});
     else
-        with_dtype(v_dtype, ranks);
-    const long long n = ((long long)a.r * a.C + 255) / 256;
-    hipLaunchKernelGGL(ad_grad_sum, dim3((unsigned)(n < 256 ? n : 256), (unsigned)(a.G < 4096 ? a.G : 4096)), dim3(256), 0,
-                       stream, a);
+        with_dtype(x_dtype, ranks);
+    const long long n = ((long long)up.r * (up.C > down.C ? up.C : down.C) + 255) / 256;
+    hipLaunchKernelGGL(ad_grad_sum, dim3((unsigned)(n < 256 ? n : 256), (unsigned)(up.G < 4096 ? up.G : 4096), 2), dim3(256),
+                       0, stream, up, down);
 }
 
 }  // namespace convimg

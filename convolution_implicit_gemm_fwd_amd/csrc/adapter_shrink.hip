@@ -5,63 +5,91 @@
 
 namespace convimg {
 
+// h of one rank of a place, with its terms for the products.
+__device__ __forceinline__ void adapter_put(const AdShrinkArgs &a, int at, int row, int i, float h, float scale)
+{
+    const int rp = adapter_ranks(a.r);
+    a.h[(long long)at * rp + i] = h;
+    if (a.kept && i < a.r)
+        a.kept[(long long)row * a.r + i] = h;
+    if (a.terms) {
+        const float v[8] = {h * scale};
+        u32v4_t t[3];
+        split8(v, t);
+        unsigned short *p = (unsigned short *)(a.terms + ((long long)at * (rp / 16) + i / 16) * kAdTermBytes) + i % 16;
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+            p[k * 16] = (unsigned short)t[k][0];
+    }
+}
+
 // ---- few rows --------------------------------------------------------------
 //
-// A workgroup takes kAdFewCols columns of one row, a thread eight of them, with
-// its part of every rank's row of the adapter in flight at once: a serving batch
-// mostly has another adapter in every row, whose 2 r K bytes are the work.  The
-// parts' sums stay apart; what reads h adds them.
-constexpr int kAdFewThreads = 128, kAdFewCols = kAdFewThreads * 8, kAdFewRanks = 16;
+// A workgroup takes RC ranks of one row, a thread eight of every 4096 columns,
+// with its part of every rank's row of the adapter in flight at once: a serving
+// batch mostly has another adapter in every row, whose 2 r K bytes are the work.
+constexpr int kAdFewWaves = 8;
 
-template <typename X, typename A>
-__global__ __launch_bounds__(kAdFewThreads) void ad_shrink_few(AdShrinkArgs a)
+template <typename X, typename A, int RC>
+__global__ __launch_bounds__(kAdFewWaves * 64) void ad_shrink_few(AdShrinkArgs a)
 {
-    __shared__ float sums[2][kAdFewRanks];
-    const int m = blockIdx.y, c = blockIdx.x * kAdFewCols + threadIdx.x * 8;
-    const int id = a.ids[m];
+    __shared__ float sums[kAdFewWaves][RC];
+    const int m = blockIdx.x, i0 = blockIdx.y * RC, wave = threadIdx.x >> 6;
+    const int id = a.key[m];
     const bool has = id >= 0 && id < a.G;
-    const Raw8<X> raw = load_raw8<X>((const typename X::raw *)a.x + m * a.ldx, c, a.K);
-    float v[8];
-    unpack8<X>(tail8<X>(raw, c, a.K), v);
-    if (a.codes) {
-        unsigned top = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            top = mx_top(top, v[e]);
-        const unsigned byte = mx_scale_byte(quad_max(top));
-        const int kb = mx_blocks(a.K);
-        if (c < kb * 32)
-            ((unsigned *)a.codes)[((long long)m * kb * 32 + c) / 8] = mx_encode8(v, mx_scale_value(byte));
-        const unsigned word = mx_scale_word<16>(byte, c >> 5);
-        if ((c & 127) == 0 && c < a.K)
-            ((unsigned *)a.scales)[(long long)(c >> 7) * a.M + m] = word;
-    }
-    float *h = a.h + ((long long)blockIdx.x * a.M + m) * a.r;
+    const typename X::raw *x = (const typename X::raw *)a.x + m * a.ldx;
     const typename A::raw *down = (const typename A::raw *)a.down + (long long)id * a.r * a.K;
-    for (int i0 = 0; i0 < a.r; i0 += kAdFewRanks) {
-        Raw8<A> w[kAdFewRanks];
+    float s[RC] = {};
+    const int end = (a.K + 127) & ~127;      // (the lanes of a scale dword stay together)
+    for (int c = threadIdx.x * 8; c < end; c += kAdFewWaves * 512) {
+        const Raw8<X> raw = load_raw8<X>(x, c, a.K);
+        Raw8<A> w[RC];
         if (has)
 #pragma unroll
-            for (int i = 0; i < kAdFewRanks; ++i)
+            for (int i = 0; i < RC; ++i)
                 w[i] = load_raw8<A>(down + (long long)min(i0 + i, a.r - 1) * a.K, c, a.K);
-        __syncthreads();      // the previous sums have been read
+        float v[8];
+        unpack8<X>(tail8<X>(raw, c, a.K), v);
+        if (blockIdx.y == 0 && (a.codes || a.codes8)) {
+            unsigned top = 0;
 #pragma unroll
-        for (int i = 0; i < kAdFewRanks; ++i) {
-            float s = 0.f;
-            if (has) {
+            for (int e = 0; e < 8; ++e)
+                top = mx_top(top, v[e]);
+            if (a.codes) {
+                const unsigned byte = mx_scale_byte(quad_max(top));
+                const int kb = mx_blocks(a.K);
+                if (c < kb * 32)
+                    ((unsigned *)a.codes)[((long long)m * kb * 32 + c) / 8] = mx_encode8(v, mx_scale_value(byte));
+                const unsigned word = mx_scale_word<16>(byte, c >> 5);
+                if ((c & 127) == 0)
+                    ((unsigned *)a.scales)[(long long)(c >> 7) * a.M + m] = word;
+            }
+            if (a.codes8)
+                mxi_emit8<16>(a.codes8, (unsigned *)a.scales8, m, a.K, c, v);
+        }
+        if (has)
+#pragma unroll
+            for (int i = 0; i < RC; ++i) {
                 float u[8];
                 unpack8<A>(tail8<A>(w[i], c, a.K), u);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    s = __builtin_fmaf(u[e], v[e], s);
+                    s[i] = __builtin_fmaf(u[e], v[e], s[i]);
             }
-            s = group_sum<64>(s);
-            if ((threadIdx.x & 63) == 0)
-                sums[threadIdx.x >> 6][i] = s;
-        }
-        __syncthreads();
-        if (threadIdx.x < kAdFewRanks && i0 + (int)threadIdx.x < a.r)
-            h[i0 + threadIdx.x] = sums[0][threadIdx.x] + sums[1][threadIdx.x];
+    }
+#pragma unroll
+    for (int i = 0; i < RC; ++i) {
+        const float t = group_sum<64>(s[i]);
+        if ((threadIdx.x & 63) == 0)
+            sums[wave][i] = t;
+    }
+    __syncthreads();
+    const int i = i0 + (int)threadIdx.x;
+    if (threadIdx.x < RC && i < adapter_ranks(a.r)) {
+        float h = 0.f;
+        for (int k = 0; k < kAdFewWaves; ++k)
+            h += sums[k][threadIdx.x];
+        adapter_put(a, m, m, i, has && i < a.r ? h : 0.f, has ? a.scale[id] : 0.f);
     }
 }
 
@@ -89,22 +117,38 @@ struct Strip16 {
         for (int j = 0; j < 4; ++j)
             *(Raw8<T> *)(lds + (4 * j + (lane >> 4)) * PITCH + (lane & 15) * 8 * ES) = r[j];
     }
-    // columns 32 j + 8 (l / 16) .. of row l % 16
-    static __device__ __forceinline__ Raw8<T> get(const unsigned char *lds, int lane, int j)
+    // what lane l put
+    static __device__ __forceinline__ Raw8<T> own(const unsigned char *lds, int lane, int j)
     {
-        return *(const Raw8<T> *)(lds + (lane & 15) * PITCH + (j * 32 + (lane >> 4) * 8) * ES);
+        return *(const Raw8<T> *)(lds + (4 * j + (lane >> 4)) * PITCH + (lane & 15) * 8 * ES);
     }
-};
-
-// Eight columns from c on of a row that starts `off` bytes from base, zeros
-// past its K; WHOLE: c + 8 <= K in every lane.
-template <typename T, bool WHOLE>
-__device__ __forceinline__ Raw8<T> strip_load(const char *base, unsigned off, int c, int K)
-{
-    constexpr int ES = sizeof(typename T::raw);
-    if constexpr (WHOLE) {
+    // A strip that the rows' end cuts: value by value, zeros past it.  `row`
+    // gives the address of row r, which lane r holds.
+    static __device__ __forceinline__ void fill(unsigned char *lds, int lane, const char *row, int k0, int K)
+    {
+        // (loads at clamped places, 16 in flight)
+#pragma unroll 1
+        for (int e0 = lane; e0 < 16 * 128; e0 += 16 * 64) {
+            typename T::raw v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int e = e0 + i * 64;
+                const typename T::raw *p = (const typename T::raw *)__shfl((unsigned long long)row, e >> 7);
+                v[i] = p[min(k0 + (e & 127), K - 1)];
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int e = e0 + i * 64;
+                *(typename T::raw *)(lds + (e >> 7) * PITCH + (e & 127) * ES) =
+                    k0 + (e & 127) < K ? v[i] : (typename T::raw)0;
+            }
+        }
+    }
+    // columns c .. c + 7 of a row
+    static __device__ __forceinline__ Raw8<T> load(const char *row, unsigned c)
+    {
         Raw8<T> r;
-        const char *p = base + (off + (unsigned)c * ES);
+        const char *p = row + c * ES;
         if constexpr (ES == 4) {
             r.w[0] = ((const u32v4_a4_t *)p)[0];
             r.w[1] = ((const u32v4_a4_t *)p)[1];
@@ -112,14 +156,23 @@ __device__ __forceinline__ Raw8<T> strip_load(const char *base, unsigned off, in
             r.w[0] = *(const u32v4_a2_t *)p;
         }
         return r;
-    } else {
-        return tail8<T>(load_raw8<T>((const typename T::raw *)(base + off), c, K), c, K);
     }
-}
+    // columns 32 j + 8 (l / 16) .. of row l % 16
+    static __device__ __forceinline__ Raw8<T> get(const unsigned char *lds, int lane, int j)
+    {
+        return *(const Raw8<T> *)(lds + (lane & 15) * PITCH + (j * 32 + (lane >> 4) * 8) * ES);
+    }
+};
+
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 
 template <typename X, typename A, int RT>
 __global__ __launch_bounds__(kAdWaves * 64) void ad_shrink_tile(AdShrinkArgs a)
 {
+    // steps of a wave in flight, and tiles of ranks; fp32 and 64 ranks fill the registers with one
+    constexpr int DEPTH = sizeof(typename X::raw) == 2 && sizeof(typename A::raw) == 2 && RT <= 2 ? 2 : 1;
+    // (both fp16: their own instruction, which has the exact products, too)
+    constexpr bool HALVES = __is_same(X, Fp16) && __is_same(A, Fp16);
     constexpr int LDS = kAdWaves * (Strip16<X>::BYTES + Strip16<A>::BYTES), SUMS = kAdWaves * RT * 64 * 16;
     __shared__ __attribute__((aligned(16))) unsigned char lds[LDS > SUMS ? LDS : SUMS];
     const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4;
@@ -132,8 +185,8 @@ __global__ __launch_bounds__(kAdWaves * 64) void ad_shrink_tile(AdShrinkArgs a)
 
     // row r16 and the rows 4 j + q, the last one again past the end
     const bool real = m0 + r16 < a.M;
-    const int at = min(m0 + r16, a.M - 1), m = a.order ? a.order[at] : at;
-    const int given = real ? a.ids[m] : -1, id = given < a.G ? given : -1;
+    const int at = min(m0 + r16, a.M - 1), m = a.order ? a.order[at] : at, rp = adapter_ranks(a.r);
+    const int given = real ? a.key[at] : -1, id = given < a.G ? given : -1;
     unsigned left = (unsigned)__ballot(id >= 0) & 0xffffu;
     const char *x[4];
     int xrow[4];
@@ -144,65 +197,77 @@ __global__ __launch_bounds__(kAdWaves * 64) void ad_shrink_tile(AdShrinkArgs a)
         x[j] = (const char *)a.x + (long long)xrow[j] * a.ldx * (long long)sizeof(typename X::raw);
         woff[j] = (unsigned)min(4 * j + q, a.r - 1) * (unsigned)a.K * (unsigned)sizeof(typename A::raw);
     }
-    if (real && id < 0)      // no adapter: 0
-        for (int i = i0 + (threadIdx.x >> 4); i < min(a.r, i0 + 16 * RT); i += kAdWaves * 4) {
-            a.h[(long long)at * a.r + i] = 0.f;
-            if (a.kept)
-                a.kept[(long long)m * a.r + i] = 0.f;
-        }
+    if (real && id < 0 && blockIdx.z == 0)      // no adapter: 0
+        for (int i = i0 + (threadIdx.x >> 4); i < min(rp, i0 + 16 * RT); i += kAdWaves * 4)
+            adapter_put(a, at, m, i, 0.f, 0.f);
 
-    bool first = blockIdx.y == 0;
+    // Pass by pass; of the workgroups that share the tile the first takes the
+    // first pass and the quantisation, the second the second pass, and so on.
+    bool first = blockIdx.y == 0 && blockIdx.z == 0;
+    unsigned pass = 0;
     do {
         int g = -1;
         if (left) {
             g = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
             left &= ~(unsigned)__ballot(id == g);
         }
-        if (!first && g < 0)
-            return;      // (a further chunk of ranks for rows without adapters)
+        if (pass++ % gridDim.z != blockIdx.z || (!first && g < 0))
+            continue;
         f32x4_t acc[RT] = {};
-        Raw8<X> xn[4];      // the next step's
-        Raw8<A> wn[4];      // 16 ranks, the next ones'
-        auto fetch = [&](int k0) {
-            const int c = k0 + r16 * 8;
+        Raw8<X> xn[DEPTH][4];      // the steps in flight
+        Raw8<A> wn[DEPTH][4];      // 16 ranks
+        // Each workgroup starts at another place of the columns: rows a power of
+        // two apart would otherwise all be read from the same memory channels.
+        const int span = kAdWaves * 128, laps = (end + span - 1) / span;
+        const int begin = (int)(blockIdx.x % (unsigned)laps) * span + wave * 128;
+        auto strip = [&](int lap) {      // of a lap before 2 laps + 4, past the last one the end
+            const int k = begin + lap * span;
+            return lap >= laps ? end : k >= laps * span ? k - laps * span : k;
+        };
+        auto fetch = [&](int slot, int k0) {
+            if (k0 + 128 <= a.K)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    xn[slot][j] = Strip16<X>::load(x[j], (unsigned)(k0 + r16 * 8));
+        };
+        // 16 ranks of the adapter from its tile t on
+        auto ranks = [&](int t) {
+            return (const char *)a.down + ((long long)max(g, 0) * a.r + min(i0 + t * 16, max(a.r - 16, 0))) * a.K
+                   * (long long)sizeof(typename A::raw);
+        };
+        auto fetch_w = [&](int slot, int t, int k0) {
             if (k0 + 128 <= a.K) {
+                const char *w = ranks(t);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    xn[j] = strip_load<X, true>(x[j], 0, c, a.K);
-            } else if (k0 < end) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    xn[j] = strip_load<X, false>(x[j], 0, c, a.K);
+                    wn[slot][j] = Strip16<A>::load(w + woff[j], (unsigned)(k0 + r16 * 8));
             }
         };
-        auto fetch_w = [&](int t, int k0) {
-            const int c = k0 + r16 * 8, row = min(i0 + t * 16, max(a.r - 16, 0));
-            const char *w =
-                (const char *)a.down + ((long long)max(g, 0) * a.r + row) * a.K * (long long)sizeof(typename A::raw);
-            if (k0 + 128 <= a.K) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    wn[j] = strip_load<A, true>(w, woff[j], c, a.K);
-            } else if (k0 < end) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    wn[j] = strip_load<A, false>(w, woff[j], c, a.K);
-            }
-        };
-        fetch(wave * 128);
-        fetch_w(0, wave * 128);
-        for (int k0 = wave * 128; k0 < end; k0 += kAdWaves * 128) {
-            const int c = k0 + r16 * 8;
+        // step `lap` of the wave, in slot U of DEPTH
+        auto step = [&](auto slot, int lap) {
+            constexpr int U = decltype(slot)::value;
+            const int k0 = strip(lap), c = k0 + r16 * 8;
+            const bool inside = k0 + 128 <= a.K, some = k0 < end;
             Raw8<X> xr[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                xr[j] = xn[j];
-            Strip16<X>::put(xs, lane, xr);
-            fetch(k0 + kAdWaves * 128);
-            if (first && (a.codes || a.codes8)) {
+                xr[j] = xn[U][j];
+            if (inside) {
+                Strip16<X>::put(xs, lane, xr);
+            } else if (some) {
+                Strip16<X>::fill(xs, lane, (const char *)a.x + (long long)m * a.ldx * (long long)sizeof(typename X::raw), k0,
+                                 a.K);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    xr[j] = Strip16<X>::own(xs, lane, j);
+            }
+            fetch(U, strip(lap + DEPTH));
+            // (all four rows of a lane side by side: one after another, each
+            // step waits for the one before; 8192 x 8192 48 us)
+            if (some && first && (a.codes || a.codes8))
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int p = m0 + 4 * j + q;
+                    const int p = m0 + 4 * j + q, row = xrow[j];
                     const bool on = p < a.M;
                     float v[8];
                     unpack8<X>(xr[j], v);
@@ -214,8 +279,7 @@ __global__ __launch_bounds__(kAdWaves * 64) void ad_shrink_tile(AdShrinkArgs a)
                     if (a.codes) {
                         const unsigned byte = mx_scale_byte(top);
                         if (on && c < kb * 32)
-                            *(unsigned *)(a.codes + ((long long)(m0 + 4 * j) * (kb * 16) + (unsigned)(q * (kb * 16) + c / 2))) =
-                                mx_encode8(v, mx_scale_value(byte));
+                            *(unsigned *)(a.codes + ((long long)p * (kb * 16) + c / 2)) = mx_encode8(v, mx_scale_value(byte));
                         const unsigned word = mx_scale_word<16>(byte, c >> 5);
                         if (on && r16 == 0)
                             ((unsigned *)a.scales)[(long long)(k0 >> 7) * a.M + p] = word;
@@ -223,30 +287,60 @@ __global__ __launch_bounds__(kAdWaves * 64) void ad_shrink_tile(AdShrinkArgs a)
                     if (a.codes8) {
                         const unsigned byte = mxi_scale_byte(top);
                         if (on && c < kb * 32)
-                            *(uint2 *)(a.codes8 + ((long long)xrow[j] * (kb * 32) + c)) = mxi_encode8(v, byte);
+                            *(uint2 *)(a.codes8 + ((long long)row * (kb * 32) + c)) = mxi_encode8(v, byte);
                         const unsigned word = mx_scale_word<16>(c < kb * 32 ? byte : 0u, c >> 5);
                         if (on && r16 == 0)
-                            ((unsigned *)a.scales8)[(long long)xrow[j] * quads + (k0 >> 7)] = word;
+                            ((unsigned *)a.scales8)[(long long)row * quads + (k0 >> 7)] = word;
                     }
                 }
-            }
             if (g < 0)
-                continue;
-            u32v4_t xf[4][split_terms<X>()];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                split_raw8<X>(Strip16<X>::get(xs, lane, j), xf[j]);
-#pragma unroll
-            for (int t = 0; t < RT; ++t) {
-                Strip16<A>::put(ws, lane, wn);
-                fetch_w(t + 1 < RT ? t + 1 : 0, t + 1 < RT ? k0 : k0 + kAdWaves * 128);
+                return;
+            u32v4_t xf[4][HALVES ? 1 : split_terms<X>()];
+            if (some)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    u32v4_t wf[split_terms<A>()];
-                    split_raw8<A>(Strip16<A>::get(ws, lane, j), wf);
-                    acc[t] = mfma_terms16(wf, xf[j], acc[t]);
+                    const Raw8<X> r = Strip16<X>::get(xs, lane, j);
+                    if constexpr (HALVES)
+                        xf[j][0] = r.w[0];
+                    else
+                        split_raw8<X>(r, xf[j]);
                 }
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+                const int at = (RT == 1 ? U : t) % DEPTH;      // (known when compiled)
+                if (inside)
+                    Strip16<A>::put(ws, lane, wn[at]);
+                else if (some)
+                    Strip16<A>::fill(ws, lane,
+                                     ranks(t) + (long long)min(r16, a.r - 1) * a.K * (long long)sizeof(typename A::raw), k0,
+                                     a.K);
+                fetch_w(at, (t + DEPTH) % RT, strip(lap + (t + DEPTH) / RT));
+                if (some)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const Raw8<A> r = Strip16<A>::get(ws, lane, j);
+                        if constexpr (HALVES) {
+                            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, r.w[0]),
+                                                                            __builtin_bit_cast(f16x8_t, xf[j][0]), acc[t], 0,
+                                                                            0, 0);
+                        } else {
+                            u32v4_t wf[split_terms<A>()];
+                            split_raw8<A>(r, wf);
+                            acc[t] = mfma_terms16(wf, xf[j], acc[t]);
+                        }
+                    }
             }
+        };
+#pragma unroll
+        for (int u = 0; u < DEPTH; ++u)
+            fetch(u, strip(u));
+#pragma unroll
+        for (int u = 0; u < DEPTH; ++u)
+            fetch_w(u, u % RT, strip(u / RT));
+        for (int lap = 0; lap < laps; lap += DEPTH) {
+            step(std::integral_constant<int, 0>{}, lap);
+            if constexpr (DEPTH == 2)
+                step(std::integral_constant<int, 1>{}, lap + 1);
         }
         first = false;
         if (g < 0)
@@ -262,16 +356,16 @@ __global__ __launch_bounds__(kAdWaves * 64) void ad_shrink_tile(AdShrinkArgs a)
 #pragma unroll
             for (int w = 1; w < kAdWaves; ++w)
                 s += sums[w][wave][lane];
+            const float scale = a.scale[g];
             const int want = i0 + wave * 16, row = min(want, max(a.r - 16, 0));
             if (id == g)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int i = row + q * 4 + e;
-                    if (i >= want && i < a.r) {
-                        a.h[(long long)at * a.r + i] = s[e];
-                        if (a.kept)
-                            a.kept[(long long)m * a.r + i] = s[e];
-                    }
+                    const int i = row + q * 4 + e, past = want + q * 4 + e;
+                    if (past >= a.r && past < rp)
+                        adapter_put(a, at, m, past, 0.f, 0.f);
+                    if (i >= want && i < a.r)
+                        adapter_put(a, at, m, i, s[e], scale);
                 }
         }
         __syncthreads();
@@ -281,33 +375,64 @@ __global__ __launch_bounds__(kAdWaves * 64) void ad_shrink_tile(AdShrinkArgs a)
 // ---- the rows sorted by adapter --------------------------------------------
 //
 // By one workgroup, eight bits of the adapter's number at a time (once for up
-// to 255 adapters), stably: each wave counts the digits of its run of rows, the
+// to 255 adapters), stably, 512 rows of a wave in flight: each wave counts the digits of its run of rows, the
 // counts become places, and a row's place is its wave's next one for the digit
 // plus the number of equal digits in lower lanes.
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 
 __global__ __launch_bounds__(kSortThreads) void ad_sort(const int *ids, int M, int G, int bits, int *order, int *temp,
-                                                        int *start)
+                                                        int *key, int *start)
 {
+    constexpr int U = 8;      // chunks of 64 rows in flight
     __shared__ int place[256][kSortWaves];
     __shared__ int waves[kSortWaves];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int run = (int)((M + kSortWaves * 64LL - 1) / (kSortWaves * 64)) * 64;
-    const long long lo = (long long)wave * run;
-    const int hi = (int)min((long long)M, lo + run);
-    auto key_of = [&](int row) {
-        const int k = ids[row];
-        return k < 0 || k > G ? G : k;
-    };
+    const long long lo = (long long)wave * run, hi = min((long long)M, lo + run);
     // (the last pass writes `order`)
     int *out = (bits + 7) / 8 % 2 ? order : temp;
     const int *in = nullptr;
+    int row[U], kk[U];
+    auto load = [&](long long p0) {      // rows and keys of U chunks, -1 past the run
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const long long p = p0 + u * 64 + lane;
+            row[u] = p < hi ? (in ? in[p] : (int)p) : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = row[u] >= 0 ? ids[row[u]] : 0;
+            kk[u] = k < 0 || k > G ? G : k;
+        }
+    };
+    // the lanes with the same digit
+    auto matching = [&](bool on, unsigned digit, int n) {
+        unsigned long long same = __ballot(on);
+        for (int b = 0; b < n; ++b) {
+            const unsigned long long set = __ballot(digit >> b & 1);
+            same &= digit >> b & 1 ? set : ~set;
+        }
+        return same;
+    };
     for (int shift = 0; shift < bits; shift += 8) {
+        auto digit_of = [&](int u) { return row[u] >= 0 ? (unsigned)kk[u] >> shift & 255 : 0u; };
+        if (lo < hi)
+            load(lo);
         for (int k = threadIdx.x; k < 256 * kSortWaves; k += kSortThreads)
             (&place[0][0])[k] = 0;
         __syncthreads();
-        for (long long p = lo + lane; p < hi; p += 64)
-            atomicAdd(&place[(key_of(in ? in[p] : (int)p) >> shift) & 255][wave], 1);
+        for (long long p0 = lo; p0 < hi; p0 += U * 64) {
+            if (p0 > lo)
+                load(p0);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (p0 + u * 64 >= hi)
+                    break;
+                const unsigned long long same = matching(row[u] >= 0, digit_of(u), min(bits - shift, 8));
+                if (row[u] >= 0 && lane == __builtin_ctzll(same))
+                    place[digit_of(u)][wave] += __builtin_popcountll(same);
+            }
+        }
         __syncthreads();
         // counts to places: thread t holds four waves of digit t / 4
         int *mine = &place[0][0] + threadIdx.x * 4, sum = mine[0] + mine[1] + mine[2] + mine[3], upto = sum;
@@ -332,23 +457,26 @@ __global__ __launch_bounds__(kSortThreads) void ad_sort(const int *ids, int M, i
             for (int g = threadIdx.x; g <= G; g += kSortThreads)
                 start[g] = place[g][0];
         __syncthreads();
-        for (long long p0 = lo; p0 < hi; p0 += 64) {
-            const long long p = p0 + lane;
-            const bool on = p < hi;
-            const int row = on ? (in ? in[p] : (int)p) : 0;
-            const unsigned digit = on ? (key_of(row) >> shift) & 255 : 0;
-            unsigned long long same = __ballot(on);
+        for (long long p0 = lo; p0 < hi; p0 += U * 64) {
+            if (run > U * 64)      // (else the rows are still there)
+                load(p0);
 #pragma unroll
-            for (int b = 0; b < 8; ++b) {
-                const unsigned long long set = __ballot(digit >> b & 1);
-                same &= digit >> b & 1 ? set : ~set;
-            }
-            const int rank = __builtin_amdgcn_mbcnt_hi((unsigned)(same >> 32), __builtin_amdgcn_mbcnt_lo((unsigned)same, 0));
-            if (on) {
-                const int at = place[digit][wave];
-                out[at + rank] = row;
-                if (rank == 0)
-                    place[digit][wave] = at + __builtin_popcountll(same);
+            for (int u = 0; u < U; ++u) {
+                if (p0 + u * 64 >= hi)
+                    break;
+                const bool on = row[u] >= 0;
+                const unsigned digit = digit_of(u);
+                const unsigned long long same = matching(on, digit, min(bits - shift, 8));
+                const int rank =
+                    __builtin_amdgcn_mbcnt_hi((unsigned)(same >> 32), __builtin_amdgcn_mbcnt_lo((unsigned)same, 0));
+                if (on) {
+                    const int at = place[digit][wave];
+                    out[at + rank] = row[u];
+                    if (shift + 8 >= bits)
+                        key[at + rank] = kk[u] < G ? kk[u] : -1;
+                    if (rank == 0)
+                        place[digit][wave] = at + __builtin_popcountll(same);
+                }
             }
         }
         __threadfence_block();
@@ -360,8 +488,8 @@ __global__ __launch_bounds__(kSortThreads) void ad_sort(const int *ids, int M, i
         for (int g = threadIdx.x; g <= G; g += kSortThreads) {
             int a = 0, b = M;      // the first place whose adapter is at least g
             while (a < b) {
-                const int mid = a + (b - a) / 2;
-                if (key_of(order[mid]) < g)
+                const int mid = a + (b - a) / 2, k = key[mid];
+                if ((k < 0 ? G : k) < g)
                     a = mid + 1;
                 else
                     b = mid;
@@ -370,22 +498,21 @@ __global__ __launch_bounds__(kSortThreads) void ad_sort(const int *ids, int M, i
         }
 }
 
-void adapter_sort(const int *ids, int M, int G, int *order, int *start, hipStream_t stream)
+void adapter_sort(const int *ids, int M, int G, int *order, int *key, int *start, hipStream_t stream)
 {
     int bits = 1;
     while (bits < 32 && (unsigned)G >> bits)
         ++bits;
-    hipLaunchKernelGGL(ad_sort, dim3(1), dim3(kSortThreads), 0, stream, ids, M, G, bits, order, order + M, start);
+    hipLaunchKernelGGL(ad_sort, dim3(1), dim3(kSortThreads), 0, stream, ids, M, G, bits, order, order + M, key, start);
 }
 
 // A row a workgroup for up to 64 rows, and for up to 1024 where the adapters
 // may be so many that the rows hardly share any.
-AdPlan adapter_plan(int M, int K, int G, bool keep)
+AdPlan adapter_plan(int M, int G)
 {
     AdPlan p;
-    p.few = !keep && (M <= 64 || (M <= 1024 && M < 8LL * G));
+    p.few = M <= 64 || (M <= 1024 && M < 8LL * G);
     p.sorted = !p.few && G > 1;
-    p.splits = p.few ? (K + kAdFewCols - 1) / kAdFewCols : 1;
     return p;
 }
 
@@ -396,17 +523,31 @@ void adapter_shrink(const AdShrinkArgs &a, const AdPlan &plan, int x_dtype, int 
             typedef decltype(x) X;
             typedef decltype(w) A;
             if (plan.few) {
-                hipLaunchKernelGGL((ad_shrink_few<X, A>), dim3(plan.splits, a.M), dim3(kAdFewThreads), 0, stream, a);
+                const int rp = adapter_ranks(a.r);
+                if (a.M * (long long)rp < 1024)      // (few workgroups: fewer ranks each)
+                    hipLaunchKernelGGL((ad_shrink_few<X, A, 4>), dim3(a.M, rp / 4), dim3(kAdFewWaves * 64), 0, stream, a);
+                else {
+                    constexpr int RC = std::is_same<A, Fp32>::value ? 8 : 16;      // (what the registers hold)
+                    hipLaunchKernelGGL((ad_shrink_few<X, A, RC>), dim3(a.M, rp / RC), dim3(kAdFewWaves * 64), 0, stream, a);
+                }
                 return;
             }
             const unsigned tiles = (unsigned)((a.M + 15LL) / 16);
-            if (a.r <= 16)
-                hipLaunchKernelGGL((ad_shrink_tile<X, A, 1>), dim3(tiles), dim3(kAdWaves * 64), 0, stream, a);
-            else if (a.r <= 32)
-                hipLaunchKernelGGL((ad_shrink_tile<X, A, 2>), dim3(tiles), dim3(kAdWaves * 64), 0, stream, a);
+            // (fewer ranks a workgroup where there are few of them: x is then read
+            // by several; two workgroups a tile where the rows may have several
+            // adapters, of which most tiles' second has nothing to do)
+            const unsigned z = a.G > 1 ? 2 : 1;
+            auto launch = [&](auto rt) {
+                constexpr int RT = decltype(rt)::value;
+                hipLaunchKernelGGL((ad_shrink_tile<X, A, RT>), dim3(tiles, (a.r + 16 * RT - 1) / (16 * RT), z),
+                                   dim3(kAdWaves * 64), 0, stream, a);
+            };
+            if (a.r <= 16 || tiles <= 64)
+                launch(std::integral_constant<int, 1>{});
+            else if (a.r <= 32 || tiles <= 128)
+                launch(std::integral_constant<int, 2>{});
             else
-                hipLaunchKernelGGL((ad_shrink_tile<X, A, 4>), dim3(tiles, (a.r + 63) / 64), dim3(kAdWaves * 64), 0,
-                                   stream, a);
+                launch(std::integral_constant<int, 4>{});
         });
     });
 }

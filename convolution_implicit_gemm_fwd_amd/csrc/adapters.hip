@@ -11,7 +11,12 @@
 
 namespace convimg {
 
-// adapter_products_*.hip
+// adapter_grads_*.hip, by the type of dy
+void adapter_grads_bf16(const AdGradArgs &up, const AdGradArgs &down, int x_dtype, hipStream_t stream);
+void adapter_grads_fp16(const AdGradArgs &up, const AdGradArgs &down, int x_dtype, hipStream_t stream);
+void adapter_grads_fp32(const AdGradArgs &up, const AdGradArgs &down, int x_dtype, hipStream_t stream);
+
+// adapter_products_*.hip, by the type of the adapters
 void gemm_adapters_bf16(const MxGemmArgs &g, const MxAdapterArgs &ad, int out_dtype, hipStream_t stream);
 void few_adapters_bf16(const MxFewArgs &g, const MxAdapterArgs &ad, int x_dtype, int out_dtype, hipStream_t stream);
 void gemm_adapters_fp16(const MxGemmArgs &g, const MxAdapterArgs &ad, int out_dtype, hipStream_t stream);
@@ -48,27 +53,42 @@ int adapters_shape(int M, int N, int K, int adapters, int rank)
     return rc;
 }
 
-// Workspace of the forward call: x's packed rows, h's parts and the sorted
-// order; for a call that keeps something and one that does not.
+// Workspace of the forward call: x's packed rows, h, its terms and the sorted
+// order.
 struct AdFwdLayout {
-    size_t h, order, total;
+    size_t h, terms, order, total;
     AdPlan plan;
 };
 
-AdFwdLayout ad_fwd_layout(int M, int K, int G, int rank, bool keep)
+size_t ad_h_bytes(int M, int rank) { return align256((size_t)M * adapter_ranks(rank) * 4); }
+size_t ad_term_bytes(int M, int rank) { return align256((size_t)M * (adapter_ranks(rank) / 16) * kAdTermBytes); }
+
+AdFwdLayout ad_fwd_layout(int M, int K, int G, int rank)
 {
     AdFwdLayout l;
-    l.plan = adapter_plan(M, K, G, keep);
-    if (few_dense(M, K))      // (its product takes the rows as they come)
-        l.plan.sorted = false;
-    l.h = few_dense(M, K) ? 0 : packed_bytes(M, K);
-    l.order = l.h + align256((size_t)l.plan.splits * M * rank * 4);
-    l.total = l.order + (l.plan.sorted ? (size_t)M * 8 : 0);
+    const bool few = few_dense(M, K);      // (its product takes the rows as they are)
+    l.plan = adapter_plan(M, G);
+    l.h = few ? 0 : packed_bytes(M, K);
+    l.terms = l.h + ad_h_bytes(M, rank);
+    l.order = l.terms + (few ? 0 : ad_term_bytes(M, rank));
+    l.total = l.order + (l.plan.sorted ? (size_t)M * 12 : 0);
     return l;
 }
 
+int grad_tiles(int C) { return (int)((C + 127LL) / 128); }
+int grad_chunks_of_ranks(int r) { return r <= 16 ? 1 : r <= 32 ? 1 : (r + 63) / 64; }
+
+// Sorted rows a chunk of the gradients: as many chunks as give about 1024
+// workgroups, in runs of 32 rows.
+int adapter_grad_per(int M, int C, int r)
+{
+    const long long tiles = (long long)grad_tiles(C) * grad_chunks_of_ranks(r), chunks = tiles < 1024 ? 1024 / tiles : 1,
+                    per = (M + chunks - 1) / chunks;
+    return (int)((per + 31) / 32 * 32 < 32 ? 32 : (per + 31) / 32 * 32);
+}
+
 struct AdBwdLayout {
-    size_t dy, t, part_down, part_up, order, start, total;
+    size_t dy, t, terms, part_down, part_up, order, start, total;
     int per_down, per_up;
 };
 
@@ -86,10 +106,11 @@ AdBwdLayout ad_bwd_layout(int M, int N, int K, int G, int rank)
     l.per_down = adapter_grad_per(M, K, rank);
     l.per_up = adapter_grad_per(M, N, rank);
     l.dy = take(packed_bytes(M, N));
-    l.t = take((size_t)M * rank * 4);
+    l.t = take(ad_h_bytes(M, rank));
+    l.terms = take(ad_term_bytes(M, rank));
     l.part_down = take((size_t)ad_chunks(M, l.per_down) * 2 * rank * K * 4);
     l.part_up = take((size_t)ad_chunks(M, l.per_up) * 2 * rank * N * 4);
-    l.order = take((size_t)M * 8);
+    l.order = take((size_t)M * 12);
     l.start = take(((size_t)G + 1) * 4);
     l.total = at;
     return l;
@@ -116,8 +137,7 @@ int mxfp4_linear_adapters_workspace(int M, int N, int K, int adapters, int rank,
         return rc;
     if (!dtype_ok(x_dtype))
         return CONVIMG_ERR_DTYPE;
-    const size_t a = ad_fwd_layout(M, K, adapters, rank, false).total, b = ad_fwd_layout(M, K, adapters, rank, true).total;
-    *bytes = a > b ? a : b;
+    *bytes = ad_fwd_layout(M, K, adapters, rank).total;
     return CONVIMG_OK;
 }
 
@@ -151,19 +171,19 @@ int mxfp4_linear_adapters_fwd(const void *x, long long ldx, int x_dtype, const v
                             mxi_scale_bytes(M, K), need};
     if (any_overlap(outs, nout, 5, in, nin, 8))
         return CONVIMG_ERR_ALIAS;
-    // (what is kept has to be whole, not in parts)
-    const AdFwdLayout l = ad_fwd_layout(M, K, adapters, rank, h || x_codes);
+    const AdFwdLayout l = ad_fwd_layout(M, K, adapters, rank);
     unsigned char *base = (unsigned char *)ws, *codes = l.h ? base : nullptr,
-                  *scales = codes ? codes + align256(mx_code_bytes(M, K)) : nullptr;
+                  *scales = codes ? codes + align256(mx_code_bytes(M, K)) : nullptr,
+                  *terms = codes ? base + l.terms : nullptr;
     int *order = l.plan.sorted ? (int *)(base + l.order) : nullptr;
-    // (h in the rows' own order needs no copy of its own)
-    float *hh = h && !order ? h : (float *)(base + l.h);
+    const int *key = order ? order + 2LL * M : ids;
+    float *hh = (float *)(base + l.h);
     if (order)
-        adapter_sort(ids, M, adapters, order, nullptr, stream);
-    const AdShrinkArgs s = {x,      down, ids, order, hh, order ? h : nullptr, codes, scales, (unsigned char *)x_codes,
+        adapter_sort(ids, M, adapters, order, order + 2LL * M, nullptr, stream);
+    const AdShrinkArgs s = {x,     down,   scale, key, order, hh, terms, h, codes, scales, (unsigned char *)x_codes,
                             (unsigned char *)x_scales, ldx, M, K, adapters, rank};
     adapter_shrink(s, l.plan, x_dtype, a_dtype, stream);
-    const MxAdapterArgs ad = {hh, up, scale, ids, order, adapters, rank, l.plan.splits, a_dtype};
+    const MxAdapterArgs ad = {terms, hh, up, scale, key, order, adapters, rank, a_dtype};
     const MxOperand b = {(const unsigned char *)w_codes, (const unsigned char *)w_scales};
     if (!codes)
         few_adapters({x, b.codes, b.scales, bias, out, ldx, M, N, K, mx_blocks(K)}, ad, x_dtype, out_dtype, stream);
@@ -222,23 +242,26 @@ int mxfp4_linear_adapters_bwd(const void *dy, long long lddy, int dy_dtype, cons
     }
     unsigned char *base = (unsigned char *)ws, *codes = base + l.dy, *scales = codes + align256(mx_code_bytes(M, N));
     float *t = (float *)(base + l.t);
-    int *order = (int *)(base + l.order), *start = (int *)(base + l.start);
-    adapter_sort(ids, M, adapters, order, start, stream);
-    const AdShrinkArgs s = {dy, up, ids, order, t, nullptr, dx ? codes : nullptr, scales, nullptr, nullptr, lddy, M, N,
-                            adapters, rank};
-    adapter_shrink(s, {false, true, 1}, dy_dtype, a_dtype, stream);
+    int *order = (int *)(base + l.order), *key = order + 2LL * M, *start = (int *)(base + l.start);
+    adapter_sort(ids, M, adapters, order, key, start, stream);
+    unsigned char *terms = dx ? base + l.terms : nullptr;
+    const AdShrinkArgs s = {dy, up, scale, key, order, t, terms, nullptr, dx ? codes : nullptr, scales, nullptr, nullptr,
+                            lddy, M, N, adapters, rank};
+    adapter_shrink(s, {false, true}, dy_dtype, a_dtype, stream);
     if (dx) {
-        const MxAdapterArgs ad = {t, down, scale, ids, order, adapters, rank, 1, a_dtype};
+        const MxAdapterArgs ad = {terms, t, down, scale, key, order, adapters, rank, a_dtype};
         gemm_adapters(gemm_args({codes, scales}, {(const unsigned char *)wt_codes, (const unsigned char *)wt_scales},
                                 nullptr, M, K, N, dx),
                       ad, dx_dtype, stream);
     }
-    adapter_grad({h, dy, nullptr, ids, order, start, scale, dup, (float *)(base + l.part_up), lddy, M, N, adapters, rank, 0,
-                  l.per_up, ad_chunks(M, l.per_up)},
-                 dy_dtype, stream);
-    adapter_grad({t, x, (const unsigned char *)x_scales, ids, order, start, scale, ddown, (float *)(base + l.part_down),
-                  ldx, M, K, adapters, rank, 1, l.per_down, ad_chunks(M, l.per_down)},
-                 x_dtype, stream);
+    const int rt = grad_chunks_of_ranks(rank);
+    const AdGradArgs up_args = {h,   dy,   nullptr, order, key, start, scale, dup, (float *)(base + l.part_up), lddy, M, N,
+                                adapters, rank, 0, rank, l.per_up, ad_chunks(M, l.per_up), grad_tiles(N), rt},
+                     down_args = {t, x, (const unsigned char *)x_scales, order, key, start, scale, ddown,
+                                  (float *)(base + l.part_down), ldx, M, K, adapters, rank, 1, adapter_ranks(rank),
+                                  l.per_down, ad_chunks(M, l.per_down), grad_tiles(K), rt};
+    auto grads = dy_dtype == CONVIMG_BF16 ? adapter_grads_bf16 : dy_dtype == CONVIMG_FP16 ? adapter_grads_fp16 : adapter_grads_fp32;
+    grads(up_args, down_args, x_dtype, stream);
     return launched();
 }
 

@@ -109,8 +109,7 @@ __global__ __launch_bounds__(kMxFewWaves * 64) void mx_gemm_few(MxFewArgs g, AD 
 #pragma unroll
         for (int m = 0; m < kMxFewM; ++m)
             if (m < g.M && (int)(threadIdx.x >> 4) < ad.r)
-                for (int k = 0; k < ad.splits; ++k)
-                    h0[m] += ad.h[((long long)k * g.M + m) * ad.r + (threadIdx.x >> 4)];
+                h0[m] = ad.h[(long long)m * adapter_ranks(ad.r) + (threadIdx.x >> 4)];
 #pragma unroll
     for (int u = 0; u < kMxFewRing; ++u)
         fetch(u * waves + wave, u);
@@ -119,17 +118,12 @@ __global__ __launch_bounds__(kMxFewWaves * 64) void mx_gemm_few(MxFewArgs g, AD 
         typedef typename AD::type T;
 #pragma unroll
         for (int m = 0; m < kMxFewM; ++m) {
-            const int id = m < g.M ? ad.ids[m] : -1;
+            const int id = m < g.M ? ad.key[m] : -1;
             if (id < 0 || id >= ad.G || n >= g.N)
                 continue;
             const typename T::raw *up = (const typename T::raw *)ad.up + (long long)id * ad.r * g.N + n;
             for (int i = first; i < ad.r; i += step) {
-                float h = h0[m];
-                if (i != first) {
-                    h = 0.f;
-                    for (int k = 0; k < ad.splits; ++k)
-                        h += ad.h[((long long)k * g.M + m) * ad.r + i];
-                }
+                const float h = i == first ? h0[m] : ad.h[(long long)m * adapter_ranks(ad.r) + i];
                 low[m] = __builtin_fmaf(h, load1<T>(up + (long long)i * g.N), low[m]);
             }
             low[m] *= ad.scale[id];
