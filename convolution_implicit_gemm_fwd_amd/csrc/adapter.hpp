@@ -11,7 +11,7 @@ struct AdShrinkArgs {
     const void *down;                   // [G][r][K]
     const float *scale;                 // [G]
     const int *key;                     // [M]: the adapter at each place of h and codes
-    const int *order;                   // [M]: the row at each place, or NULL for their own order
+    const int *order, *start;           // adapter_sort: [M], the row at each place; NULL for their own order
     float *h;                           // [M][adapter_ranks(r)]
     unsigned char *terms;               // h for the products (MxAdapterArgs), or NULL
     float *kept;                        // [M][r]: h in the rows' own order, too, or NULL
@@ -32,7 +32,7 @@ void adapter_shrink(const AdShrinkArgs &a, const AdPlan &plan, int x_dtype, int 
 // The rows sorted by adapter, those without one last, rows of one adapter by
 // their numbers: order [M] (and as much again behind it), key [M], the adapter
 // at each place or -1, and start [G + 1], the first place of each adapter and of
-// the rows without, or NULL.
+// the rows without.
 void adapter_sort(const int *ids, int M, int G, int *order, int *key, int *start, hipStream_t stream);
 
 // One operand of the gradients: out[g][i][c] = scale_g * sum over the rows m

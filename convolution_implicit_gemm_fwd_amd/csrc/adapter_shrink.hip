@@ -101,8 +101,6 @@ __global__ __launch_bounds__(kAdFewWaves * 64) void ad_shrink_few(AdShrinkArgs a
 // it.  They reach the matrix instruction's form (a lane eight columns of row
 // lane % 16) through LDS that is the wave's own.  (Loading them in that form
 // straight away puts neighbouring lanes on different rows: 8192 x 8192 71 us.)
-// Where the 16 rows have several adapters, at the sorted runs' ends, x is read
-// again (from cache) for each.
 constexpr int kAdWaves = 8;
 
 // 16 rows of 128 columns of a wave, in LDS.
@@ -177,42 +175,48 @@ __global__ __launch_bounds__(kAdWaves * 64) void ad_shrink_tile(AdShrinkArgs a)
     __shared__ __attribute__((aligned(16))) unsigned char lds[LDS > SUMS ? LDS : SUMS];
     const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int m0 = blockIdx.x * 16, i0 = blockIdx.y * 16 * RT;
+    const int i0 = blockIdx.y * 16 * RT, rp = adapter_ranks(a.r);
     const int kb = mx_blocks(a.K), quads = (a.K + 127) / 128, end = quads * 128;
     unsigned char *const xs = lds + wave * Strip16<X>::BYTES,
                   *const ws = lds + kAdWaves * Strip16<X>::BYTES + wave * Strip16<A>::BYTES;
     f32x4_t(*sums)[RT][64] = (f32x4_t(*)[RT][64])lds;
-
-    // row r16 and the rows 4 j + q, the last one again past the end
-    const bool real = m0 + r16 < a.M;
-    const int at = min(m0 + r16, a.M - 1), m = a.order ? a.order[at] : at, rp = adapter_ranks(a.r);
-    const int given = real ? a.key[at] : -1, id = given < a.G ? given : -1;
-    unsigned left = (unsigned)__ballot(id >= 0) & 0xffffu;
-    const char *x[4];
-    int xrow[4];
     unsigned woff[4];      // rank 4 j + q of a tile of ranks; a tile that would pass the rank ends with it
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        xrow[j] = __shfl(m, 4 * j + q);
-        x[j] = (const char *)a.x + (long long)xrow[j] * a.ldx * (long long)sizeof(typename X::raw);
+    for (int j = 0; j < 4; ++j)
         woff[j] = (unsigned)min(4 * j + q, a.r - 1) * (unsigned)a.K * (unsigned)sizeof(typename A::raw);
-    }
-    if (real && id < 0 && blockIdx.z == 0)      // no adapter: 0
-        for (int i = i0 + (threadIdx.x >> 4); i < min(rp, i0 + 16 * RT); i += kAdWaves * 4)
-            adapter_put(a, at, m, i, 0.f, 0.f);
 
-    // Pass by pass; of the workgroups that share the tile the first takes the
-    // first pass and the quantisation, the second the second pass, and so on.
-    bool first = blockIdx.y == 0 && blockIdx.z == 0;
-    unsigned pass = 0;
-    do {
-        int g = -1;
-        if (left) {
-            g = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
-            left &= ~(unsigned)__ballot(id == g);
+    // A tile's own workgroup quantises its rows and takes the adapter that they
+    // begin with (or have, unsorted); of an adapter that begins inside a tile one
+    // of the workgroups behind the tiles' takes care.
+    const int tiles = (int)((a.M + 15LL) / 16);
+    const bool own = (int)blockIdx.x < tiles;
+    for (int turn = (int)blockIdx.x - tiles; own || turn < a.G; turn += (int)gridDim.x - tiles) {
+        int m0 = (int)blockIdx.x * 16;
+        if (!own) {
+            const int s = a.start[turn];
+            if (s == a.start[turn + 1] || (s & 15) == 0)
+                continue;
+            m0 = s & ~15;
         }
-        if (pass++ % gridDim.z != blockIdx.z || (!first && g < 0))
-            continue;
+        // row r16 and the rows 4 j + q, the last one again past the end
+        const bool real = m0 + r16 < a.M;
+        const int at = min(m0 + r16, a.M - 1), m = a.order ? a.order[at] : at;
+        const int given = real ? a.key[at] : -1, id = given < a.G ? given : -1;
+        const unsigned have = (unsigned)__ballot(id >= 0) & 0xffffu;
+        const int g = own ? (have ? __builtin_amdgcn_readlane(id, __builtin_ctz(have)) : -1) : turn;
+        const char *x[4];
+        int xrow[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            xrow[j] = __shfl(m, 4 * j + q);
+            x[j] = (const char *)a.x + (long long)xrow[j] * a.ldx * (long long)sizeof(typename X::raw);
+        }
+        if (own && real && id < 0)      // no adapter: 0
+            for (int i = i0 + (threadIdx.x >> 4); i < min(rp, i0 + 16 * RT); i += kAdWaves * 4)
+                adapter_put(a, at, m, i, 0.f, 0.f);
+        const bool quantise = own && blockIdx.y == 0 && (a.codes || a.codes8);
+        if (g < 0 && !quantise)
+            return;
         f32x4_t acc[RT] = {};
         Raw8<X> xn[DEPTH][4];      // the steps in flight
         Raw8<A> wn[DEPTH][4];      // 16 ranks
@@ -264,7 +268,7 @@ __global__ __launch_bounds__(kAdWaves * 64) void ad_shrink_tile(AdShrinkArgs a)
             fetch(U, strip(lap + DEPTH));
             // (all four rows of a lane side by side: one after another, each
             // step waits for the one before; 8192 x 8192 48 us)
-            if (some && first && (a.codes || a.codes8))
+            if (some && quantise)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int p = m0 + 4 * j + q, row = xrow[j];
@@ -342,9 +346,8 @@ __global__ __launch_bounds__(kAdWaves * 64) void ad_shrink_tile(AdShrinkArgs a)
             if constexpr (DEPTH == 2)
                 step(std::integral_constant<int, 1>{}, lap + 1);
         }
-        first = false;
         if (g < 0)
-            break;
+            return;
         // the waves' sums in order; a lane holds ranks 4 q .. 4 q + 3 of row r16
         __syncthreads();
 #pragma unroll
@@ -368,8 +371,10 @@ __global__ __launch_bounds__(kAdWaves * 64) void ad_shrink_tile(AdShrinkArgs a)
                         adapter_put(a, at, m, i, s[e], scale);
                 }
         }
+        if (own)
+            return;
         __syncthreads();
-    } while (left);
+    }
 }
 
 // ---- the rows sorted by adapter --------------------------------------------
@@ -534,12 +539,11 @@ void adapter_shrink(const AdShrinkArgs &a, const AdPlan &plan, int x_dtype, int 
             }
             const unsigned tiles = (unsigned)((a.M + 15LL) / 16);
             // (fewer ranks a workgroup where there are few of them: x is then read
-            // by several; two workgroups a tile where the rows may have several
-            // adapters, of which most tiles' second has nothing to do)
-            const unsigned z = a.G > 1 ? 2 : 1;
+            // by several)
+            const unsigned more = a.order ? (a.G < 256 ? a.G : 256) : 0;      // for adapters that begin inside a tile
             auto launch = [&](auto rt) {
                 constexpr int RT = decltype(rt)::value;
-                hipLaunchKernelGGL((ad_shrink_tile<X, A, RT>), dim3(tiles, (a.r + 16 * RT - 1) / (16 * RT), z),
+                hipLaunchKernelGGL((ad_shrink_tile<X, A, RT>), dim3(tiles + more, (a.r + 16 * RT - 1) / (16 * RT)),
                                    dim3(kAdWaves * 64), 0, stream, a);
             };
             if (a.r <= 16 || tiles <= 64)

@@ -71,7 +71,7 @@ AdFwdLayout ad_fwd_layout(int M, int K, int G, int rank)
     l.h = few ? 0 : packed_bytes(M, K);
     l.terms = l.h + ad_h_bytes(M, rank);
     l.order = l.terms + (few ? 0 : ad_term_bytes(M, rank));
-    l.total = l.order + (l.plan.sorted ? (size_t)M * 12 : 0);
+    l.total = l.order + (l.plan.sorted ? (size_t)M * 12 + ((size_t)G + 1) * 4 : 0);
     return l;
 }
 
@@ -177,10 +177,11 @@ int mxfp4_linear_adapters_fwd(const void *x, long long ldx, int x_dtype, const v
                   *terms = codes ? base + l.terms : nullptr;
     int *order = l.plan.sorted ? (int *)(base + l.order) : nullptr;
     const int *key = order ? order + 2LL * M : ids;
+    int *start = order ? order + 3LL * M : nullptr;
     float *hh = (float *)(base + l.h);
     if (order)
-        adapter_sort(ids, M, adapters, order, order + 2LL * M, nullptr, stream);
-    const AdShrinkArgs s = {x,     down,   scale, key, order, hh, terms, h, codes, scales, (unsigned char *)x_codes,
+        adapter_sort(ids, M, adapters, order, order + 2LL * M, start, stream);
+    const AdShrinkArgs s = {x, down, scale, key, order, start, hh, terms, h, codes, scales, (unsigned char *)x_codes,
                             (unsigned char *)x_scales, ldx, M, K, adapters, rank};
     adapter_shrink(s, l.plan, x_dtype, a_dtype, stream);
     const MxAdapterArgs ad = {terms, hh, up, scale, key, order, adapters, rank, a_dtype};
@@ -245,7 +246,7 @@ int mxfp4_linear_adapters_bwd(const void *dy, long long lddy, int dy_dtype, cons
     int *order = (int *)(base + l.order), *key = order + 2LL * M, *start = (int *)(base + l.start);
     adapter_sort(ids, M, adapters, order, key, start, stream);
     unsigned char *terms = dx ? base + l.terms : nullptr;
-    const AdShrinkArgs s = {dy, up, scale, key, order, t, terms, nullptr, dx ? codes : nullptr, scales, nullptr, nullptr,
+    const AdShrinkArgs s = {dy, up, scale, key, order, start, t, terms, nullptr, dx ? codes : nullptr, scales, nullptr, nullptr,
                             lddy, M, N, adapters, rank};
     adapter_shrink(s, {false, true}, dy_dtype, a_dtype, stream);
     if (dx) {
