@@ -40,6 +40,8 @@ constexpr int kMaxRank = 4096;
 
 // Columns of an adapter at most: 16 rows of it stay below 2^31 bytes.
 constexpr int kMaxAdapterCols = (1 << 25) - 1;
+// Rows: a launch with a workgroup of 512 threads for 16 of them holds fewer than 2^32 threads.
+constexpr int kMaxAdapterRows = (1 << 26) - 1;
 
 int adapters_shape(int M, int N, int K, int adapters, int rank)
 {
@@ -48,8 +50,8 @@ int adapters_shape(int M, int N, int K, int adapters, int rank)
         rc = N <= 0 ? CONVIMG_ERR_SHAPE : mx_shape(N, K);
     if (rc == CONVIMG_OK)
         rc = rank <= 0 || adapters <= 0 ? CONVIMG_ERR_SHAPE
-             : rank > kMaxRank || N > kMaxAdapterCols || K > kMaxAdapterCols ? CONVIMG_ERR_RANGE
-                                                                            : CONVIMG_OK;
+             : rank > kMaxRank || N > kMaxAdapterCols || K > kMaxAdapterCols || M > kMaxAdapterRows ? CONVIMG_ERR_RANGE
+                                                                                                   : CONVIMG_OK;
     return rc;
 }
 
@@ -119,7 +121,12 @@ AdBwdLayout ad_bwd_layout(int M, int N, int K, int G, int rank)
 int ad_bwd_shape(int M, int N, int K, int adapters, int rank)
 {
     const int rc = adapters_shape(M, K, N, adapters, rank);      // dy's rows and wt's
-    return rc != CONVIMG_OK ? rc : mx_shape(M, K);
+    if (rc != CONVIMG_OK)
+        return rc;
+    // (the gradients' launch: a workgroup of 256 threads for 128 columns and 64 ranks)
+    if (((long long)grad_tiles(N) + grad_tiles(K)) * grad_chunks_of_ranks(rank) > (1 << 22))
+        return CONVIMG_ERR_RANGE;
+    return mx_shape(M, K);
 }
 
 }  // namespace convimg

@@ -145,6 +145,14 @@ __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsign
     const int group = KG > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / (NW * 64)) : 0;
     unsigned char *const lds = smem;
     smem += group * (STAGES * STAGE);
+    // (adapters: whether another group of waves left infinities out, a word a wave behind the rest)
+    constexpr bool ADAPT = !__is_same(AD, MxNoAdapters);
+    [[maybe_unused]] volatile int *const flags = (int *)(lds + mx_gemm_lds<S, sizeof(typename O::raw)>());
+    if constexpr (ADAPT && KG > 1) {
+        if (group == 0 && lane == 0)
+            flags[wave] = 0;
+        mx_wait_lds();      // (before the loop's barriers, behind which the others write)
+    }
     const int wm = wave % WM, wn = wave / WM;
     const int half = lane >> 5, l32 = lane & 31;
     int tm, tn;
@@ -327,14 +335,19 @@ __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsign
     // Adapters, here and not while the first copies are under way: the loop's
     // registers are free again, of which the largest tile has none to spare.
     [[maybe_unused]] bool infinite = false;
-    if constexpr (!__is_same(AD, MxNoAdapters))
+    if constexpr (ADAPT) {
         infinite = adapter_expand<typename AD::type, FM, FN, KG>(ad, g.M, g.N, m0 + wm * TM, n0 + wn * TN, group, acc);
+        if (KG > 1 && group > 0 && infinite && lane == 0)
+            flags[wave] = 1;
+    }
 
     // Rows of the output through LDS, as many blocks of 32 a wave as it holds,
     // so that stores are 16 bytes a lane along the row.
     mx_wait_vm<0>();
     mx_wait_lds();
     mx_barrier();
+    if constexpr (ADAPT && KG > 1)
+        infinite |= flags[wave] != 0;
     if constexpr (KG > 1) {
         // [block of 16 values][group - 1][the group's thread]
         f32x4_t *sums = (f32x4_t *)lds;
@@ -374,7 +387,7 @@ __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsign
     for (int i0 = 0; i0 < FM; i0 += G) {
         // (adapters: row l32 of each block at its own place of the output)
         [[maybe_unused]] int place[G];
-        if constexpr (!__is_same(AD, MxNoAdapters))
+        if constexpr (ADAPT)
 #pragma unroll
             for (int i = 0; i < G; ++i)
                 place[i] = ad.row(min(m0 + wm * TM + (i0 + i) * 32 + l32, g.M - 1));
@@ -407,7 +420,7 @@ __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsign
             for (int p = 0; p < 32 / RP; ++p) {
                 const int r = p * RP + lane / CHUNKS;
                 long long row = m + r;
-                if constexpr (!__is_same(AD, MxNoAdapters))
+                if constexpr (ADAPT)
                     row = __shfl(place[i], r);
                 to[p] = (typename O::raw *)g.out + row * g.N + n;
             }
@@ -438,7 +451,7 @@ __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsign
             __builtin_amdgcn_wave_barrier();
         }
     }
-    if constexpr (!__is_same(AD, MxNoAdapters))
+    if constexpr (ADAPT)
         if (infinite) {
             mx_wait_vm<0>();
             adapter_infinite<typename AD::type, O>(ad, g.M, g.N, m0 + wm * TM, n0 + wn * TN, TM, TN, g.out);
@@ -457,7 +470,7 @@ __global__ __launch_bounds__(S::threads) void mx_gemm_tile(MxGemmArgs g)
 template <typename S, typename O, typename T>
 __global__ __launch_bounds__(S::threads) void mx_gemm_tile_adapters(MxGemmArgs g, MxAdapters<T> ad)
 {
-    __shared__ __attribute__((aligned(16))) unsigned char smem[mx_gemm_lds<S, sizeof(typename O::raw)>()];
+    __shared__ __attribute__((aligned(16))) unsigned char smem[mx_gemm_lds<S, sizeof(typename O::raw)>() + S::WM * S::WN * 4];
     const unsigned id = mx_xcd_tile(blockIdx.x, gridDim.x);
     if (id < (unsigned)g.tm * g.tn)
         mx_gemm_body<S, O>(g, id, smem, ad);

@@ -611,7 +611,10 @@ int mxfp4_linear_adapters_workspace(int M, int N, int K, int adapters, int rank,
  *   h         device, fp32 [M][rank]: what the forward call wrote
  *   dx        device, [M][K] in dx_dtype
  *   ddown, dup  device, fp32, [adapters][rank][K] and [adapters][rank][N]
- *   ws        at least mxfp4_linear_adapters_bwd_workspace bytes */
+ *   ws        at least mxfp4_linear_adapters_bwd_workspace bytes
+ *
+ * CONVIMG_ERR_RANGE also for more than 2^22 tiles of 128 columns (of N and of
+ * K) by 64 ranks. */
 int mxfp4_linear_adapters_bwd(const void *dy, long long lddy, int dy_dtype, const void *x, long long ldx,
                               const void *x_scales, int x_dtype, const void *wt_codes, const void *wt_scales,
                               const void *down, const void *up, const float *scale, const int *ids, int adapters,
