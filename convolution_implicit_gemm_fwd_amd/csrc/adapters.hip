@@ -80,11 +80,11 @@ AdFwdLayout ad_fwd_layout(int M, int K, int G, int rank)
 int grad_tiles(int C) { return (int)((C + 127LL) / 128); }
 int grad_chunks_of_ranks(int r) { return r <= 16 ? 1 : r <= 32 ? 1 : (r + 63) / 64; }
 
-// Sorted rows a chunk of the gradients: as many chunks as give about 1024
+// Sorted rows a chunk of the gradients: as many chunks as give about 512
 // workgroups, in runs of 32 rows.
 int adapter_grad_per(int M, int C, int r)
 {
-    const long long tiles = (long long)grad_tiles(C) * grad_chunks_of_ranks(r), chunks = tiles < 1024 ? 1024 / tiles : 1,
+    const long long tiles = (long long)grad_tiles(C) * grad_chunks_of_ranks(r), chunks = tiles < 512 ? 512 / tiles : 1,
                     per = (M + chunks - 1) / chunks;
     return (int)((per + 31) / 32 * 32 < 32 ? 32 : (per + 31) / 32 * 32);
 }
