@@ -100,7 +100,9 @@ __global__ __launch_bounds__(kAdFewWaves * 64) void ad_shrink_few(AdShrinkArgs a
 // row, the next step in flight; in that form four lanes hold a block and quantise
 // it.  They reach the matrix instruction's form (a lane eight columns of row
 // lane % 16) through LDS that is the wave's own.  (Loading them in that form
-// straight away puts neighbouring lanes on different rows: 8192 x 8192 71 us.)
+// straight away puts neighbouring lanes on different rows: 8192 x 8192 71 us
+// against 40.  Two steps in flight overflow the registers: 2011 x 4096 with 64
+// ranks 28 us against 19.)
 constexpr int kAdWaves = 8;
 
 // 16 rows of 128 columns of a wave, in LDS.
@@ -167,8 +169,6 @@ typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 template <typename X, typename A, int RT>
 __global__ __launch_bounds__(kAdWaves * 64) void ad_shrink_tile(AdShrinkArgs a)
 {
-    // steps of a wave in flight, and tiles of ranks; fp32 and 64 ranks fill the registers with one
-    constexpr int DEPTH = sizeof(typename X::raw) == 2 && sizeof(typename A::raw) == 2 && RT <= 2 ? 2 : 1;
     // (both fp16: their own instruction, which has the exact products, too)
     constexpr bool HALVES = __is_same(X, Fp16) && __is_same(A, Fp16);
     constexpr int LDS = kAdWaves * (Strip16<X>::BYTES + Strip16<A>::BYTES), SUMS = kAdWaves * RT * 64 * 16;
@@ -218,44 +218,44 @@ __global__ __launch_bounds__(kAdWaves * 64) void ad_shrink_tile(AdShrinkArgs a)
         if (g < 0 && !quantise)
             return;
         f32x4_t acc[RT] = {};
-        Raw8<X> xn[DEPTH][4];      // the steps in flight
-        Raw8<A> wn[DEPTH][4];      // 16 ranks
+        Raw8<X> xn[4];      // the next step's
+        Raw8<A> wn[4];      // the next 16 ranks'
         // Each workgroup starts at another place of the columns: rows a power of
         // two apart would otherwise all be read from the same memory channels.
         const int span = kAdWaves * 128, laps = (end + span - 1) / span;
         const int begin = (int)(blockIdx.x % (unsigned)laps) * span + wave * 128;
-        auto strip = [&](int lap) {      // of a lap before 2 laps + 4, past the last one the end
+        auto strip = [&](int lap) {      // past the last lap the end
             const int k = begin + lap * span;
             return lap >= laps ? end : k >= laps * span ? k - laps * span : k;
         };
-        auto fetch = [&](int slot, int k0) {
+        auto fetch = [&](int k0) {
             if (k0 + 128 <= a.K)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    xn[slot][j] = Strip16<X>::load(x[j], (unsigned)(k0 + r16 * 8));
+                    xn[j] = Strip16<X>::load(x[j], (unsigned)(k0 + r16 * 8));
         };
         // 16 ranks of the adapter from its tile t on
         auto ranks = [&](int t) {
             return (const char *)a.down + ((long long)max(g, 0) * a.r + min(i0 + t * 16, max(a.r - 16, 0))) * a.K
                    * (long long)sizeof(typename A::raw);
         };
-        auto fetch_w = [&](int slot, int t, int k0) {
+        auto fetch_w = [&](int t, int k0) {
             if (k0 + 128 <= a.K) {
                 const char *w = ranks(t);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    wn[slot][j] = Strip16<A>::load(w + woff[j], (unsigned)(k0 + r16 * 8));
+                    wn[j] = Strip16<A>::load(w + woff[j], (unsigned)(k0 + r16 * 8));
             }
         };
-        // step `lap` of the wave, in slot U of DEPTH
-        auto step = [&](auto slot, int lap) {
-            constexpr int U = decltype(slot)::value;
+        fetch(strip(0));
+        fetch_w(0, strip(0));
+        for (int lap = 0; lap < laps; ++lap) {
             const int k0 = strip(lap), c = k0 + r16 * 8;
             const bool inside = k0 + 128 <= a.K, some = k0 < end;
             Raw8<X> xr[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                xr[j] = xn[U][j];
+                xr[j] = xn[j];
             if (inside) {
                 Strip16<X>::put(xs, lane, xr);
             } else if (some) {
@@ -265,7 +265,7 @@ __global__ __launch_bounds__(kAdWaves * 64) void ad_shrink_tile(AdShrinkArgs a)
                 for (int j = 0; j < 4; ++j)
                     xr[j] = Strip16<X>::own(xs, lane, j);
             }
-            fetch(U, strip(lap + DEPTH));
+            fetch(strip(lap + 1));
             // (all four rows of a lane side by side: one after another, each
             // step waits for the one before; 8192 x 8192 48 us)
             if (some && quantise)
@@ -298,7 +298,7 @@ __global__ __launch_bounds__(kAdWaves * 64) void ad_shrink_tile(AdShrinkArgs a)
                     }
                 }
             if (g < 0)
-                return;
+                continue;
             u32v4_t xf[4][HALVES ? 1 : split_terms<X>()];
             if (some)
 #pragma unroll
@@ -311,14 +311,13 @@ __global__ __launch_bounds__(kAdWaves * 64) void ad_shrink_tile(AdShrinkArgs a)
                 }
 #pragma unroll
             for (int t = 0; t < RT; ++t) {
-                const int at = (RT == 1 ? U : t) % DEPTH;      // (known when compiled)
                 if (inside)
-                    Strip16<A>::put(ws, lane, wn[at]);
+                    Strip16<A>::put(ws, lane, wn);
                 else if (some)
                     Strip16<A>::fill(ws, lane,
                                      ranks(t) + (long long)min(r16, a.r - 1) * a.K * (long long)sizeof(typename A::raw), k0,
                                      a.K);
-                fetch_w(at, (t + DEPTH) % RT, strip(lap + (t + DEPTH) / RT));
+                fetch_w((t + 1) % RT, strip(lap + (t + 1) / RT));
                 if (some)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -334,17 +333,6 @@ __global__ __launch_bounds__(kAdWaves * 64) void ad_shrink_tile(AdShrinkArgs a)
                         }
                     }
             }
-        };
-#pragma unroll
-        for (int u = 0; u < DEPTH; ++u)
-            fetch(u, strip(u));
-#pragma unroll
-        for (int u = 0; u < DEPTH; ++u)
-            fetch_w(u, u % RT, strip(u / RT));
-        for (int lap = 0; lap < laps; lap += DEPTH) {
-            step(std::integral_constant<int, 0>{}, lap);
-            if constexpr (DEPTH == 2)
-                step(std::integral_constant<int, 1>{}, lap + 1);
         }
         if (g < 0)
             return;
