@@ -25,14 +25,19 @@ __device__ __forceinline__ void adapter_put(const AdShrinkArgs &a, int at, int r
 
 // ---- few rows --------------------------------------------------------------
 //
-// A workgroup takes RC ranks of one row, a thread eight of every 4096 columns,
-// with its part of every rank's row of the adapter in flight at once: a serving
+// A workgroup takes four ranks of one row, a thread eight of every 4096 columns,
+// with its part of each rank's row of the adapter in flight at once: a serving
 // batch mostly has another adapter in every row, whose 2 r K bytes are the work.
-constexpr int kAdFewWaves = 8;
+// The latency of one read bounds it: 3.1 us for one row of 4096 columns and 16
+// ranks, 3.4 for 64 rows with 64 adapters.  (16 ranks a workgroup read x fewer
+// times, but their sums across the wave take longer: 6.5 and 7.2 us, and 10
+// against 8.3 for 256 rows.)
+constexpr int kAdFewWaves = 8, kAdFewRanks = 4;
 
-template <typename X, typename A, int RC>
+template <typename X, typename A>
 __global__ __launch_bounds__(kAdFewWaves * 64) void ad_shrink_few(AdShrinkArgs a)
 {
+    constexpr int RC = kAdFewRanks;
     __shared__ float sums[kAdFewWaves][RC];
     const int m = blockIdx.x, i0 = blockIdx.y * RC, wave = threadIdx.x >> 6;
     const int id = a.key[m];
@@ -103,6 +108,11 @@ __global__ __launch_bounds__(kAdFewWaves * 64) void ad_shrink_few(AdShrinkArgs a
 // straight away puts neighbouring lanes on different rows: 8192 x 8192 71 us
 // against 40.  Two steps in flight overflow the registers: 2011 x 4096 with 64
 // ranks 28 us against 19.)
+//
+// 8192 x 8192 and 16 ranks, x from memory: 51 us, 134 MB read and 37 written, 3.4
+// TB/s (quantising alone 42 us there); 8192 x 4096 30 us.  Two workgroups a CU is
+// what the registers allow, and the steps wait for their loads: four waves a
+// SIMD spill and take twice as long.
 constexpr int kAdWaves = 8;
 
 // 16 rows of 128 columns of a wave, in LDS.
@@ -368,9 +378,13 @@ __global__ __launch_bounds__(kAdWaves * 64) void ad_shrink_tile(AdShrinkArgs a)
 // ---- the rows sorted by adapter --------------------------------------------
 //
 // By one workgroup, eight bits of the adapter's number at a time (once for up
-// to 255 adapters), stably, 512 rows of a wave in flight: each wave counts the digits of its run of rows, the
-// counts become places, and a row's place is its wave's next one for the digit
-// plus the number of equal digits in lower lanes.
+// to 255 adapters), stably, 512 rows of a wave in flight: each wave counts the
+// digits of its run of rows, the counts become places, and a row's place is its
+// wave's next one for the digit plus the number of equal digits in lower lanes.
+// Lanes with equal digits find each other by a ballot for each bit in use, and
+// one of them counts for all (an LDS atomic a lane: equal ones wait for each
+// other, 16 us for 8192 rows of 4 adapters against 10; 2011 rows 5 us, 200 3.6).
+// It is latency all along; several workgroups would have to wait for each other.
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 
 __global__ __launch_bounds__(kSortThreads) void ad_sort(const int *ids, int M, int G, int bits, int *order, int *temp,
@@ -499,12 +513,14 @@ void adapter_sort(const int *ids, int M, int G, int *order, int *key, int *start
     hipLaunchKernelGGL(ad_sort, dim3(1), dim3(kSortThreads), 0, stream, ids, M, G, bits, order, order + M, key, start);
 }
 
-// A row a workgroup for up to 64 rows, and for up to 1024 where the adapters
-// may be so many that the rows hardly share any.
+// A row a workgroup for up to 256 rows, unsorted; 16 sorted rows a workgroup
+// above.  With 4096 x 4096 and 16 ranks, sorting and the product included: 64
+// rows of 4 adapters 11 us against 21 sorted, 256 rows of 8 adapters 18 against
+// 24 and of 32 25 against 26, 512 rows of 16 adapters 34 against 28.
 AdPlan adapter_plan(int M, int G)
 {
     AdPlan p;
-    p.few = M <= 64 || (M <= 1024 && M < 8LL * G);
+    p.few = M <= 256;
     p.sorted = !p.few && G > 1;
     return p;
 }
@@ -516,30 +532,31 @@ void adapter_shrink(const AdShrinkArgs &a, const AdPlan &plan, int x_dtype, int 
             typedef decltype(x) X;
             typedef decltype(w) A;
             if (plan.few) {
-                const int rp = adapter_ranks(a.r);
-                if (a.M * (long long)rp < 1024)      // (few workgroups: fewer ranks each)
-                    hipLaunchKernelGGL((ad_shrink_few<X, A, 4>), dim3(a.M, rp / 4), dim3(kAdFewWaves * 64), 0, stream, a);
-                else {
-                    constexpr int RC = std::is_same<A, Fp32>::value ? 8 : 16;      // (what the registers hold)
-                    hipLaunchKernelGGL((ad_shrink_few<X, A, RC>), dim3(a.M, rp / RC), dim3(kAdFewWaves * 64), 0, stream, a);
-                }
+                hipLaunchKernelGGL((ad_shrink_few<X, A>), dim3(a.M, adapter_ranks(a.r) / kAdFewRanks), dim3(kAdFewWaves * 64),
+                                   0, stream, a);
                 return;
             }
             const unsigned tiles = (unsigned)((a.M + 15LL) / 16);
-            // (fewer ranks a workgroup where there are few of them: x is then read
-            // by several)
             const unsigned more = a.order ? (a.G < 256 ? a.G : 256) : 0;      // for adapters that begin inside a tile
             auto launch = [&](auto rt) {
                 constexpr int RT = decltype(rt)::value;
                 hipLaunchKernelGGL((ad_shrink_tile<X, A, RT>), dim3(tiles + more, (a.r + 16 * RT - 1) / (16 * RT)),
                                    dim3(kAdWaves * 64), 0, stream, a);
             };
-            if (a.r <= 16 || tiles <= 64)
-                launch(std::integral_constant<int, 1>{});
-            else if (a.r <= 32 || tiles <= 128)
+            // More ranks a workgroup, which reads x for all of them, if that leaves
+            // workgroups enough.  64 ranks of 4096 columns, with 16, 32 and 64 ranks a
+            // workgroup: 300 rows 11.3, 12.6 and 16.8 us, 1000 rows 15.8, 13.6 and
+            // 16.5, 2011 rows 24.2, 20.7 and 17.8 (fp16 and kept: 18.6 and 21.6 for
+            // the latter two), 8192 rows 75, 53 and 46.
+            auto enough = [&](int ranks, int least) {
+                return a.r > ranks / 2 && (long long)tiles * ((a.r + ranks - 1) / ranks) >= least;
+            };
+            if (enough(64, 200))
+                launch(std::integral_constant<int, 4>{});
+            else if (enough(32, 100))
                 launch(std::integral_constant<int, 2>{});
             else
-                launch(std::integral_constant<int, 4>{});
+                launch(std::integral_constant<int, 1>{});
         });
     });
 }

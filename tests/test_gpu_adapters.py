@@ -49,7 +49,8 @@ def want_forward(x, w, bias, ad, ids, out):
 
 FORWARD = [(1, 1, 1, 1, 1), (1, 40, 33, 2, 5), (1, 300, 2500, 3, 16), (2, 64, 96, 1, 64), (3, 70, 513, 5, 17), (4, 130, 1000, 4, 70),
            (5, 33, 100, 3, 1), (17, 48, 640, 30, 8), (64, 96, 1024, 3, 16), (64, 520, 1200, 9, 33), (65, 100, 130, 4, 16),
-           (130, 257, 300, 2, 40), (300, 64, 64, 7, 20), (513, 140, 97, 1, 16), (700, 400, 160, 20, 130)]
+           (130, 257, 300, 2, 40), (256, 96, 200, 6, 16), (257, 96, 200, 6, 16), (300, 64, 64, 7, 20), (400, 64, 264, 5, 130),
+           (513, 140, 97, 1, 16), (700, 400, 160, 20, 130), (1700, 48, 520, 4, 24)]
 
 
 @pytest.mark.parametrize("M,N,K,G,r", FORWARD)
@@ -73,7 +74,8 @@ def test_forward(M, N, K, G, r, dtype, adtype, out, order):
 
 
 BACKWARD = [(1, 1, 1, 1, 1), (1, 40, 33, 2, 5), (3, 70, 513, 5, 17), (33, 48, 64, 3, 16), (64, 130, 100, 4, 70), (129, 257, 130, 2, 40),
-            (300, 64, 64, 7, 20), (777, 100, 72, 3, 8), (2300, 40, 200, 3, 16), (5000, 33, 30, 2, 33)]
+            (257, 60, 72, 4, 16), (300, 64, 64, 7, 20), (777, 100, 72, 3, 8), (1700, 264, 40, 3, 24), (2300, 40, 200, 3, 16),
+            (5000, 33, 30, 2, 33)]
 
 
 @pytest.mark.parametrize("M,N,K,G,r", BACKWARD)
@@ -120,7 +122,7 @@ def test_no_row_has_an_adapter():
         assert torch.equal(dx, cim.mxfp4_linear_nhwc(dy, wt, None, out_dtype=FP32)) and not ddown.any() and not dup.any()
 
 
-@pytest.mark.parametrize("M", [3, 40, 200])
+@pytest.mark.parametrize("M", [3, 40, 200, 300])
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 def test_infinities_stay_with_their_row_and_adapter(M, dtype):
     """Adapter 1 holds infinities and NaN and some rows do: only those rows, and rows of adapter 1, are not finite."""
@@ -151,15 +153,16 @@ def test_infinities_stay_with_their_row_and_adapter(M, dtype):
     assert torch.equal(back[0][1:], grads[0][1:]) and torch.equal(back[1], grads[1]) and torch.equal(back[2], grads[2])
 
 
-def test_same_row_alone_and_in_a_batch():
+@pytest.mark.parametrize("M", [200, 300])
+def test_same_row_alone_and_in_a_batch(M):
     """A row's output is one adapter's, whatever else is in the batch."""
     w, bias, ad = layer(2, 96, 160, 6, 16, BF16)
     q = cim.mxfp4_quantize_nhwc(w)
-    x = rows(1, 200, 160, BF16)
-    ids = numbers(1, 200, 6, "mixed")
+    x = rows(1, M, 160, BF16)
+    ids = numbers(1, M, 6, "mixed")
     every = cim.mxfp4_linear_adapters_nhwc(x, q, bias, ad, ids, out_dtype=FP32)
     y, tol, _, _ = want_forward(x, w, bias, ad, ids, FP32)
-    for k in (0, 3, 63, 64, 150, 199):
+    for k in (0, 3, 63, 64, 150, M - 1):
         one = cim.mxfp4_linear_adapters_nhwc(x[k:k + 1], q, bias, ad, ids[k:k + 1], out_dtype=FP32)
         assert (np.abs(f64(one) - f64(every[k:k + 1])) <= 2 * tol[k:k + 1]).all()
 

@@ -97,7 +97,7 @@ def test_graph_replays():
     w, bias, ad = layer(2, 96, 160, 5, 16, BF16)
     q, wt = cim.mxfp4_quantize_nhwc(w), cim.mxfp4_quantize_nhwc(w, transpose=True)
     gamma = torch.rand(160, device="cuda") + 0.5
-    x, dy, ids = rows(1, 200, 160, BF16), rows(3, 200, 96, BF16), numbers(1, 200, 5, "mixed")
+    x, dy, ids = rows(1, 300, 160, BF16), rows(3, 300, 96, BF16), numbers(1, 300, 5, "mixed")
 
     def step(m):
         y, n8, rstd = cim.layer_norm_mxint8_nhwc(x[:m], gamma)
@@ -108,7 +108,7 @@ def test_graph_replays():
                      cim.mxint8_dequantize_nhwc(y8, BF16), cim.mxfp4_linear_adapters_nhwc(y[:2], q, None, ad, ids[:2])))
 
     graphs = []
-    for m in (200, 40):
+    for m in (300, 200, 40):
         side = torch.cuda.Stream()
         side.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(side):
@@ -119,9 +119,9 @@ def test_graph_replays():
             out = step(m)
         graphs.append((m, graph, out))
     for k in range(4):
-        x.copy_(rows(10 + k, 200, 160, BF16))
-        dy.copy_(rows(20 + k, 200, 96, BF16))
-        ids.copy_(numbers(30 + k, 200, 5, "mixed" if k % 2 else "runs"))
+        x.copy_(rows(10 + k, 300, 160, BF16))
+        dy.copy_(rows(20 + k, 300, 96, BF16))
+        ids.copy_(numbers(30 + k, 300, 5, "mixed" if k % 2 else "runs"))
         for _, graph, _ in graphs:
             graph.replay()
         torch.cuda.synchronize()
