@@ -78,10 +78,11 @@ AdFwdLayout ad_fwd_layout(int M, int K, int G, int rank)
 }
 
 int grad_tiles(int C) { return (int)((C + 127LL) / 128); }
-int grad_chunks_of_ranks(int r) { return r <= 16 ? 1 : r <= 32 ? 1 : (r + 63) / 64; }
+int grad_chunks_of_ranks(int r) { return (r + 63) / 64; }
 
-// Sorted rows a chunk of the gradients: as many chunks as give about 512
-// workgroups, in runs of 32 rows.
+// Sorted rows a chunk of the gradients: so many that there are about 512
+// workgroups, in runs of 32 rows.  (With 1024 the 8192 rows above 4096 columns
+// take 35 us instead of 33.6, and the sums over the chunks 6.6 instead of 6.3.)
 int adapter_grad_per(int M, int C, int r)
 {
     const long long tiles = (long long)grad_tiles(C) * grad_chunks_of_ranks(r), chunks = tiles < 512 ? 512 / tiles : 1,
