@@ -5,7 +5,8 @@
 // Values are split into bf16 terms that add up to them exactly (bf16 1, fp16 2,
 // fp32 3 terms of at most 8 bits), so that bf16 matrix instructions give fp32
 // products: those of terms i and j with i + j <= 2, the others are below
-// 2^-24 of the product.
+// 2^-24 of the product.  (The smallest bf16 is 2^-133: an fp32 value's bits below
+// that are left out.)
 #pragma once
 
 #include "row_common.hpp"

@@ -574,6 +574,7 @@ int mxfp4_linear_bwd_mxint8(const void *dy, long long lddy, int dy_dtype, const 
  * where the adapter's part is taken from x itself, not from Q(x), and added
  * before the one rounding to out_dtype.  A row depends on its own adapter only:
  * an infinity or a NaN in another one or in another row does not reach it.
+ * Products and sums are fp32; of an fp32 value the bits below 2^-133 may be lost.
  *
  *   x, w_codes, w_scales, bias, out   as for mxfp4_linear_fwd, x dense
  *   down      device, [adapters][rank][K] in a_dtype

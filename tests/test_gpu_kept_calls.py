@@ -328,3 +328,26 @@ def test_adapters_past_32_bit_offsets():
         ref.check(ddown[[G - 1, G - 2]], want, tol, "ddown")
         assert not ddown[:G - 2].any() and not dup[:G - 2].any()
         del ddown, dup
+
+
+@pytest.mark.parametrize("dtype,low", [(BF16, -130), (FP16, -22), (FP32, -100)])
+@pytest.mark.parametrize("M", [3, 40, 300])
+def test_the_smallest_values(dtype, low, M):
+    """Rows near and below the smallest normal value lose nothing: large adapters bring them back to ordinary sizes."""
+    N, K, G, r = 64, 160, 3, 20
+    up = 10 if dtype == FP16 else 100
+    x, dy = ((rows(s, M, n, FP32) * 2.0 ** low).to(dtype) for s, n in ((1, K), (2, N)))
+    assert (x.float().abs() < torch.finfo(dtype).tiny).any() or dtype == FP32
+    w, _, ad = layer(3, N, K, G, r, FP32)
+    ad = cim.Adapters((ad.down * 2.0 ** up).to(dtype), (ad.up * 2.0 ** up).to(dtype), ad.scale)
+    ids = numbers(4, M, G, "mixed")
+    zero = torch.zeros_like(w)
+    y, tol, h, dh = want_forward(x, zero, None, ad, ids, FP32)
+    got, _, gh = cim.mxfp4_linear_adapters_nhwc(x, cim.mxfp4_quantize_nhwc(zero), None, ad, ids, out_dtype=FP32, save=True)
+    ref.check(gh, h, dh + 2.0 ** -149, "h")
+    ref.check(got, y, tol, "out")
+    n = f64(ids).astype(np.int64)
+    one = torch.ones((M, r), device="cuda")
+    _, ddown, dup = cim.mxfp4_linear_adapters_bwd_nhwc(dy, torch.ones((M, K), device="cuda"), None, ad, ids, one)
+    t, dt = kept.through(f64(dy), f64(ad.up), n)
+    ref.check(ddown, *kept.grads(t, dt, np.ones((M, K)), f64(ad.scale), n), "ddown")
