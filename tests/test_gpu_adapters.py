@@ -107,10 +107,11 @@ def test_backward(M, N, K, G, r, dtype, adtype, grad, out, order):
     assert none is None and torch.equal(d2, ddown) and torch.equal(u2, dup)
 
 
-def test_no_row_has_an_adapter():
-    for M in (1, 4, 40, 200):
+@pytest.mark.parametrize("G", [1, 3])
+def test_no_row_has_an_adapter(G):
+    for M in (1, 4, 40, 200, 300):
         x = rows(1, M, 96, BF16)
-        w, bias, ad = layer(2, 64, 96, 3, 16, BF16)
+        w, bias, ad = layer(2, 64, 96, G, 16, BF16)
         q = cim.mxfp4_quantize_nhwc(w)
         ids = torch.full((M,), -1, dtype=torch.int32, device="cuda")
         got, _, h = cim.mxfp4_linear_adapters_nhwc(x, q, bias, ad, ids, out_dtype=FP32, save=True)
@@ -120,6 +121,29 @@ def test_no_row_has_an_adapter():
         wt = cim.mxfp4_quantize_nhwc(w, transpose=True)
         dx, ddown, dup = cim.mxfp4_linear_adapters_bwd_nhwc(dy, x, wt, ad, ids, h, dx_dtype=FP32)
         assert torch.equal(dx, cim.mxfp4_linear_nhwc(dy, wt, None, out_dtype=FP32)) and not ddown.any() and not dup.any()
+
+
+@pytest.mark.parametrize("M", [200, 300])
+@pytest.mark.parametrize("G,last", [(1, 111), (3, 111), (3, 101)])
+def test_only_some_rows_have_an_adapter(M, G, last):
+    """Whole tiles of rows without one, and an adapter with one row: the others are the layer's alone."""
+    x, dy = rows(1, M, 96, BF16), rows(3, M, 64, BF16)
+    w, bias, ad = layer(2, 64, 96, G, 16, BF16)
+    q, wt = cim.mxfp4_quantize_nhwc(w), cim.mxfp4_quantize_nhwc(w, transpose=True)
+    ids = torch.full((M,), -1, dtype=torch.int32, device="cuda")
+    ids[100:last] = G - 1
+    y, tol, h, dh = want_forward(x, w, bias, ad, ids, FP32)
+    got, _, gh = cim.mxfp4_linear_adapters_nhwc(x, q, bias, ad, ids, out_dtype=FP32, save=True)
+    ref.check(got, y, tol, "out")
+    ref.check(gh, h, dh + 1e-40, "h")
+    none = ids < 0
+    assert torch.equal(got[none], cim.mxfp4_linear_nhwc(x, q, bias, out_dtype=FP32)[none]) and not gh[none].any()
+    dx, ddown, dup = cim.mxfp4_linear_adapters_bwd_nhwc(dy, x, wt, ad, ids, gh, dx_dtype=FP32)
+    assert torch.equal(dx[none], cim.mxfp4_linear_nhwc(dy, wt, None, out_dtype=FP32)[none])
+    n = f64(ids).astype(np.int64)
+    t, dt = kept.through(f64(dy), f64(ad.up), n)
+    ref.check(ddown, *kept.grads(t, dt, f64(x), f64(ad.scale), n), "ddown")
+    ref.check(dup, *kept.grads(f64(gh), 0 * f64(gh), f64(dy), f64(ad.scale), n), "dup")
 
 
 @pytest.mark.parametrize("M", [3, 40, 200, 300])
