@@ -105,8 +105,8 @@ __global__ __launch_bounds__(kAdFewWaves * 64) void ad_shrink_few(AdShrinkArgs a
 // row, the next step in flight; in that form four lanes hold a block and quantise
 // it.  They reach the matrix instruction's form (a lane eight columns of row
 // lane % 16) through LDS that is the wave's own.  (Loading them in that form
-// straight away puts neighbouring lanes on different rows: 8192 x 8192 71 us
-// against 40.  Two steps in flight overflow the registers: 2011 x 4096 with 64
+// straight away puts neighbouring lanes on different rows: 8192 x 8192 71 us, x
+// in cache, against 40.  Two steps in flight overflow the registers: 2011 x 4096 with 64
 // ranks 28 us against 19.)
 //
 // 8192 x 8192 and 16 ranks, x from memory: 51 us, 134 MB read and 37 written, 3.4
@@ -277,7 +277,7 @@ __global__ __launch_bounds__(kAdWaves * 64) void ad_shrink_tile(AdShrinkArgs a)
             }
             fetch(strip(lap + 1));
             // (all four rows of a lane side by side: one after another, each
-            // step waits for the one before; 8192 x 8192 48 us)
+            // step waits for the one before; 8192 x 8192 48 us, x in cache, against 40)
             if (some && quantise)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
