@@ -268,15 +268,21 @@ __device__ __forceinline__ bool adapter_expand(const MxAdapterArgs &a, int M, in
     return infinite;
 }
 
-// The outputs that an infinity or a NaN in up reaches, over what was stored for
-// them: TM x TN of them from row m0 and column n0 on, by one wave.
+// Adds what infinities and NaN in up make to the outputs that they reach, of
+// which the rest was stored: TM x TN of them from row m0 and column n0 on, by one
+// wave.  (An infinity that the rest is in fp16, but not the bias, counts as a sum
+// past fp16's largest value, which is finite before it is rounded.)
 template <typename T, typename O>
-__device__ __forceinline__ void adapter_infinite(const MxAdapterArgs &a, int M, int N, int m0, int n0, int TM, int TN,
-                                                 void *out)
+__device__ __forceinline__ void adapter_infinite(const MxAdapterArgs &a, const float *bias, int M, int N, int m0, int n0,
+                                                 int TM, int TN, void *out)
 {
     for (int k = threadIdx.x & 63; k < TM * TN; k += 64) {
         const int m = m0 + k / TN, n = n0 + k % TN, row = a.row(min(m, M - 1)), id = m < M && n < N ? a.key[m] : -1;
         if (id < 0 || id >= a.G)
+            continue;
+        typename O::raw *o = (typename O::raw *)out + (long long)row * N + n;
+        float rest = load1<O>(o);
+        if (rest != rest)
             continue;
         float s = 0.f;
         for (int i = 0; i < a.r; ++i) {
@@ -285,8 +291,11 @@ __device__ __forceinline__ void adapter_infinite(const MxAdapterArgs &a, int M, 
                 s += a.h[(long long)m * adapter_ranks(a.r) + i] * a.scale[id] * u;
             }
         }
-        if (!(__builtin_fabsf(s) < __builtin_inff()))
-            store1<O>((typename O::raw *)out + (long long)row * N + n, s);
+        if (!(__builtin_fabsf(s) < __builtin_inff())) {
+            if (O::code == CONVIMG_FP16 && __builtin_isinf(rest) && !(bias && __builtin_isinf(bias[n])))
+                rest = 0.f;
+            store1<O>(o, rest + s);
+        }
     }
 }
 

@@ -453,8 +453,8 @@ __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsign
     }
     if constexpr (ADAPT)
         if (infinite) {
-            mx_wait_vm<0>();
-            adapter_infinite<typename AD::type, O>(ad, g.M, g.N, m0 + wm * TM, n0 + wn * TN, TM, TN, g.out);
+            __threadfence_block();      // (the wave reads what its other lanes stored)
+            adapter_infinite<typename AD::type, O>(ad, g.bias, g.M, g.N, m0 + wm * TM, n0 + wn * TN, TM, TN, g.out);
         }
 }
 

@@ -1,0 +1,70 @@
+"""What infinities, NaN and every bit of an fp32 value become in the products of the low-rank adapters on the GPU: the
+kind of each output (finite, an infinity, NaN) and, where the definition is exact in fp32, its value."""
+import numpy as np
+import pytest
+import torch
+
+import convolution_implicit_gemm_fwd_amd as cim
+import row_reference as ref
+from gpu_harness import need_gpu
+from row_reference import f64
+from test_gpu_adapters import layer
+from test_gpu_mxfp4 import rows
+
+pytestmark = pytest.mark.gpu
+BF16, FP16, FP32 = torch.bfloat16, torch.float16, torch.float32
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    need_gpu()
+
+
+def kind(a):
+    """0 finite, 1 and -1 the infinities, 2 NaN."""
+    return np.where(np.isnan(a), 2, np.where(np.isinf(a), np.sign(a), 0)).astype(int)
+
+
+def same_kind(got, want, out, what):
+    """The kind of every output; want: the definition's values in 64 bits, rounded to the output's type here."""
+    got, want = kind(f64(got)), kind(f64(torch.from_numpy(want).to(out)))
+    bad = np.argwhere(got != want)
+    assert not len(bad), "%s: %d of another kind, the first at %s: %d for %d" % (
+        what, len(bad), bad[0], got[tuple(bad[0])], want[tuple(bad[0])])
+
+
+def part(x, ad, ids):
+    """The adapters' part of every row and h, term by term in 64 bits (0 times an infinity is NaN)."""
+    down, up, scale, n = f64(ad.down), f64(ad.up), f64(ad.scale), f64(ids).astype(int)
+    h, y = np.zeros((x.shape[0], down.shape[1])), np.zeros((x.shape[0], up.shape[2]))
+    with np.errstate(all="ignore"):
+        for m in np.nonzero((n >= 0) & (n < len(scale)))[0]:
+            g = n[m]
+            h[m] = (x[m] * down[g]).sum(-1)
+            y[m] = scale[g] * (h[m][:, None] * up[g]).sum(0)
+    return y, h
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 64, 96), (40, 64, 96), (61, 96, 1100), (300, 64, 96), (2500, 520, 96)])
+@pytest.mark.parametrize("out", [BF16, FP16, FP32])
+def test_an_infinity_in_up_is_added_to_the_rest(M, N, K, out):
+    """Over an infinity or a NaN of the layer's own part (a row of x with an infinity, a scale byte of the weights that
+    stands for NaN, the bias) and over a finite sum past the output's largest value."""
+    x = rows(1, M, K, BF16)
+    w, bias, ad = layer(2, N, K, 3, 16, BF16)
+    ids = (torch.arange(M, device="cuda") % 4 - 1).int()
+    ids[0] = ids[M - 1] = 1
+    x[0, 7] = INF
+    bias[20], bias[21], bias[22], bias[23] = INF, NAN, 1e5, -1e5
+    q = cim.mxfp4_quantize_nhwc(w)
+    q.scales[0, 9, 0] = 255
+    for n in (5, 9, 20, 21, 22, 23):
+        ad.up[1, 2, n] = INF
+    ad.up[1, 2, 24], ad.up[1, 2, N - 1] = -INF, NAN
+    got = cim.mxfp4_linear_adapters_nhwc(x, q, bias, ad, ids, out_dtype=out)
+    b = np.nan_to_num(ref.mx_quantize(f64(x))[2]) @ ref.mx_quantize(f64(w))[2].T
+    b[0], b[:, 9] = NAN, NAN
+    with np.errstate(invalid="ignore"):
+        want = b + f64(bias) + part(f64(x), ad, ids)[0]
+    same_kind(got, want, out, "out")
