@@ -88,8 +88,21 @@ struct MxNoAdapters {};
 __host__ __device__ inline int adapter_ranks(int r) { return (r + 15) & ~15; }
 
 // h of a place as the products take it: scaled, for each 16 ranks three terms
-// of 16, zeros past the rank.
+// of 16, zeros past the rank.  The terms of an infinity or a NaN are 0, the first
+// one with a sign, which no other first term of that size has.
 constexpr int kAdTermBytes = 96;
+
+__device__ __forceinline__ void adapter_terms(float h, unsigned short (&t)[3])
+{
+    const float v[8] = {h};
+    u32v4_t s[3];
+    split8(v, s);
+    const bool finite = __builtin_fabsf(h) < __builtin_inff();
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+        t[k] = finite ? (unsigned short)s[k][0] : (unsigned short)0;
+    t[0] = !finite ? 0x8000 : t[0] == 0x8000 ? 0 : t[0];
+}
 
 struct MxAdapterArgs {
     const unsigned char *terms;      // [M][ranks / 16][3][16] bf16, 16-byte aligned
@@ -158,8 +171,10 @@ __device__ __forceinline__ bool adapter_up8(const typename T::raw (&w)[8], u32v4
 // clamped places: a branch around each would make the wave wait for them one
 // by one); of KG groups of waves that share the tile each takes every KG-th
 // step.  A place has zeros for h in another adapter's product.  Zero times an
-// infinity would not do: such values of up are left out (0) here, and the answer
-// says that there are some, for adapter_infinite.  (Selecting by place after the
+// infinity would not do, nor an infinity times a value's lower terms, which may be
+// 0: values of up that are not finite are left out (0) here, those of h were
+// before, and the answer says that there are some of h (1) or of up (2), for
+// adapter_infinite.  (Selecting by place after the
 // product instead takes the sums from the matrix unit's registers: the largest
 // tile then spills, 8192^3 with 16 ranks 777 us.)
 //
@@ -169,7 +184,7 @@ __device__ __forceinline__ bool adapter_up8(const typename T::raw (&w)[8], u32v4
 // that of 61 x 8000 x 4096 with an adapter a row 6 us, the rows' parts of up
 // (8000 x 16 a row) being read from memory then.
 template <typename T, int FM, int FN, int KG>
-__device__ __forceinline__ bool adapter_expand(const MxAdapterArgs &a, int M, int N, int m0, int n0, int group,
+__device__ __forceinline__ unsigned adapter_expand(const MxAdapterArgs &a, int M, int N, int m0, int n0, int group,
                                                f32x16_t (&acc)[FM][FN])
 {
     constexpr int P = FM * FN <= 1 ? 8 : FM * FN <= 2 ? 4 : 2, NT = split_terms<T>();
@@ -177,6 +192,8 @@ __device__ __forceinline__ bool adapter_expand(const MxAdapterArgs &a, int M, in
     const int steps = adapter_ranks(a.r) / 16;
     int id[FM];
     unsigned any[FM], left[FM];
+    typedef short i16x2 __attribute__((ext_vector_type(2)));
+    i16x2 low = {};
     bool infinite = false;
 #pragma unroll
     for (int i = 0; i < FM; ++i)
@@ -218,7 +235,7 @@ __device__ __forceinline__ bool adapter_expand(const MxAdapterArgs &a, int M, in
     };
     int g0 = next();
     if (g0 < 0)
-        return false;
+        return 0;
     do {
         int g[P];
         u32v4_t h[P][FM][3];
@@ -253,8 +270,12 @@ __device__ __forceinline__ bool adapter_expand(const MxAdapterArgs &a, int M, in
 #pragma unroll
                 for (int k = 0; k < 3; ++k)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        h[p][i][k][e] = id[i] == g[p] ? h[p][i][k][e] : 0u;
+                    for (int e = 0; e < 4; ++e) {
+                        const unsigned v = id[i] == g[p] ? h[p][i][k][e] : 0u;
+                        h[p][i][k][e] = v;
+                        if (k == 0)
+                            low = __builtin_elementwise_min(low, __builtin_bit_cast(i16x2, v));
+                    }
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
                 u32v4_t b[NT];
@@ -265,34 +286,49 @@ __device__ __forceinline__ bool adapter_expand(const MxAdapterArgs &a, int M, in
             }
         }
     } while (g0 >= 0);
-    return infinite;
+    return (__any(min(low[0], low[1]) == -32768) ? 1u : 0u) | (infinite ? 2u : 0u);
 }
 
-// Adds what infinities and NaN in up make to the outputs that they reach, of
-// which the rest was stored: TM x TN of them from row m0 and column n0 on, by one
-// wave.  (An infinity that the rest is in fp16, but not the bias, counts as a sum
-// past fp16's largest value, which is finite before it is rounded.)
+// Adds what was left out of h and of up, as far as `left` says there is, to the
+// outputs that it reaches, of which the rest was stored: TM x TN of them from row
+// m0 and column n0 on, by one wave.  (An infinity that the rest is in fp16, but
+// not the bias, counts as a sum past fp16's largest value, which is finite before
+// it is rounded; where scale h is past fp32's largest value and the sum is not, the
+// output is rounded twice.)
 template <typename T, typename O>
 __device__ __forceinline__ void adapter_infinite(const MxAdapterArgs &a, const float *bias, int M, int N, int m0, int n0,
-                                                 int TM, int TN, void *out)
+                                                 int TM, int TN, unsigned left, void *out)
 {
-    for (int k = threadIdx.x & 63; k < TM * TN; k += 64) {
-        const int m = m0 + k / TN, n = n0 + k % TN, row = a.row(min(m, M - 1)), id = m < M && n < N ? a.key[m] : -1;
+    auto finite = [](float v) { return __builtin_fabsf(v) < __builtin_inff(); };
+    const int lane = threadIdx.x & 63;
+    for (int m = m0; m < min(m0 + TM, M); ++m) {
+        const int id = a.key[m];
         if (id < 0 || id >= a.G)
             continue;
-        typename O::raw *o = (typename O::raw *)out + (long long)row * N + n;
-        float rest = load1<O>(o);
-        if (rest != rest)
+        const float *h = a.h + (long long)m * adapter_ranks(a.r), scale = a.scale[id];
+        bool some = false;
+        for (int i = lane; i < a.r; i += 64)
+            some |= !finite(h[i] * scale);
+        if (!__any(some) && !(left & 2))
             continue;
-        float s = 0.f;
-        for (int i = 0; i < a.r; ++i) {
-            const float u = load1<T>((const typename T::raw *)a.up + ((long long)id * a.r + i) * N + n);
-            if (!(__builtin_fabsf(u) < __builtin_inff())) {
-                s += a.h[(long long)m * adapter_ranks(a.r) + i] * a.scale[id] * u;
+        const typename T::raw *up = (const typename T::raw *)a.up + (long long)id * a.r * N;
+        for (int n = n0 + lane; n < min(n0 + TN, N); n += 64) {
+            typename O::raw *o = (typename O::raw *)out + (long long)a.row(m) * N + n;
+            float rest = load1<O>(o), s = 0.f;
+            if (rest != rest)
+                continue;
+            bool any = false;
+            for (int i = 0; i < a.r; ++i) {
+                const float u = load1<T>(up + (long long)i * N + n);
+                if (!finite(u) || !finite(h[i] * scale)) {
+                    s = __builtin_fmaf(h[i], u, s);
+                    any = true;
+                }
             }
-        }
-        if (!(__builtin_fabsf(s) < __builtin_inff())) {
-            if (O::code == CONVIMG_FP16 && __builtin_isinf(rest) && !(bias && __builtin_isinf(bias[n])))
+            if (!any)
+                continue;
+            s *= scale;
+            if (O::code == CONVIMG_FP16 && __builtin_isinf(rest) && !(bias && __builtin_isinf(bias[n])) && !finite(s))
                 rest = 0.f;
             store1<O>(o, rest + s);
         }

@@ -13,13 +13,12 @@ __device__ __forceinline__ void adapter_put(const AdShrinkArgs &a, int at, int r
     if (a.kept && i < a.r)
         a.kept[(long long)row * a.r + i] = h;
     if (a.terms) {
-        const float v[8] = {h * scale};
-        u32v4_t t[3];
-        split8(v, t);
+        unsigned short t[3];
+        adapter_terms(h * scale, t);
         unsigned short *p = (unsigned short *)(a.terms + ((long long)at * (rp / 16) + i / 16) * kAdTermBytes) + i % 16;
 #pragma unroll
         for (int k = 0; k < 3; ++k)
-            p[k * 16] = (unsigned short)t[k][0];
+            p[k * 16] = t[k];
     }
 }
 

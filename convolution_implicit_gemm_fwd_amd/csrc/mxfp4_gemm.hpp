@@ -145,7 +145,7 @@ __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsign
     const int group = KG > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / (NW * 64)) : 0;
     unsigned char *const lds = smem;
     smem += group * (STAGES * STAGE);
-    // (adapters: whether another group of waves left infinities out, a word a wave behind the rest)
+    // (adapters: whether another group of waves left something out, a word a wave behind the rest)
     constexpr bool ADAPT = !__is_same(AD, MxNoAdapters);
     [[maybe_unused]] volatile int *const flags = (int *)(lds + mx_gemm_lds<S, sizeof(typename O::raw)>());
     if constexpr (ADAPT && KG > 1) {
@@ -334,11 +334,11 @@ __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsign
 
     // Adapters, here and not while the first copies are under way: the loop's
     // registers are free again, of which the largest tile has none to spare.
-    [[maybe_unused]] bool infinite = false;
+    [[maybe_unused]] unsigned left = 0;      // what adapter_infinite has to add
     if constexpr (ADAPT) {
-        infinite = adapter_expand<typename AD::type, FM, FN, KG>(ad, g.M, g.N, m0 + wm * TM, n0 + wn * TN, group, acc);
-        if (KG > 1 && group > 0 && infinite && lane == 0)
-            flags[wave] = 1;
+        left = adapter_expand<typename AD::type, FM, FN, KG>(ad, g.M, g.N, m0 + wm * TM, n0 + wn * TN, group, acc);
+        if (KG > 1 && group > 0 && left && lane == 0)
+            flags[wave] = 3;
     }
 
     // Rows of the output through LDS, as many blocks of 32 a wave as it holds,
@@ -347,7 +347,7 @@ __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsign
     mx_wait_lds();
     mx_barrier();
     if constexpr (ADAPT && KG > 1)
-        infinite |= flags[wave] != 0;
+        left |= flags[wave];
     if constexpr (KG > 1) {
         // [block of 16 values][group - 1][the group's thread]
         f32x4_t *sums = (f32x4_t *)lds;
@@ -452,9 +452,9 @@ __device__ __forceinline__ void mx_gemm_body(const MxGemmArgs &g, int id, unsign
         }
     }
     if constexpr (ADAPT)
-        if (infinite) {
+        if (left) {
             __threadfence_block();      // (the wave reads what its other lanes stored)
-            adapter_infinite<typename AD::type, O>(ad, g.bias, g.M, g.N, m0 + wm * TM, n0 + wn * TN, TM, TN, g.out);
+            adapter_infinite<typename AD::type, O>(ad, g.bias, g.M, g.N, m0 + wm * TM, n0 + wn * TN, TM, TN, left, g.out);
         }
 }
 

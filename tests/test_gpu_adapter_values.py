@@ -68,3 +68,43 @@ def test_an_infinity_in_up_is_added_to_the_rest(M, N, K, out):
     with np.errstate(invalid="ignore"):
         want = b + f64(bias) + part(f64(x), ad, ids)[0]
     same_kind(got, want, out, "out")
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 64, 96), (40, 64, 96), (61, 96, 1100), (300, 64, 96), (700, 64, 96), (2500, 520, 96)])
+@pytest.mark.parametrize("adtype", [BF16, FP16, FP32])
+def test_an_infinity_in_h_meets_every_value_of_up(M, N, K, adtype):
+    """An infinity in down makes h one; times up it is an infinity, also where up has few bits, and NaN where it is 0."""
+    x = rows(1, M, K, BF16)
+    w, bias, ad = layer(2, N, K, 3, 40, adtype)
+    ids = (torch.arange(M, device="cuda") % 4 - 1).int()
+    ids[0] = 1
+    ad.down[1, 3, 5], ad.down[2, 33, 7] = -INF, NAN
+    x[:, 5] = torch.where(x[:, 5] == 0, 1, x[:, 5])
+    ad.up[1, 3, :40] = torch.arange(-20, 20, device="cuda").to(adtype) / 4
+    got, _, h = cim.mxfp4_linear_adapters_nhwc(x, cim.mxfp4_quantize_nhwc(w), bias, ad, ids, out_dtype=FP32, save=True)
+    y, want_h = part(f64(x), ad, ids)
+    same_kind(h, want_h, FP32, "h")
+    b = ref.mx_quantize(f64(x))[2] @ ref.mx_quantize(f64(w))[2].T + f64(bias)
+    same_kind(got, b + y, FP32, "out")
+    clean = ad.down.clone()
+    clean[1, 3, 5] = clean[2, 33, 7] = 0
+    finite = cim.mxfp4_linear_adapters_nhwc(x, cim.mxfp4_quantize_nhwc(w), bias, ad._replace(down=clean), ids, out_dtype=FP32)
+    others = (ids != 1) & (ids != 2)
+    assert torch.equal(got[others], finite[others])
+
+
+@pytest.mark.parametrize("M", [3, 40, 300])
+def test_scaled_h_past_the_largest_value(M):
+    """scale * h overflows where scale * (h up) does not: the formula's order counts.  (fp32 sums of one term; x, down
+    and up are powers of two, so that every step is exact.)"""
+    N, K, r = 64, 96, 16
+    x = torch.zeros(M, K, device="cuda")
+    x[:, 3] = 2.0 ** 20
+    down, up = torch.zeros(2, r, K, device="cuda"), torch.zeros(2, r, N, device="cuda")
+    down[:, 5, 3] = 2.0 ** 20
+    up[0, 5], up[1, 5] = 2.0 ** -120, 2.0 ** -60
+    ad = cim.Adapters(down, up, torch.tensor([2.0 ** 100, 2.0 ** 10], device="cuda"))
+    ids = (torch.arange(M, device="cuda") % 3 - 1).int()
+    zero = cim.mxfp4_quantize_nhwc(torch.zeros(N, K, device="cuda"))
+    got = cim.mxfp4_linear_adapters_nhwc(x, zero, None, ad, ids)
+    assert np.array_equal(f64(got), part(f64(x), ad, ids)[0])
