@@ -104,12 +104,18 @@ __global__ __launch_bounds__(kMxFewWaves * 64) void mx_gemm_few(MxFewArgs g, AD 
             load_row(i, raw[i]);
     // Adapters: thread 16 i + n takes the ranks i, i + 4 waves, .. of column n.
     // h comes in before the weights, up behind their first stages.
-    [[maybe_unused]] float low[kMxFewM] = {}, h0[kMxFewM] = {};
-    if constexpr (ADAPT)
+    // (the scale multiplies their whole sum: an infinite one would make NaN of the
+    // 0 of a thread without a rank; thread 16 m + n has that of row m)
+    [[maybe_unused]] float low[kMxFewM] = {}, h0[kMxFewM] = {}, scale = 0.f;
+    if constexpr (ADAPT) {
+        const int id = (int)(threadIdx.x >> 4) < g.M ? ad.key[threadIdx.x >> 4] : -1;
+        if (id >= 0 && id < ad.G)
+            scale = ad.scale[id];
 #pragma unroll
         for (int m = 0; m < kMxFewM; ++m)
             if (m < g.M && (int)(threadIdx.x >> 4) < ad.r)
                 h0[m] = ad.h[(long long)m * adapter_ranks(ad.r) + (threadIdx.x >> 4)];
+    }
 #pragma unroll
     for (int u = 0; u < kMxFewRing; ++u)
         fetch(u * waves + wave, u);
@@ -126,7 +132,6 @@ __global__ __launch_bounds__(kMxFewWaves * 64) void mx_gemm_few(MxFewArgs g, AD 
                 const float h = i == first ? h0[m] : ad.h[(long long)m * adapter_ranks(ad.r) + i];
                 low[m] = __builtin_fmaf(h, load1<T>(up + (long long)i * g.N), low[m]);
             }
-            low[m] *= ad.scale[id];
         }
     }
 #pragma unroll
@@ -187,15 +192,19 @@ __global__ __launch_bounds__(kMxFewWaves * 64) void mx_gemm_few(MxFewArgs g, AD 
             }
     mx_wait_lds();
     mx_barrier();
-    for (int e = threadIdx.x; e < g.M * 16; e += blockDim.x) {
+    static_assert(kMxFewM * 16 <= 64, "an output a thread of the first wave");
+    if (const int e = threadIdx.x; e < g.M * 16) {
         const int n = n0 + (e & 15);
         if (n < g.N) {
             float s = g.bias ? g.bias[n] : 0.f;
             for (int k = 0; k < waves; ++k)
                 s += *(const float *)(ring[k][0] + e * 4);
-            if constexpr (ADAPT)
+            if constexpr (ADAPT) {
+                float t = 0.f;
                 for (int k = 0; k < waves; ++k)
-                    s += *(const float *)(ring[k][0] + kMxFewM * 64 + e * 4);
+                    t += *(const float *)(ring[k][0] + kMxFewM * 64 + e * 4);
+                s += scale * t;
+            }
             store1<O>((typename O::raw *)g.out + (long long)(e >> 4) * g.N + n, s);
         }
     }

@@ -108,3 +108,19 @@ def test_scaled_h_past_the_largest_value(M):
     zero = cim.mxfp4_quantize_nhwc(torch.zeros(N, K, device="cuda"))
     got = cim.mxfp4_linear_adapters_nhwc(x, zero, None, ad, ids)
     assert np.array_equal(f64(got), part(f64(x), ad, ids)[0])
+
+
+@pytest.mark.parametrize("M", [2, 3, 4, 40, 300])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("r", [1, 16, 20, 40])
+def test_an_infinite_scale(M, dtype, r):
+    """It multiplies the sum over the ranks, whichever threads hold it."""
+    N, K = 64, 2048
+    x = rows(1, M, K, dtype)
+    w, bias, ad = layer(2, N, K, 2, r, dtype)
+    ad.scale[0], ad.scale[1] = INF, -INF
+    ids = (torch.arange(M, device="cuda") % 3 - 1).flip(0).int()
+    got = cim.mxfp4_linear_adapters_nhwc(x, cim.mxfp4_quantize_nhwc(w), bias, ad, ids, out_dtype=FP32)
+    b = ref.mx_quantize(f64(x))[2] @ ref.mx_quantize(f64(w))[2].T + f64(bias)
+    y, h = part(f64(x), ad, ids)
+    same_kind(got, b + y, FP32, "out")
