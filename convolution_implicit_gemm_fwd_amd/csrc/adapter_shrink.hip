@@ -350,6 +350,44 @@ __global__ __launch_bounds__(kAdWaves * 64) void ad_shrink_tile(AdShrinkArgs a)
 #pragma unroll
         for (int t = 0; t < RT; ++t)
             sums[wave][t][lane] = acc[t];
+        // An infinity times a lower term, which may be 0, made NaN: such a sum over
+        // the wave's columns once more, value by value.
+        if constexpr (!HALVES && split_terms<X>() + split_terms<A>() > 2) {
+            bool nan = false;
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    nan |= acc[t][e] != acc[t][e];
+            if (nan && id == g) {
+                // (through empty asm: nothing of this is computed, and held in registers,
+                // before it is known to be wanted)
+                int K = a.K, row = m, four = 4 * q, adapter = g, r0 = i0;
+                asm volatile("" : "+s"(K), "+v"(row), "+v"(four), "+v"(adapter), "+s"(r0));
+#pragma unroll 1
+                for (int k = 0; k < RT * 4; ++k) {
+                    float &sum = ((float *)&sums[wave][k / 4][lane])[k % 4];
+                    if (sum == sum)
+                        continue;
+                    const typename X::raw *x1 = (const typename X::raw *)a.x + row * a.ldx;
+                    const typename A::raw *w = (const typename A::raw *)a.down
+                        + ((long long)adapter * a.r + min(min(r0 + k / 4 * 16, max(a.r - 16, 0)) + four + k % 4, a.r - 1)) * K;
+                    float s = 0.f;
+#pragma unroll 1
+                    for (int lap = 0; lap < laps && s == s; ++lap)
+#pragma unroll 1
+                        for (int c = strip(lap), last = min(c + 128, K); c < last && s == s; c += 8) {
+                            float v[8], u[8];
+                            load8<X>(x1, c, K, v);
+                            load8<A>(w, c, K, u);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                s = __builtin_fmaf(u[e], v[e], s);
+                        }
+                    sum = s;
+                }
+            }
+        }
         __syncthreads();
         if (wave < RT) {
             f32x4_t s = sums[0][wave][lane];

@@ -124,3 +124,29 @@ def test_an_infinite_scale(M, dtype, r):
     b = ref.mx_quantize(f64(x))[2] @ ref.mx_quantize(f64(w))[2].T + f64(bias)
     y, h = part(f64(x), ad, ids)
     same_kind(got, b + y, FP32, "out")
+
+
+def whole(g, shape, dtype):
+    """Whole numbers other than 0 of at most 4: products and sums are exact in fp32, and their lower parts are 0."""
+    return torch.from_numpy(g.integers(1, 5, shape) * g.choice([-1.0, 1.0], shape)).to(dtype).cuda()
+
+
+@pytest.mark.parametrize("M,K,G,r", [(3, 200, 3, 16), (40, 1100, 3, 5), (200, 200, 3, 40), (300, 200, 1, 16), (300, 1100, 3, 20),
+                                     (1700, 200, 3, 32), (3300, 200, 3, 64)])
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+@pytest.mark.parametrize("adtype", [BF16, FP16, FP32])
+def test_infinities_in_x_and_in_down_reach_h(M, K, G, r, dtype, adtype):
+    g = np.random.default_rng(M + r)
+    x = whole(g, (M, K), dtype)
+    ad = cim.Adapters(whole(g, (G, r, K), adtype), whole(g, (G, r, 64), adtype), torch.ones(G, device="cuda"))
+    ids = torch.from_numpy(g.integers(-1, G, M).astype(np.int32)).cuda()
+    ids[0] = ids[M - 1] = G - 1
+    x[0, 7], x[1, K - 1], x[M - 1, 130], x[M // 2, 40], x[M // 2, 150] = INF, -INF, INF, INF, -INF
+    x[2, 9] = NAN
+    ad.down[0, 1, 7] = ad.down[G - 1, 1, 130] = 0      # times an infinity of x
+    ad.down[0, 2, 60], ad.down[G - 1, r - 1, 7], ad.down[G - 1, 0, K - 1] = INF, -INF, INF
+    x[5 % M, 60], x[1, 60] = 0, -INF
+    q = cim.mxfp4_quantize_nhwc(torch.zeros(64, K, device="cuda"))
+    h = cim.mxfp4_linear_adapters_nhwc(x, q, None, ad, ids, out_dtype=FP32, save=True)[2]
+    want = part(f64(x), ad, ids)[1]
+    assert np.array_equal(f64(h), want, equal_nan=True), np.argwhere((f64(h) != want) & ~(np.isnan(want) & np.isnan(f64(h))))[:5]
