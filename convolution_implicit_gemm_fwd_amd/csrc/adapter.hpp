@@ -32,8 +32,8 @@ void adapter_shrink(const AdShrinkArgs &a, const AdPlan &plan, int x_dtype, int 
 // The rows sorted by adapter, those without one last, rows of one adapter by
 // their numbers: order [M] (and as much again behind it), key [M], the adapter
 // at each place or -1, and start [G + 1], the first place of each adapter and of
-// the rows without.
-void adapter_sort(const int *ids, int M, int G, int *order, int *key, int *start, hipStream_t stream);
+// the rows without.  With `nan` a 0 there.
+void adapter_sort(const int *ids, int M, int G, int *order, int *key, int *start, int *nan, hipStream_t stream);
 
 // One operand of the gradients: out[g][i][c] = scale_g * sum over the rows m
 // of g of u[m][i] * v[m][c].
@@ -45,6 +45,7 @@ struct AdGradArgs {
     const float *scale;
     float *out;                         // [G][r][C]
     float *part;                        // [chunks][2][r][C]
+    int *nan;                           // set if a sum is NaN; 0 before
     long long ldv;
     int M, C, G, r;
     int u_sorted, u_ld;                 // u's rows are in sorted order; their stride

@@ -26,6 +26,10 @@ struct Grad8x8 {
         r[e] = tail8<V>(load_raw8<V>((const typename V::raw *)a.v + m * a.ldv, c, a.C), c, a.C);
     }
     __device__ __forceinline__ void clear(int e) { r[e] = {}; }
+    static __device__ __forceinline__ float value(const AdGradArgs &a, int m, int c)
+    {
+        return load1<V>((const typename V::raw *)a.v + m * a.ldv + c);
+    }
     __device__ __forceinline__ void column(int j, u32v4_t (&t)[TERMS]) const
     {
         if constexpr (V::code == CONVIMG_BF16) {      // (the halves of the rows' words, two and two)
@@ -67,6 +71,10 @@ struct Grad8x8<Kept> {
     {
         q[e] = uint2{0, 0};
         unit[e] = 0.f;
+    }
+    static __device__ __forceinline__ float value(const AdGradArgs &a, int m, int c)
+    {
+        return (float)((const signed char *)a.v)[(long long)m * ((a.C + 31) & ~31) + c] * mxi_unit(a.vs, m, a.C, c);
     }
     __device__ __forceinline__ void column(int j, u32v4_t (&t)[1]) const
     {
@@ -184,19 +192,26 @@ __device__ __forceinline__ void ad_grad_body(const AdGradArgs &a, unsigned b, f3
             for (int e = 0; e < 4; ++e) {
                 const int i = i0 + t * 16 + q * 4 + e;
                 float o[8];
+                bool nan = false;
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
+                for (int j = 0; j < 8; ++j) {
                     o[j] = acc[t][j][e] * s;
+                    nan |= o[j] != o[j];
+                }
                 if (i < a.r && c < a.C)
                     store8<Fp32>(out + (long long)i * a.C, c, a.C, o);
+                if (nan)
+                    *a.nan = 1;
             }
         }
     }
 }
 
-// Both operands' gradients in one launch, up's first.
+// Both operands' gradients in one launch, up's first.  16 ranks of 16- and 8-bit
+// rows: four waves a SIMD, for which the compiler would take two registers too many.
 template <typename DY, typename X, int RT>
-__global__ __launch_bounds__(kAdGradWaves * 64) void ad_grad(AdGradArgs up, AdGradArgs down, unsigned up_blocks)
+__global__ __launch_bounds__(kAdGradWaves * 64, RT == 1 && !__is_same(DY, Fp32) && !__is_same(X, Fp32) ? 4 : 1)
+void ad_grad(AdGradArgs up, AdGradArgs down, unsigned up_blocks)
 {
     __shared__ f32x4_t sums[kAdGradWaves - 1][8][64];
     if (blockIdx.x < up_blocks)
@@ -205,12 +220,29 @@ __global__ __launch_bounds__(kAdGradWaves * 64) void ad_grad(AdGradArgs up, AdGr
         ad_grad_body<X, RT>(down, blockIdx.x - up_blocks, sums);
 }
 
+// One value of a gradient, value by value.
+template <typename V>
+__device__ __forceinline__ float ad_grad_value(const AdGradArgs &a, int g, int i, int c)
+{
+    float s = 0.f;
+#pragma unroll 4
+    for (int p = a.start[g]; p < a.start[g + 1]; ++p) {
+        const int m = a.order[p];
+        s = __builtin_fmaf(a.u[(long long)(a.u_sorted ? p : m) * a.u_ld + i], Grad8x8<V>::value(a, m, c), s);
+    }
+    return s * a.scale[g];
+}
+
 // The sums of the adapters whose rows lie in several chunks, in order, and
-// zeros for those without rows.
-static __global__ __launch_bounds__(256) void ad_grad_sum(AdGradArgs up, AdGradArgs down)
+// zeros for those without rows.  An infinity of one operand times a lower term of
+// the other, which may be 0, makes NaN: where some sum is NaN, those are taken
+// once more.  (Here, where registers are free: in ad_grad it took a wave a SIMD.)
+template <typename DY, typename X>
+__global__ __launch_bounds__(256) void ad_grad_sum(AdGradArgs up, AdGradArgs down)
 {
     const AdGradArgs &a = blockIdx.z == 0 ? up : down;
     const long long per = (long long)a.r * a.C;
+    const int nan = *a.nan;
     for (int g = blockIdx.y; g < a.G; g += gridDim.y) {
         const int g0 = a.start[g], g1 = a.start[g + 1];
         const int first = g0 / a.per, last = (g1 - 1) / a.per;
@@ -227,6 +259,15 @@ static __global__ __launch_bounds__(256) void ad_grad_sum(AdGradArgs up, AdGradA
             a.out[g * per + p] = s;
         }
     }
+    if (!nan)
+        return;
+    for (int g = blockIdx.y; g < a.G; g += gridDim.y)
+        for (long long p = (long long)blockIdx.x * 256 + threadIdx.x; p < per; p += (long long)gridDim.x * 256) {
+            float &out = a.out[g * per + p];
+            const int i = (int)(p / a.C), c = (int)(p - (long long)i * a.C);
+            if (out != out)
+                out = blockIdx.z == 0 ? ad_grad_value<DY>(a, g, i, c) : ad_grad_value<X>(a, g, i, c);
+        }
 }
 
 inline int grad_ranks(int r) { return r <= 16 ? 1 : r <= 32 ? 2 : 4; }
@@ -236,6 +277,7 @@ template <typename DY>
 void adapter_grads_of(const AdGradArgs &up, const AdGradArgs &down, int x_dtype, hipStream_t stream)
 {
     const unsigned n_up = (unsigned)up.tiles * up.ranks * up.chunks, n_down = (unsigned)down.tiles * down.ranks * down.chunks;
+    const long long n = ((long long)up.r * (up.C > down.C ? up.C : down.C) + 255) / 256;
     auto launch = [&](auto x, auto rt) {
         hipLaunchKernelGGL((ad_grad<DY, decltype(x), decltype(rt)::value>), dim3(n_up + n_down), dim3(kAdGradWaves * 64), 0,
                            stream, up, down, n_up);
@@ -246,14 +288,14 @@ void adapter_grads_of(const AdGradArgs &up, const AdGradArgs &down, int x_dtype,
         case 2: launch(x, std::integral_constant<int, 2>{}); break;
         default: launch(x, std::integral_constant<int, 4>{}); break;
         }
+        hipLaunchKernelGGL((ad_grad_sum<DY, decltype(x)>),
+                           dim3((unsigned)(n < 256 ? n : 256), (unsigned)(up.G < 4096 ? up.G : 4096), 2), dim3(256), 0,
+                           stream, up, down);
     };
     if (x_dtype == CONVIMG_MXINT8)
         ranks(Kept{});
     else
         with_dtype(x_dtype, ranks);
-    const long long n = ((long long)up.r * (up.C > down.C ? up.C : down.C) + 255) / 256;
-    hipLaunchKernelGGL(ad_grad_sum, dim3((unsigned)(n < 256 ? n : 256), (unsigned)(up.G < 4096 ? up.G : 4096), 2), dim3(256),
-                       0, stream, up, down);
 }
 
 }  // namespace convimg

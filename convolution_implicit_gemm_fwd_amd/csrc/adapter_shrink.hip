@@ -425,8 +425,10 @@ __global__ __launch_bounds__(kAdWaves * 64) void ad_shrink_tile(AdShrinkArgs a)
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 
 __global__ __launch_bounds__(kSortThreads) void ad_sort(const int *ids, int M, int G, int bits, int *order, int *temp,
-                                                        int *key, int *start)
+                                                        int *key, int *start, int *nan)
 {
+    if (nan && threadIdx.x == 0)
+        *nan = 0;
     constexpr int U = 8;      // chunks of 64 rows in flight
     __shared__ int place[256][kSortWaves];
     __shared__ int waves[kSortWaves];
@@ -542,12 +544,13 @@ __global__ __launch_bounds__(kSortThreads) void ad_sort(const int *ids, int M, i
         }
 }
 
-void adapter_sort(const int *ids, int M, int G, int *order, int *key, int *start, hipStream_t stream)
+void adapter_sort(const int *ids, int M, int G, int *order, int *key, int *start, int *nan, hipStream_t stream)
 {
     int bits = 1;
     while (bits < 32 && (unsigned)G >> bits)
         ++bits;
-    hipLaunchKernelGGL(ad_sort, dim3(1), dim3(kSortThreads), 0, stream, ids, M, G, bits, order, order + M, key, start);
+    hipLaunchKernelGGL(ad_sort, dim3(1), dim3(kSortThreads), 0, stream, ids, M, G, bits, order, order + M, key,
+                       start, nan);
 }
 
 // A row a workgroup for up to 256 rows, unsorted; 16 sorted rows a workgroup

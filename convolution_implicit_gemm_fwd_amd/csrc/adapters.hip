@@ -91,7 +91,7 @@ int adapter_grad_per(int M, int C, int r)
 }
 
 struct AdBwdLayout {
-    size_t dy, t, terms, part_down, part_up, order, start, total;
+    size_t dy, t, terms, part_down, part_up, order, start, nan, total;
     int per_down, per_up;
 };
 
@@ -115,6 +115,7 @@ AdBwdLayout ad_bwd_layout(int M, int N, int K, int G, int rank)
     l.part_up = take((size_t)ad_chunks(M, l.per_up) * 2 * rank * N * 4);
     l.order = take((size_t)M * 12);
     l.start = take(((size_t)G + 1) * 4);
+    l.nan = take(4);
     l.total = at;
     return l;
 }
@@ -188,7 +189,7 @@ int mxfp4_linear_adapters_fwd(const void *x, long long ldx, int x_dtype, const v
     int *start = order ? order + 3LL * M : nullptr;
     float *hh = (float *)(base + l.h);
     if (order)
-        adapter_sort(ids, M, adapters, order, order + 2LL * M, start, stream);
+        adapter_sort(ids, M, adapters, order, order + 2LL * M, start, nullptr, stream);
     const AdShrinkArgs s = {x, down, scale, key, order, start, hh, terms, h, codes, scales, (unsigned char *)x_codes,
                             (unsigned char *)x_scales, ldx, M, K, adapters, rank};
     adapter_shrink(s, l.plan, x_dtype, a_dtype, stream);
@@ -251,8 +252,9 @@ int mxfp4_linear_adapters_bwd(const void *dy, long long lddy, int dy_dtype, cons
     }
     unsigned char *base = (unsigned char *)ws, *codes = base + l.dy, *scales = codes + align256(mx_code_bytes(M, N));
     float *t = (float *)(base + l.t);
-    int *order = (int *)(base + l.order), *key = order + 2LL * M, *start = (int *)(base + l.start);
-    adapter_sort(ids, M, adapters, order, key, start, stream);
+    int *order = (int *)(base + l.order), *key = order + 2LL * M, *start = (int *)(base + l.start),
+        *nan = (int *)(base + l.nan);
+    adapter_sort(ids, M, adapters, order, key, start, nan, stream);
     unsigned char *terms = dx ? base + l.terms : nullptr;
     const AdShrinkArgs s = {dy, up, scale, key, order, start, t, terms, nullptr, dx ? codes : nullptr, scales, nullptr, nullptr,
                             lddy, M, N, adapters, rank};
@@ -264,10 +266,10 @@ int mxfp4_linear_adapters_bwd(const void *dy, long long lddy, int dy_dtype, cons
                       ad, dx_dtype, stream);
     }
     const int rt = grad_chunks_of_ranks(rank);
-    const AdGradArgs up_args = {h,   dy,   nullptr, order, key, start, scale, dup, (float *)(base + l.part_up), lddy, M, N,
+    const AdGradArgs up_args = {h,   dy,   nullptr, order, key, start, scale, dup, (float *)(base + l.part_up), nan, lddy, M, N,
                                 adapters, rank, 0, rank, l.per_up, ad_chunks(M, l.per_up), grad_tiles(N), rt},
                      down_args = {t, x, (const unsigned char *)x_scales, order, key, start, scale, ddown,
-                                  (float *)(base + l.part_down), ldx, M, K, adapters, rank, 1, adapter_ranks(rank),
+                                  (float *)(base + l.part_down), nan, ldx, M, K, adapters, rank, 1, adapter_ranks(rank),
                                   l.per_down, ad_chunks(M, l.per_down), grad_tiles(K), rt};
     auto grads = dy_dtype == CONVIMG_BF16 ? adapter_grads_bf16 : dy_dtype == CONVIMG_FP16 ? adapter_grads_fp16 : adapter_grads_fp32;
     grads(up_args, down_args, x_dtype, stream);

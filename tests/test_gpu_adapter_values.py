@@ -150,3 +150,36 @@ def test_infinities_in_x_and_in_down_reach_h(M, K, G, r, dtype, adtype):
     h = cim.mxfp4_linear_adapters_nhwc(x, q, None, ad, ids, out_dtype=FP32, save=True)[2]
     want = part(f64(x), ad, ids)[1]
     assert np.array_equal(f64(h), want, equal_nan=True), np.argwhere((f64(h) != want) & ~(np.isnan(want) & np.isnan(f64(h))))[:5]
+
+
+@pytest.mark.parametrize("M,G,r", [(40, 3, 8), (300, 1, 16), (300, 3, 24), (700, 3, 40), (2300, 3, 8), (2300, 2, 70)])
+@pytest.mark.parametrize("grad,dtype", [(BF16, BF16), (FP16, FP16), (FP32, FP32), (FP32, "kept"), (BF16, FP32)])
+def test_infinities_in_the_gradients(M, G, r, grad, dtype):
+    """In dy, in x, in h and in up: of whole numbers the gradients are exact wherever no infinity reaches."""
+    N, K = 72, 136
+    g = np.random.default_rng(M + r)
+    dy, h = whole(g, (M, N), grad), whole(g, (M, r), FP32)
+    x = whole(g, (M, K), BF16 if dtype == "kept" else dtype)
+    ad = cim.Adapters(whole(g, (G, r, K), grad), whole(g, (G, r, N), grad), torch.full((G,), 0.5, device="cuda"))
+    ids = torch.from_numpy(g.integers(-1, G, M).astype(np.int32)).cuda()
+    ids[0] = ids[M - 1] = G - 1
+    dy[0, 7], dy[M // 2, N - 1], dy[1, 20], dy[3, 20] = INF, -INF, INF, -INF
+    h[0, 1] = h[M // 2, 2] = 0      # times an infinity of dy
+    h[5, r - 1], h[M - 1, 3] = INF, NAN
+    x[M - 1, K - 1], x[2, 33] = INF, NAN
+    x[0, 4], x[1, 5] = 0, 0         # times an infinite t
+    ad.up[0, 4, 9] = INF
+    want_x = f64(x)
+    if dtype == "kept":
+        x = cim.mxint8_quantize_nhwc(x)
+        want_x[M - 1, 128:], want_x[2, 32:64] = NAN, NAN
+    none, ddown, dup = cim.mxfp4_linear_adapters_bwd_nhwc(dy, x, None, ad, ids, h)
+    n = f64(ids).astype(int)
+    t = part(f64(dy), ad._replace(down=ad.up), ids)[1]
+    with np.errstate(all="ignore"):
+        for k in range(G):
+            m = np.nonzero(n == k)[0]
+            for got, u, v, what in ((ddown, t, want_x, "ddown"), (dup, f64(h), f64(dy), "dup")):
+                want = 0.5 * sum((u[i][:, None] * v[i][None] for i in m), np.zeros((r, v.shape[1])))
+                a = f64(got[k])
+                assert np.array_equal(a, want, equal_nan=True), (what, k, np.argwhere(kind(a) != kind(want))[:5])
