@@ -301,36 +301,37 @@ __device__ __forceinline__ void adapter_infinite(const MxAdapterArgs &a, const f
 {
     auto finite = [](float v) { return __builtin_fabsf(v) < __builtin_inff(); };
     const int lane = threadIdx.x & 63;
-    for (int m = m0; m < min(m0 + TM, M); ++m) {
-        const int id = a.key[m];
-        if (id < 0 || id >= a.G)
-            continue;
-        const float *h = a.h + (long long)m * adapter_ranks(a.r), scale = a.scale[id];
-        bool some = false;
-        for (int i = lane; i < a.r; i += 64)
-            some |= !finite(h[i] * scale);
-        if (!__any(some) && !(left & 2))
-            continue;
-        const typename T::raw *up = (const typename T::raw *)a.up + (long long)id * a.r * N;
-        for (int n = n0 + lane; n < min(n0 + TN, N); n += 64) {
-            typename O::raw *o = (typename O::raw *)out + (long long)a.row(m) * N + n;
-            float rest = load1<O>(o), s = 0.f;
-            if (rest != rest)
-                continue;
-            bool any = false;
-            for (int i = 0; i < a.r; ++i) {
-                const float u = load1<T>(up + (long long)i * N + n);
-                if (!finite(u) || !finite(h[i] * scale)) {
-                    s = __builtin_fmaf(h[i], u, s);
-                    any = true;
+    for (int base = m0; base < min(m0 + TM, M); base += 64) {
+        // a lane a row: its adapter, and whether something of its h was left out
+        const int mine = min(base + lane, M - 1), given = base + lane < min(m0 + TM, M) ? a.key[mine] : -1;
+        bool some = (left & 2) != 0;
+        if (given >= 0 && given < a.G)
+            for (int i = 0; i < a.r; ++i)
+                some |= !finite(a.h[(long long)mine * adapter_ranks(a.r) + i] * a.scale[given]);
+        for (unsigned long long rows = __ballot(some && given >= 0 && given < a.G); rows; rows &= rows - 1) {
+            const int k = __builtin_ctzll(rows), m = base + k, id = __builtin_amdgcn_readlane(given, k);
+            const float *h = a.h + (long long)m * adapter_ranks(a.r), scale = a.scale[id];
+            const typename T::raw *up = (const typename T::raw *)a.up + (long long)id * a.r * N;
+            for (int n = n0 + lane; n < min(n0 + TN, N); n += 64) {
+                typename O::raw *o = (typename O::raw *)out + (long long)a.row(m) * N + n;
+                float rest = load1<O>(o), s = 0.f;
+                if (rest != rest)
+                    continue;
+                bool any = false;
+                for (int i = 0; i < a.r; ++i) {
+                    const float u = load1<T>(up + (long long)i * N + n);
+                    if (!finite(u) || !finite(h[i] * scale)) {
+                        s = __builtin_fmaf(h[i], u, s);
+                        any = true;
+                    }
                 }
+                if (!any)
+                    continue;
+                s *= scale;
+                if (O::code == CONVIMG_FP16 && __builtin_isinf(rest) && !(bias && __builtin_isinf(bias[n])) && !finite(s))
+                    rest = 0.f;
+                store1<O>(o, rest + s);
             }
-            if (!any)
-                continue;
-            s *= scale;
-            if (O::code == CONVIMG_FP16 && __builtin_isinf(rest) && !(bias && __builtin_isinf(bias[n])) && !finite(s))
-                rest = 0.f;
-            store1<O>(o, rest + s);
         }
     }
 }
