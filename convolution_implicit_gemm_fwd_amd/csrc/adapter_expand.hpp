@@ -4,9 +4,12 @@
 //
 // Values are split into bf16 terms that add up to them exactly (bf16 1, fp16 2,
 // fp32 3 terms of at most 8 bits), so that bf16 matrix instructions give fp32
-// products: those of terms i and j with i + j <= 2, the others are below
-// 2^-24 of the product.  (The smallest bf16 is 2^-133: an fp32 value's bits below
-// that are left out.)
+// products: those of terms i and j with i + j <= 3.  Term i is below 2^(1 - 8 i)
+// of the value, so the one product left out, of the last terms of two fp32 values,
+// is below 2^-30; without those of i + j = 3, which reach 2^-21 together and all
+// have the product's sign, a sum of products would be off by several units in its
+// last place.  (The smallest bf16 is 2^-133: an fp32 value's bits below that are
+// left out.)
 #pragma once
 
 #include "row_common.hpp"
@@ -60,7 +63,7 @@ template <int NA, int NB>
 __device__ __forceinline__ f32x4_t mfma_terms16(const u32v4_t (&a)[NA], const u32v4_t (&b)[NB], f32x4_t c)
 {
 #pragma unroll
-    for (int s = 2; s >= 0; --s)
+    for (int s = 3; s >= 0; --s)
 #pragma unroll
         for (int i = 0; i < NA; ++i)
             if (s - i >= 0 && s - i < NB)
@@ -73,7 +76,7 @@ template <int NA, int NB>
 __device__ __forceinline__ f32x16_t mfma_terms32(const u32v4_t (&a)[NA], const u32v4_t (&b)[NB], f32x16_t c)
 {
 #pragma unroll
-    for (int s = 2; s >= 0; --s)
+    for (int s = 3; s >= 0; --s)
 #pragma unroll
         for (int i = 0; i < NA; ++i)
             if (s - i >= 0 && s - i < NB)

@@ -183,3 +183,57 @@ def test_infinities_in_the_gradients(M, G, r, grad, dtype):
                 want = 0.5 * sum((u[i][:, None] * v[i][None] for i in m), np.zeros((r, v.shape[1])))
                 a = f64(got[k])
                 assert np.array_equal(a, want, equal_nan=True), (what, k, np.argwhere(kind(a) != kind(want))[:5])
+
+
+LONG = (1 + 2.0 ** -7 - 2.0 ** -23, 1 + 2.0 ** -7 - 2.0 ** -10)      # fp32 and fp16 values whose lower terms are as large as they get
+
+
+def long_values(g, shape, dtype):
+    """Values of every bit of their type, half of them such that what a term leaves is as large as it gets."""
+    a = np.where(g.random(shape) < 0.5, LONG[0 if dtype == FP32 else 1], g.uniform(1, 2, shape))
+    return torch.from_numpy(a * g.choice([-1.0, 1.0], shape) * np.exp2(g.integers(-3, 4, shape))).to(dtype).cuda()
+
+
+# One product of two fp32 values, the sum of products of their bf16 terms, the largest last: that addition is off by a
+# step of fp32 at most, 2 u, however the instruction rounds; the seven before it are 2^-6 of it and less, a step of
+# theirs together below u / 4; what no term holds is below 2^-30.
+ONE = 2.25 * ref.U
+
+
+def close(got, want, what):
+    over = np.abs(f64(got) - want) / np.abs(want)
+    assert over.max() <= ONE, "%s: off by %.3g u" % (what, over.max() / ref.U)
+
+
+@pytest.mark.parametrize("M", [3, 40, 300])
+@pytest.mark.parametrize("dtype,adtype", [(FP32, FP32), (FP16, FP32), (FP32, FP16)])
+def test_a_single_product_is_an_fp32_product(M, dtype, adtype):
+    """Forward: a row with one value, an adapter a row, one rank a column.  Backward: an adapter has one row."""
+    N, K, r = 96, 160, 16
+    g = np.random.default_rng(M)
+    at = torch.arange(M, device="cuda")
+    x = torch.zeros(M, K, dtype=dtype, device="cuda")
+    x[at, at % K] = long_values(g, M, dtype)
+    down, up = long_values(g, (M, r, K), adtype), long_values(g, (M, r, N), adtype)
+    one = torch.arange(N, device="cuda") % r == torch.arange(r, device="cuda")[:, None]
+    ids, scale = at.flip(0).int(), torch.ones(M, device="cuda")
+    zero, zero_t = (cim.mxfp4_quantize_nhwc(torch.zeros(*s, device="cuda")) for s in ((N, K), (K, N)))
+    ad = cim.Adapters(down, torch.where(one, up, 0).to(adtype), scale)
+    out, _, h = cim.mxfp4_linear_adapters_nhwc(x, zero, None, ad, ids, out_dtype=FP32, save=True)
+    n, m = f64(ids).astype(int), np.arange(M)
+    close(h, f64(x)[m, m % K][:, None] * f64(down)[n, :, m % K], "h")
+    close(out, f64(h)[:, np.arange(N) % r] * f64(up)[n][:, np.arange(N) % r, np.arange(N)], "out")
+    # (t is up's column 5 then, exactly; dx one rank a column)
+    dy = torch.zeros(M, N, dtype=dtype, device="cuda")
+    dy[:, 5] = 1
+    xs = long_values(g, (M, K), dtype)
+    cols = torch.arange(K, device="cuda") % r == torch.arange(r, device="cuda")[:, None]
+    ad = cim.Adapters(torch.where(cols, down, 0).to(adtype), up, scale)
+    dx, ddown, dup = cim.mxfp4_linear_adapters_bwd_nhwc(dy, xs, zero_t, ad, ids, h, dx_dtype=FP32)
+    t = f64(up)[n][:, :, 5]
+    close(dx, t[:, np.arange(K) % r] * f64(down)[n][:, np.arange(K) % r, np.arange(K)], "dx")
+    close(ddown[ids.long()], t[:, :, None] * f64(xs)[:, None, :], "ddown")
+    assert np.array_equal(f64(dup[ids.long()][:, :, 5]), f64(h))
+    dy = long_values(g, (M, N), dtype)
+    dup = cim.mxfp4_linear_adapters_bwd_nhwc(dy, xs, None, ad, ids, h)[2]
+    close(dup[ids.long()], f64(h)[:, :, None] * f64(dy)[:, None, :], "dup")
