@@ -237,3 +237,23 @@ def test_a_single_product_is_an_fp32_product(M, dtype, adtype):
     dy = long_values(g, (M, N), dtype)
     dup = cim.mxfp4_linear_adapters_bwd_nhwc(dy, xs, None, ad, ids, h)[2]
     close(dup[ids.long()], f64(h)[:, :, None] * f64(dy)[:, None, :], "dup")
+
+
+@pytest.mark.parametrize("M", [3, 40, 200, 300])
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+def test_every_row_of_a_bad_adapter_and_no_other(M, dtype):
+    """An infinity in down: not one finite output among its adapter's rows, and every other row as it was, whether
+    something is kept for the backward pass or not."""
+    x = rows(1, M, 96, dtype)
+    w, bias, ad = layer(2, 64, 96, 3, 16, dtype)
+    q = cim.mxfp4_quantize_nhwc(w)
+    ids = (torch.arange(M, device="cuda") % 4 - 1).int()
+    clean = cim.mxfp4_linear_adapters_nhwc(x, q, bias, ad, ids, out_dtype=FP32, save=True)
+    assert torch.equal(cim.mxfp4_linear_adapters_nhwc(x, q, bias, ad, ids, out_dtype=FP32), clean[0])
+    ad.down[1, 3, 5] = INF
+    got = cim.mxfp4_linear_adapters_nhwc(x, q, bias, ad, ids, out_dtype=FP32, save=True)
+    mine = ids == 1
+    assert mine.any() and not torch.isfinite(got[0][mine]).any() and not torch.isfinite(got[2][mine][:, 3]).any()
+    assert torch.equal(got[0][~mine], clean[0][~mine]) and torch.equal(got[2][~mine], clean[2][~mine])
+    alone = cim.mxfp4_linear_adapters_nhwc(x, q, bias, ad, ids, out_dtype=FP32)
+    assert torch.equal(alone[~mine], clean[0][~mine]) and not torch.isfinite(alone[mine]).any()
