@@ -257,3 +257,40 @@ def test_every_row_of_a_bad_adapter_and_no_other(M, dtype):
     assert torch.equal(got[0][~mine], clean[0][~mine]) and torch.equal(got[2][~mine], clean[2][~mine])
     alone = cim.mxfp4_linear_adapters_nhwc(x, q, bias, ad, ids, out_dtype=FP32)
     assert torch.equal(alone[~mine], clean[0][~mine]) and not torch.isfinite(alone[mine]).any()
+
+
+def test_infinities_between_replays():
+    """A captured training step finds infinities in some replays and none in the next: each equals the eager result, and
+    nothing is left of them."""
+    M, N, K, r = 700, 96, 160, 20
+    g = np.random.default_rng(3)
+    x, dy = whole(g, (M, K), FP32), whole(g, (M, N), BF16)
+    ad = cim.Adapters(whole(g, (3, r, K), BF16), whole(g, (3, r, N), BF16), torch.tensor([0.5, 1, -2], device="cuda"))
+    w = rows(2, N, K, FP32)
+    q, wt = cim.mxfp4_quantize_nhwc(w), cim.mxfp4_quantize_nhwc(w, transpose=True)
+    ids = torch.from_numpy(g.integers(-1, 3, M).astype(np.int32)).cuda()
+
+    def step():
+        out, k, h = cim.mxfp4_linear_adapters_nhwc(x, q, None, ad, ids, out_dtype=FP32, save=True)
+        return (out, h, *cim.mxfp4_linear_adapters_bwd_nhwc(dy, k, wt, ad, ids, h, dx_dtype=FP32))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    clean = [t.clone() for t in step()]
+    for k in range(5):
+        for t, v in ((x, INF), (dy, -INF), (ad.up, NAN)):
+            at = t.view(-1)[[7, t.numel() - 5]]
+            if k % 2:
+                t.view(-1)[[7, t.numel() - 5]] = v
+            graph.replay()
+            torch.cuda.synchronize()
+            got, eager = [o.clone() for o in out], step()
+            for a, b, c in zip(got, eager, clean):
+                assert np.array_equal(f64(a), f64(b), equal_nan=True)
+                assert k % 2 or torch.equal(a, c)
+            t.view(-1)[[7, t.numel() - 5]] = at
