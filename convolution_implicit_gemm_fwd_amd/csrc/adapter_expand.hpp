@@ -185,7 +185,9 @@ __device__ __forceinline__ bool adapter_up8(const typename T::raw (&w)[8], u32v4
 // be told from the product's own spread for 4 adapters in runs and 16 ranks (260
 // us), 50 us for 64 ranks; in that of 2011 x 4096 x 4096 14 us for 64 ranks; in
 // that of 61 x 8000 x 4096 with an adapter a row 6 us, the rows' parts of up
-// (8000 x 16 a row) being read from memory then.
+// (8000 x 16 a row) being read from memory then.  (Three steps in flight instead of
+// two in the 128 x 128 tiles, for which there are registers: 2011 x 4096 x 4096 with
+// 64 ranks, the whole call, 60.1 us against 59.5.)
 template <typename T, int FM, int FN, int KG>
 __device__ __forceinline__ unsigned adapter_expand(const MxAdapterArgs &a, int M, int N, int m0, int n0, int group,
                                                f32x16_t (&acc)[FM][FN])

@@ -97,9 +97,11 @@ struct Grad8x8<Kept> {
 // the second.
 //
 // 8192 rows of 4 adapters, 16 ranks, 4096 columns of dy (bf16) and 4096 of x (8
-// bits): 33.7 us for both gradients, 118 MB read (3.5 TB/s), 6.2 for the sums
-// over the chunks.  Each run of 32 rows waits for its order, then for its rows;
-// the waves of two other workgroups a SIMD are what covers that.
+// bits): 32.3 us for both gradients, 118 MB read (3.7 TB/s), 7.1 for the sums
+// over the chunks; 32 ranks 48.7 and 9, 64 ranks 109 and 15.  Each run of 32 rows
+// waits for its order, then for its rows; the waves of other workgroups are what
+// covers that, three a SIMD with 16- or 8-bit rows and 16 ranks, one with fp32 rows
+// or 32 ranks, none above.
 constexpr int kAdGradCols = 128, kAdGradWaves = 4;
 
 template <typename V, int RT>
@@ -236,7 +238,7 @@ __device__ __forceinline__ float ad_grad_value(const AdGradArgs &a, int g, int i
 // The sums of the adapters whose rows lie in several chunks, in order, and
 // zeros for those without rows.  An infinity of one operand times a lower term of
 // the other, which may be 0, makes NaN: where some sum is NaN, those are taken
-// once more.  (Here, where registers are free: in ad_grad it took a wave a SIMD.)
+// once more.  (Here, where registers are free: in ad_grad they cost a wave a SIMD.)
 template <typename DY, typename X>
 __global__ __launch_bounds__(256) void ad_grad_sum(AdGradArgs up, AdGradArgs down)
 {
@@ -270,6 +272,13 @@ __global__ __launch_bounds__(256) void ad_grad_sum(AdGradArgs up, AdGradArgs dow
         }
 }
 
+// 16 RT ranks a workgroup, which reads v for all of them: the largest RT that the
+// ranks fill.  The registers that more ranks take cost waves, four a SIMD at RT 1,
+// two at 2 and one at 4 (fp32 two, two, one), and that is more than they save: 8192
+// rows of 4 adapters with x kept, 4096 + 4096 columns, the whole call without dx,
+// with RT 1, 2 and 4: 16 ranks 72, 85 and 142 us, 32 ranks 88, 93 and 146, 64 ranks
+// 129, 127 and 165, 128 ranks 222, 208 and 250; 2048 rows of 8, 64 ranks: 65, 75 and
+// 103.
 inline int grad_ranks(int r) { return r <= 16 ? 1 : r <= 32 ? 2 : 4; }
 
 // The launches for one type of dy.

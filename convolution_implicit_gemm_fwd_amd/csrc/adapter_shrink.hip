@@ -108,10 +108,12 @@ __global__ __launch_bounds__(kAdFewWaves * 64) void ad_shrink_few(AdShrinkArgs a
 // in cache, against 40.  Two steps in flight overflow the registers: 2011 x 4096 with 64
 // ranks 28 us against 19.)
 //
-// 8192 x 8192 and 16 ranks, x from memory: 51 us, 134 MB read and 37 written, 3.4
-// TB/s (quantising alone 42 us there); 8192 x 4096 30 us.  Two workgroups a CU is
-// what the registers allow, and the steps wait for their loads: four waves a
-// SIMD spill and take twice as long.
+// 8192 x 8192 and 16 ranks, x from memory: 51 us, 144 MB read and 37 written, 3.5
+// TB/s (quantising alone 42 us there); 8192 x 4096 30 us.  The steps wait for their
+// loads, and few of them are in flight: of 213 to 256 registers a lane (by the
+// types and RT) a SIMD holds two waves, so a CU one workgroup of eight.  fp32 rows
+// spill 84 to 284 bytes a lane, fp16 or bf16 rows with 64 ranks of another type up
+// to 152.  (Held to four waves a SIMD all spill and take twice as long.)
 constexpr int kAdWaves = 8;
 
 // 16 rows of 128 columns of a wave, in LDS.
@@ -555,8 +557,13 @@ void adapter_sort(const int *ids, int M, int G, int *order, int *key, int *start
 
 // A row a workgroup for up to 256 rows, unsorted; 16 sorted rows a workgroup
 // above.  With 4096 x 4096 and 16 ranks, sorting and the product included: 64
-// rows of 4 adapters 11 us against 21 sorted, 256 rows of 8 adapters 18 against
-// 24 and of 32 25 against 26, 512 rows of 16 adapters 34 against 28.
+// rows of 4 adapters 12 us against 22 sorted, 256 rows of 8 adapters 18.5 against
+// 24.5 and of 32 24.4 against 25.6, 512 rows of 16 adapters 29.5 against 29.  Each
+// row reads its adapter for itself, so more ranks move the bound down, which the
+// rule does not follow: with 64 ranks 64 rows of 4 adapters 16 against 23 and of
+// 64 33 against 36, 128 rows of 8 26 against 25, 256 rows of 8 44 against 29 and
+// of one 29 against 22; with 128 ranks 64 rows of 4 23 against 25, 256 of 8 76
+// against 36.
 AdPlan adapter_plan(int M, int G)
 {
     AdPlan p;

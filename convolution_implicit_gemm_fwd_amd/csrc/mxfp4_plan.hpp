@@ -54,6 +54,13 @@ inline auto tiles_of(int M, int N)
 //     With fewer tiles the larger ones are one round, and either may win:
 //     3500x3500 (784) x1000 16.7 against 19.2 and x2000 26.1 against 26.8,
 //     3328x3328 (676) 14.3 against 14.4 and 23.7 against 22.0.
+// With adapters beside the product, which cost the smaller tiles waves, the same
+// bounds hold (16 ranks, the whole call): 64x4096x4096 12.1 in 32 x 32 against 13.2
+// in 64 x 32; 256 rows 18.6 in 64 x 64 against 21.9 in 128 x 64 and 23.2 in 64 x 32;
+// 512 rows 28.9 in 128 x 64 against 30.0 and 32.7; 1024 rows 34.9 in 128 x 128
+// against 41.0 and 47.4; 4096 rows 65.2 in 256 x 256 against 72.7; short ones within
+// 4 %: 8192x8192x256 73.2 against 72.1 in 256 x 256, x512 82.0 against 80.0 in the
+// longer 128 x 128.
 enum Shape { k256, k128, k128Short, k128x64, k64, k64x32, k32 };
 
 template <typename C>

@@ -459,7 +459,9 @@ int layer_norm_bwd_workspace(long long rows, int cols, size_t *bytes);
  * is u = 2^(s - 127), s the smallest whole number of at least 1 for which 127 u
  * reaches the block's largest magnitude; a value is stored as value / u rounded
  * to the nearest whole number, ties to even, so it is off by at most u / 2 and
- * none saturates.  The values code * u are exact in bf16.  A block that holds
+ * none saturates.  The values code * u are exact in bf16.  (The published MXINT8
+ * format reads the same codes as multiples of 1/64 of its scale: its scale byte
+ * for these values would be s + 6.)  A block that holds
  * an infinity or a NaN gets the byte 255 and stands for NaN throughout.  Layout,
  * with kp = cols rounded up to 32:
  *
@@ -573,7 +575,8 @@ int mxfp4_linear_bwd_mxint8(const void *dy, long long lddy, int dy_dtype, const 
  *
  * where the adapter's part is taken from x itself, not from Q(x), and added
  * before the one rounding to out_dtype.  A row depends on its own adapter only:
- * an infinity or a NaN in another one or in another row does not reach it.
+ * an infinity or a NaN in another one or in another row does not reach it, and
+ * its own make what the formulas make of them, whatever the number of rows.
  * Products and sums are fp32; of an fp32 value the bits below 2^-133 may be lost.
  *
  *   x, w_codes, w_scales, bias, out   as for mxfp4_linear_fwd, x dense
